@@ -162,6 +162,11 @@ void prof_free() {
 
 }  // namespace
 
+// error texts for the entry points of the other host file (attn_api.hip)
+void sffn_err_clear() { g_err[0] = 0; }
+int sffn_err_set(int status, const char* text) { return fail(status, "%s", text); }
+int sffn_err_hip(hipError_t e, const char* what) { return hip_fail(e, what); }
+
 bool sffn_prof_events(int kid, hipEvent_t* start, hipEvent_t* stop) {
   if (g_prof.kernel != kid || g_prof.used >= g_prof.max) return false;
   *start = g_prof.ev[2 * g_prof.used];

@@ -1,0 +1,208 @@
+// Shared declarations of the paged K/V cache, the attention over it and the residual norm (gfx950, wave64).
+#pragma once
+#include "common.h"
+
+namespace sffn {
+
+enum { T_F32 = 0, T_F16 = 1, T_BF16 = 2, T_I8 = 3, T_E4M3 = 4 };   // sffn_type
+
+// Rows whose scale would be below this are stored as zeros with scale 0, so that the attention can work with the
+// scales' logarithms and reciprocals in normal fp32 numbers.
+constexpr float KV_MIN_SCALE = 7.888609052210118e-31f;   // 2^-100
+
+// A cache as the kernels take it: pages [n_pages, hkv, 1 << psh, d], scales [n_pages, hkv, 1 << psh].
+struct Kv {
+  char* k;
+  char* v;
+  float* ks;
+  float* vs;
+  int n_pages, psh, hkv, d;
+};
+// The sequences of a call (cu [S + 1], len [S], table rows of `cols` entries, ldt apart).
+struct Seqs {
+  const int* cu;
+  const int* len;
+  const int* table;
+  int S, T, cols, ldt;
+};
+// One sequence, clamped so that nothing read from device memory can lead an access out of the caller's tensors:
+// its first row of the token tensors, its new tokens, its cached tokens (at most what its table row can hold).
+struct Seq {
+  int q0, n, len;
+};
+__device__ __forceinline__ Seq load_seq(const Seqs& q, int s, int psh) {
+  Seq r;
+  const int a = q.cu[s], b = q.cu[s + 1], l = q.len[s];
+  r.q0 = min(max(a, 0), q.T);
+  r.n = min(max(b, r.q0), q.T) - r.q0;
+  r.len = min(max(l, 0), q.cols << psh);
+  return r;
+}
+
+// The sequence of token t: how many of cu[1 .. S] are at most t, counted over a group of G lanes (G-ary search, the
+// same t in every lane of a group). S: t lies behind the last sequence.
+template <int G>
+__device__ __forceinline__ int find_seq(const int* __restrict__ cu, int S, int t) {
+  int lo = 0, hi = S;                          // the answer is in lo .. hi
+  const int lane = threadIdx.x & (G - 1);
+  while (__any(lo < hi)) {
+    const int step = (hi - lo + G) / G;        // lane i looks at entry lo + i * step (< hi)
+    const int e = lo + lane * step;
+    const bool in = lo < hi && e < hi;
+    const bool le = in && cu[e + 1] <= t;
+    const int c = (int)group_sum<G>(le ? 1.f : 0.f);
+    if (lo < hi) {
+      const int nlo = c ? lo + (c - 1) * step + 1 : lo;
+      const int nhi = c ? min(hi, lo + c * step) : lo;
+      lo = nlo;
+      hi = max(nhi, nlo);
+    }
+  }
+  return lo;
+}
+
+// The key units (1 << ush keys each) that a tile of rows at positions p_lo .. p_hi reads, as one list: first the
+// units of the always-visible first tokens that lie before the window, then those of the window itself.
+struct Units {
+  int sink, w0, tot;        // units before the window; first window unit; all
+  __device__ __forceinline__ int key0(int u, int ush) const { return (u < sink ? u : u - sink + w0) << ush; }
+};
+__device__ __forceinline__ Units key_units(int p_lo, int p_hi, int len, int window, int sinks, int ush) {
+  const int end = min(len, p_hi + 1);          // keys at or after it are visible to no row
+  Units u{0, 0, 0};
+  if (end <= 0) return u;
+  const int lo = window > 0 ? max(0, p_lo - window + 1) : 0;
+  u.w0 = lo >> ush;
+  u.sink = min((min(sinks, lo) + (1 << ush) - 1) >> ush, u.w0);
+  u.tot = u.sink + ((end + (1 << ush) - 1) >> ush) - u.w0;
+  return u;
+}
+// Units of each share when a list of `tot` is split into at most ns shares of at least `least` units, whole
+// multiples of `step`.
+__device__ __forceinline__ int share_units(int tot, int ns, int least, int step) {
+  const int per = max(least, (tot + ns - 1) / ns);
+  return (per + step - 1) / step * step;
+}
+
+// Arguments of an attention call. Rows of one K/V head: r = i * G + g for new token i and query head hk * G + g.
+struct AttnArgs {
+  const char* q;
+  char* out;
+  float* lse;
+  Kv kv;
+  Seqs sq;
+  int hq, G, max_q, window, sinks, ns;
+  long ldq, ldo;            // elements between tokens
+  float c;                  // softmax scale * log2(e)
+  float* po;                // partial outputs [T * hq][ns][d], used when ns > 1
+  float2* pml;              // their maxima (log2 domain) and sums [T * hq][ns]
+};
+
+constexpr int FEW_USH = 5, FEW_LEAST = 8;       // few-row kernel: units of 32 keys, at least 8 of them a share
+constexpr int MANY_USH = 6, MANY_LEAST = 4, MANY_ROWS = 128;
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef __fp16 fp16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+
+// 16-bit operands are kept as raw bits; BF says which of the two types they are.
+template <bool BF>
+__device__ __forceinline__ f32x4 mfma16(const uint4& a, const uint4& b, f32x4 c) {
+  if constexpr (BF) return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
+  else return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
+}
+template <bool BF>
+__device__ __forceinline__ f32x16 mfma32(const uint4& a, const uint4& b, f32x16 c) {
+  if constexpr (BF) return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
+  else return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
+}
+// two fp32 values as 16 bits each, rounded to nearest even
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (BF) return __builtin_bit_cast(uint32_t, bf2{(__bf16)a, (__bf16)b});
+  else return __builtin_bit_cast(uint32_t, half2v{(_Float16)a, (_Float16)b});
+}
+template <bool BF>
+__device__ __forceinline__ float lo16(uint32_t u) {
+  if constexpr (BF) return __uint_as_float(u << 16);
+  else return (float)__builtin_bit_cast(half2v, u).x;
+}
+template <bool BF>
+__device__ __forceinline__ float hi16(uint32_t u) {
+  if constexpr (BF) return __uint_as_float(u & 0xFFFF0000u);
+  else return (float)__builtin_bit_cast(half2v, u).y;
+}
+// a bit pattern that is nonzero iff one of the two 16-bit values is infinite or NaN (all exponent bits set: adding
+// the lowest exponent bit carries into the sign's place exactly then)
+template <bool BF>
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t u) {
+  constexpr uint32_t E = BF ? 0x7F807F80u : 0x7C007C00u, L = BF ? 0x00800080u : 0x04000400u;
+  return ((u & E) + L) & 0x80008000u;
+}
+
+// Four 8-bit codes as four fp16 values (exact). int8: the code + 128 in the low byte of 0x64xx is 1024 + code + 128;
+// one packed subtraction leaves the code.
+template <bool E4M3>
+__device__ __forceinline__ uint2 codes4(uint32_t u) {
+  if constexpr (E4M3) {
+    const half2v a = __builtin_bit_cast(half2v, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)u, 1.0f, false));
+    const half2v b = __builtin_bit_cast(half2v, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)u, 1.0f, true));
+    return make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+  } else {
+    u ^= 0x80808080u;
+    const half2v k = {(_Float16)-1152.f, (_Float16)-1152.f};
+    const half2v a = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(0x64646464u, u, 0x07010700u)) + k;
+    const half2v b = __builtin_bit_cast(half2v, __builtin_amdgcn_perm(0x64646464u, u, 0x07030702u)) + k;
+    return make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+  }
+}
+
+// What the softmax takes from a key's scales. With 8-bit V rows the weights p_j s_j that multiply the codes must not
+// leave fp16's range whatever the scales are, so the running maximum is taken over x_j + log2 s_j (x: scores in
+// log2 units): P_j = 2^(x_j + log2 s_j - m) <= 1 multiplies the codes, and the softmax's own sum is that of P_j / s_j.
+// A row with scale 0 has codes 0, so any scale serves; one with scale NaN counts in the sum as if it had scale 0, and
+// its weight in the second product is NaN for the rows that see it.
+struct VScale {
+  float lg, inv;
+};
+__device__ __forceinline__ VScale v_scale(float s) {
+  const float t = s >= KV_MIN_SCALE ? s : KV_MIN_SCALE;
+  return {__builtin_amdgcn_logf(t), __builtin_amdgcn_rcpf(t)};
+}
+// Factor of what was accumulated under the maximum m when the maximum becomes `to` (finite): never 0 where something
+// was, so that an infinity or NaN stays one however small its weight has become.
+__device__ __forceinline__ float fade(float m, float to) {
+  return m == -INFINITY ? 0.f : fmaxf(__builtin_amdgcn_exp2f(m - to), 1.1754944e-38f);
+}
+
+// natural logarithm of L * 2^M (-infinity for a row without visible keys)
+__device__ __forceinline__ float log_sum(float M, float L) {
+  return L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * 0.6931471805599453f;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+}  // namespace sffn
+
+// error text of the calling thread (api.hip)
+void sffn_err_clear();
+int sffn_err_set(int status, const char* text);
+int sffn_err_hip(hipError_t e, const char* what);
+
+// Launches. Types are sffn_type values; host code has checked every argument.
+hipError_t sffn_launch_add_rmsnorm(const void* x, int xt, const void* res, int rt, const float* w, double eps, int T,
+                                   int D, long ldx, long ldr, void* y, int yt, float* y_scale, void* res_out, long ldy,
+                                   long ldro, hipStream_t st);
+hipError_t sffn_launch_kv_write(const sffn::Kv& kv, int kvt, const sffn::Seqs& sq, const void* k, const void* v, int xt,
+                                long ldk, long ldv, hipStream_t st);
+hipError_t sffn_launch_kv_read(const sffn::Kv& kv, int kvt, const sffn::Seqs& sq, void* k, void* v, int xt, long ldk,
+                               long ldv, hipStream_t st);
+// rows of one K/V head per sequence that the few-row kernel takes (0: none)
+int sffn_attn_few_rows(int d);
+hipError_t sffn_launch_attn_few(const sffn::AttnArgs& a, int qt, int kvt, hipStream_t st);
+hipError_t sffn_launch_attn_many(const sffn::AttnArgs& a, int qt, int kvt, hipStream_t st);
+hipError_t sffn_launch_attn_join(const sffn::AttnArgs& a, int qt, bool few, hipStream_t st);

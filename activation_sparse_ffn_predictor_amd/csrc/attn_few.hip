@@ -1,0 +1,380 @@
+// Attention over the paged cache for few rows a K/V head (single tokens, a few drafted ones).
+//
+// S^T = K Q^T and O^T = V^T P^T on the matrix cores (16x16x32): a lane's column is one row of Q in both products, so
+// a row's maximum and sum live in the lanes that hold its scores, and the scores of a lane are, as they are, its part
+// of the next product's operand (the order of the keys within a product is free, V is read in the same one).
+#include "attn.h"
+
+using namespace sffn;
+
+namespace {
+
+constexpr int NT = 256, NW = 4;
+
+// A 16-byte slot of V's tile in LDS: key's 16-byte chunk c goes to slot c ^ few_swz(key), so that the 16 (32) rows
+// that a transposing read touches at one column spread over the banks.
+template <int RB>   // bytes of a tile row
+__device__ __forceinline__ int few_swz(int key, bool codes) {
+  if (codes) return RB >= 256 ? key & 15 : RB == 128 ? (key >> 1) & 7 : (key >> 2) & 3;
+  return RB >= 256 ? (key & 7) << 1 : ((key >> 1) & 3) << 1;
+}
+
+// KVM 0: cache of the query's 16-bit type, 1: int8, 2: e4m3 (both computed in fp16: codes are exact there, and bf16
+// queries are scaled by one power of two into fp16's range). DP: head size padded to 64, 128 or 256. QB: 16-row tiles.
+template <bool BF, int KVM, int DP, int QB>
+__global__ __launch_bounds__(NT) void k_attn_few(AttnArgs a) {
+  constexpr bool C8 = KVM != 0, CB = BF && !C8;
+  constexpr int EB = C8 ? 1 : 2, RB = DP * EB, KS = DP / 32, DB = DP / 16, CPR = RB / 16;   // chunks a row
+  constexpr int KL = RB / 64;                      // 16-byte K loads of a lane per 16 keys
+  constexpr int RPI = 64 / CPR, VL = 16 / RPI;     // V rows a load instruction covers; V loads per 16 keys
+  constexpr int VT = 32 * RB, OS = DP + 4;         // V tile of a wave; row stride of the merge (floats)
+  constexpr int LDS = NW * VT > NW * QB * 16 * OS * 4 ? NW * VT : NW * QB * 16 * OS * 4;
+  __shared__ __align__(16) char lds[LDS];
+  __shared__ float mlw[NW][QB * 16][2];
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, g4 = l >> 4, ql = l & 15;
+  const int hk = blockIdx.y, s = blockIdx.z, d = a.kv.d, G = a.G;
+  const Seq sq = load_seq(a.sq, s, a.kv.psh);
+  const int n = min(sq.n, a.max_q), rows = n * G;
+  if (rows == 0) return;
+  const int p0 = sq.len - sq.n, p1 = p0 + n - 1;   // positions of the first and last new token
+  const Units un = key_units(p0, p1, sq.len, a.window, a.sinks, FEW_USH);
+  const int per = share_units(un.tot, a.ns, FEW_LEAST, NW), used = max(1, (un.tot + per - 1) / per);
+  const int split = blockIdx.x;
+  if (split >= used) return;
+  const int u1 = min(un.tot, (split + 1) * per);
+
+  // queries: 8 consecutive elements of row ql per product step
+  uint4 qf[QB][KS];
+  int pos[QB];
+  float c = a.c;
+#pragma unroll
+  for (int qb = 0; qb < QB; ++qb) {
+    const int r = qb * 16 + ql, i = r / G, g = r - i * G;
+    pos[qb] = r < rows ? p0 + i : p1;              // rows past the last compute along and are dropped
+    const char* qp = a.q + ((long)(sq.q0 + i) * a.ldq + (long)(hk * G + g) * d) * 2;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int ch = C8 ? ((ks >> 1) * 4 + g4) * 2 + (ks & 1) : ks * 4 + g4;
+      qf[qb][ks] = r < rows && ch * 8 < d ? *reinterpret_cast<const uint4*>(qp + ch * 16) : make_uint4(0, 0, 0, 0);
+    }
+  }
+  if constexpr (C8 && BF) {
+    // bf16 queries into fp16: times one power of two that takes the largest to 2^15 (exact but for elements below
+    // 2^-29 of it, which lose bits under 2^-40 of it)
+    float big = 0.f;
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb)
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const uint32_t u[4] = {qf[qb][ks].x, qf[qb][ks].y, qf[qb][ks].z, qf[qb][ks].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) big = fmaxf(big, fmaxf(fabsf(lo16<true>(u[k])), fabsf(hi16<true>(u[k]))));
+      }
+    big = wave_max(big);
+    const int e = big > 0.f && big < 3.4e38f ? 14 - ((int)((__float_as_uint(big) >> 23) & 255) - 127) : 0;
+    const int e1 = min(max(e, -126), 126);
+    const float up = __uint_as_float((uint32_t)(e1 + 127) << 23);
+    c = c * __uint_as_float((uint32_t)(127 - e1) << 23);
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb)
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const uint4 t = qf[qb][ks];
+        qf[qb][ks] = make_uint4(pack2<false>(lo16<true>(t.x) * up, hi16<true>(t.x) * up),
+                                pack2<false>(lo16<true>(t.y) * up, hi16<true>(t.y) * up),
+                                pack2<false>(lo16<true>(t.z) * up, hi16<true>(t.z) * up),
+                                pack2<false>(lo16<true>(t.w) * up, hi16<true>(t.w) * up));
+      }
+  }
+
+  float m[QB], ls[QB];
+  f32x4 o[QB][DB];
+#pragma unroll
+  for (int qb = 0; qb < QB; ++qb) {
+    m[qb] = -INFINITY;
+    ls[qb] = 0.f;
+#pragma unroll
+    for (int db = 0; db < DB; ++db) o[qb][db] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  char* vt = lds + w * VT;
+  const int* trow = a.sq.table + (long)s * a.sq.ldt;
+  const uint32_t dB = (uint32_t)d * EB;
+
+  for (int u = split * per + w; u < u1; u += NW) {
+    const int t0 = un.key0(u, FEW_USH);
+    uint4 kr[2][KL], vr[2][VL];
+    float4 ksc[2], vsc[2];
+    int have[2];                                   // keys of each 16 that exist
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      // 16 keys share a page; what does not exist (behind the sequence, a bad page) reads as zeros
+      const int t = t0 + kb * 16, pg = t >> a.kv.psh;
+      const int pid = __builtin_amdgcn_readfirstlane(trow[min(pg, a.sq.cols - 1)]);
+      have[kb] = (unsigned)pid < (unsigned)a.kv.n_pages ? min(16, max(0, sq.len - t)) : 0;
+      const long r = (((long)(have[kb] ? pid : 0) * a.kv.hkv + hk) << a.kv.psh) + (t & ((1 << a.kv.psh) - 1));
+      const Buf bk(a.kv.k + r * dB, have[kb] * dB), bv(a.kv.v + r * dB, have[kb] * dB);
+#pragma unroll
+      for (int i = 0; i < KL; ++i) {
+        const uint32_t ch = i * 4 + g4;
+        kr[kb][i] = bk.ld16(boff(ch * 16 < dB, ql * dB + ch * 16));
+      }
+#pragma unroll
+      for (int i = 0; i < VL; ++i) {
+        const uint32_t key = i * RPI + l / CPR, ch = l % CPR;
+        vr[kb][i] = bv.ld16(boff(ch * 16 < dB, key * dB + ch * 16));
+      }
+      if constexpr (C8) {
+        const Buf sk(a.kv.ks + r, have[kb] * 4), sv(a.kv.vs + r, have[kb] * 4);
+        ksc[kb] = sk.ldf4(g4 * 16);
+        vsc[kb] = sv.ldf4(g4 * 16);
+      }
+    }
+    // scores
+    f32x4 sc[QB][2];
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) sc[qb][kb] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < KL; ++i) {
+        if constexpr (C8) {
+          const uint4 t = kr[kb][i];
+          const uint2 x0 = codes4<KVM == 2>(t.x), x1 = codes4<KVM == 2>(t.y), x2 = codes4<KVM == 2>(t.z),
+                      x3 = codes4<KVM == 2>(t.w);
+          const uint4 ka = make_uint4(x0.x, x0.y, x1.x, x1.y), kc = make_uint4(x2.x, x2.y, x3.x, x3.y);
+#pragma unroll
+          for (int qb = 0; qb < QB; ++qb) {
+            sc[qb][kb] = mfma16<false>(ka, qf[qb][2 * i], sc[qb][kb]);
+            sc[qb][kb] = mfma16<false>(kc, qf[qb][2 * i + 1], sc[qb][kb]);
+          }
+        } else {
+#pragma unroll
+          for (int qb = 0; qb < QB; ++qb) sc[qb][kb] = mfma16<CB>(kr[kb][i], qf[qb][i], sc[qb][kb]);
+        }
+      }
+    // every key of the unit visible to every row?
+    const bool full = have[0] + have[1] == 32 && t0 + 31 <= p0 &&
+                      (a.window <= 0 || t0 > p1 - a.window || t0 + 32 <= a.sinks);
+    uint4 pf[QB];
+    uint32_t vis[QB];                              // bit kb * 4 + i: key kb * 16 + g4 * 4 + i is visible to row ql
+    float lg[2][4], inv[2][4], kf[2][4];
+    uint32_t vnan = 0;                             // as vis: the key's V row has no scale
+    if constexpr (C8) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        const float ka[4] = {ksc[kb].x, ksc[kb].y, ksc[kb].z, ksc[kb].w};
+        const float va[4] = {vsc[kb].x, vsc[kb].y, vsc[kb].z, vsc[kb].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const VScale v = v_scale(va[i]);
+          kf[kb][i] = ka[i] * c;
+          lg[kb][i] = v.lg;
+          inv[kb][i] = v.inv;
+          vnan |= va[i] != va[i] ? 1u << (kb * 4 + i) : 0u;
+        }
+      }
+    }
+    const bool any_vnan = C8 && __any(vnan != 0);
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb) {
+      float x[2][4], top = -INFINITY;
+      vis[qb] = 255u;
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[kb][i] = C8 ? fmaf(sc[qb][kb][i], kf[kb][i], lg[kb][i]) : sc[qb][kb][i] * c;
+      if (!full) {
+        vis[qb] = 0;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int kk = g4 * 4 + i, j = t0 + kb * 16 + kk;
+            const bool see = kk < have[kb] && j <= pos[qb] && (a.window <= 0 || j > pos[qb] - a.window || j < a.sinks);
+            x[kb][i] = see ? x[kb][i] : -INFINITY;
+            vis[qb] |= see ? 1u << (kb * 4 + i) : 0u;
+          }
+      }
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, x[kb][i]);
+      top = fmaxf(top, __shfl_xor(top, 16, WAVE));
+      top = fmaxf(top, __shfl_xor(top, 32, WAVE));
+      const float mn = fmaxf(m[qb], top), ms = mn == -INFINITY ? 0.f : mn;
+      const float al = fade(m[qb], ms);
+      float p[2][4], sum = 0.f;
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[kb][i] = exp2_fast(x[kb][i] - ms);
+          sum = C8 ? fmaf(p[kb][i], inv[kb][i], sum) : sum + p[kb][i];
+        }
+      ls[qb] = ls[qb] * al + sum;
+      if (__any(mn > m[qb])) {
+#pragma unroll
+        for (int db = 0; db < DB; ++db) o[qb][db] *= al;
+      }
+      m[qb] = mn;
+      if (C8 && any_vnan) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if ((vnan & vis[qb]) >> e & 1) p[e >> 2][e & 3] = __uint_as_float(0x7FC00000u);
+      }
+      // weights of one rounding (half a step of the type each) enter the second product
+      pf[qb] = make_uint4(pack2<CB>(p[0][0], p[0][1]), pack2<CB>(p[0][2], p[0][3]), pack2<CB>(p[1][0], p[1][1]),
+                          pack2<CB>(p[1][2], p[1][3]));
+    }
+    // V through the wave's own LDS tile (the LDS pipe keeps a wave's accesses in order)
+    bool odd = false;                              // an infinity or NaN in a unit that some row sees only in part
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < VL; ++i) {
+        const int key = kb * 16 + i * RPI + l / CPR, ch = l % CPR;
+        *reinterpret_cast<uint4*>(vt + key * RB + ((ch ^ few_swz<RB>(key, C8)) << 4)) = vr[kb][i];
+        if (!C8 && !full) {
+          const uint4 t = vr[kb][i];
+          odd |= (nonfinite2<CB>(t.x) | nonfinite2<CB>(t.y) | nonfinite2<CB>(t.z) | nonfinite2<CB>(t.w)) != 0;
+        }
+      }
+    asm volatile("" ::: "memory");
+    const bool slow = !C8 && !full && __any(odd);
+#pragma unroll
+    for (int db = 0; db < DB; ++db) {
+      uint4 vf;
+      if constexpr (C8) {
+        const int j = ql >> 1, key = (j < 4 ? 0 : 12) + g4 * 4 + j;   // rows 0-3: keys g4*4.., 4-7: 16 + g4*4..
+        const i32x2 t = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)(
+            vt + key * RB + ((db ^ few_swz<RB>(key, true)) << 4) + (ql & 1) * 8));
+        const uint2 x0 = codes4<KVM == 2>((uint32_t)t.x), x1 = codes4<KVM == 2>((uint32_t)t.y);
+        vf = make_uint4(x0.x, x0.y, x1.x, x1.y);
+      } else {
+        const int key = g4 * 4 + (ql >> 2), ch = db * 2 + ((ql & 3) >> 1);
+        const int at = ((ch ^ few_swz<RB>(key, false)) << 4) + (ql & 1) * 8;   // keys 16 apart: the same slot
+        const fp16x4 t0v = __builtin_amdgcn_ds_read_tr16_b64_v4f16(
+            (__attribute__((address_space(3))) fp16x4*)(vt + key * RB + at));
+        const fp16x4 t1v = __builtin_amdgcn_ds_read_tr16_b64_v4f16(
+            (__attribute__((address_space(3))) fp16x4*)(vt + (key + 16) * RB + at));
+        const uint2 y0 = __builtin_bit_cast(uint2, t0v), y1 = __builtin_bit_cast(uint2, t1v);
+        vf = make_uint4(y0.x, y0.y, y1.x, y1.y);
+      }
+      if (!slow) {
+#pragma unroll
+        for (int qb = 0; qb < QB; ++qb) o[qb][db] = mfma16<CB>(vf, pf[qb], o[qb][db]);
+      } else {
+        // finite values as usual; infinities and NaN only where a row sees them: counted by products of 0 / 1
+        // operands, one for each kind, and added to the rows whose count is not 0
+        uint32_t fin[4], ind[3][4];
+        const uint32_t raw[4] = {vf.x, vf.y, vf.z, vf.w};
+        constexpr uint32_t ONE = CB ? 0x3F80u : 0x3C00u, EXP = CB ? 0x7F80u : 0x7C00u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          fin[k] = ind[0][k] = ind[1][k] = ind[2][k] = 0;
+#pragma unroll
+          for (int sh = 0; sh < 32; sh += 16) {
+            const uint32_t v = (raw[k] >> sh) & 0xFFFFu;
+            fin[k] |= ((v & EXP) != EXP ? v : 0u) << sh;
+            ind[0][k] |= (v == EXP ? ONE : 0u) << sh;
+            ind[1][k] |= (v == (EXP | 0x8000u) ? ONE : 0u) << sh;
+            ind[2][k] |= ((v & 0x7FFFu) > EXP ? ONE : 0u) << sh;
+          }
+        }
+#pragma unroll
+        for (int qb = 0; qb < QB; ++qb) {
+          uint32_t one[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            one[k] = ((vis[qb] >> (2 * k)) & 1 ? ONE : 0u) | ((vis[qb] >> (2 * k + 1)) & 1 ? ONE << 16 : 0u);
+          o[qb][db] = mfma16<CB>(make_uint4(fin[0], fin[1], fin[2], fin[3]), pf[qb], o[qb][db]);
+#pragma unroll
+          for (int kind = 0; kind < 3; ++kind) {
+            const f32x4 cnt = mfma16<CB>(make_uint4(ind[kind][0], ind[kind][1], ind[kind][2], ind[kind][3]),
+                                         make_uint4(one[0], one[1], one[2], one[3]), f32x4{0.f, 0.f, 0.f, 0.f});
+            const float add = __uint_as_float(kind == 0 ? 0x7F800000u : kind == 1 ? 0xFF800000u : 0x7FC00000u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[qb][db][i] += cnt[i] > 0.f ? add : 0.f;
+          }
+        }
+      }
+    }
+    asm volatile("" ::: "memory");
+  }
+
+  // the waves' parts joined in wave order
+  __syncthreads();
+  float* om = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int qb = 0; qb < QB; ++qb) {
+    float t = ls[qb];
+    t += __shfl_xor(t, 16, WAVE);
+    t += __shfl_xor(t, 32, WAVE);
+    if (g4 == 0) {
+      mlw[w][qb * 16 + ql][0] = m[qb];
+      mlw[w][qb * 16 + ql][1] = t;
+    }
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+      *reinterpret_cast<f32x4*>(om + ((w * QB + qb) * 16 + ql) * OS + db * 16 + g4 * 4) = o[qb][db];
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < rows * (DP / 8); e += NT) {
+    const int r = e / (DP / 8), d0 = (e % (DP / 8)) * 8, i = r / G, g = r - i * G;
+    if (d0 >= d) continue;
+    float M = -INFINITY, L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < NW; ++k) M = fmaxf(M, mlw[k][r][0]);
+    const float ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      const float f = fade(mlw[k][r][0], ms);
+      L = fmaf(mlw[k][r][1], f, L);
+      const float* src = om + ((k * QB) * 16 + r) * OS + d0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] = fmaf(src[j], f, acc[j]);
+    }
+    const long row = (long)(sq.q0 + i) * a.hq + hk * G + g;
+    if (used == 1) {
+      const float iv = L == 0.f ? 0.f : 1.f / L;   // no key was visible: 0
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] *= iv;
+      *reinterpret_cast<uint4*>(a.out + ((long)(sq.q0 + i) * a.ldo + (long)(hk * G + g) * d + d0) * 2) =
+          make_uint4(pack2<BF>(acc[0], acc[1]), pack2<BF>(acc[2], acc[3]), pack2<BF>(acc[4], acc[5]),
+                     pack2<BF>(acc[6], acc[7]));
+      if (a.lse && d0 == 0) a.lse[row] = log_sum(M, L);
+    } else {
+      float* po = a.po + (row * a.ns + split) * d + d0;
+      reinterpret_cast<float4*>(po)[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      reinterpret_cast<float4*>(po)[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      if (d0 == 0) a.pml[row * a.ns + split] = make_float2(M, L);
+    }
+  }
+}
+
+}  // namespace
+
+int sffn_attn_few_rows(int d) { return d <= 128 ? 32 : 16; }
+
+hipError_t sffn_launch_attn_few(const AttnArgs& a, int qt, int kvt, hipStream_t st) {
+  const dim3 grid(a.ns, a.kv.hkv, a.sq.S);
+  const bool bf = qt == T_BF16;
+  const int kvm = kvt == T_I8 ? 1 : kvt == T_E4M3 ? 2 : 0;
+  const bool two = a.max_q * a.G > 16;
+#define GO(BF, KVM, DP, QB) hipLaunchKernelGGL((k_attn_few<BF, KVM, DP, QB>), grid, dim3(NT), 0, st, a)
+#define TYPES(DP, QB)                                                                        \
+  if (bf) {                                                                                  \
+    if (kvm == 0) GO(true, 0, DP, QB); else if (kvm == 1) GO(true, 1, DP, QB); else GO(true, 2, DP, QB); \
+  } else {                                                                                   \
+    if (kvm == 0) GO(false, 0, DP, QB); else if (kvm == 1) GO(false, 1, DP, QB); else GO(false, 2, DP, QB); \
+  }
+  if (a.kv.d <= 64) { if (two) { TYPES(64, 2) } else { TYPES(64, 1) } }
+  else if (a.kv.d <= 128) { if (two) { TYPES(128, 2) } else { TYPES(128, 1) } }
+  else { TYPES(256, 1) }
+#undef TYPES
+#undef GO
+  return hipGetLastError();
+}

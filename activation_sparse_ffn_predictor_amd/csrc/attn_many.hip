@@ -1,0 +1,442 @@
+// Attention over the paged cache for many rows a K/V head (chunks of a prompt), and the join of split results.
+//
+// As the few-row kernel, S^T = K Q^T and O^T = V^T P^T, with 32x32x16 products: a lane's column is one of the wave's
+// 32 rows, its 16 scores per 32 keys are that row's, and they are the second product's operand as they are. Four
+// waves (128 rows of one K/V head, the query heads of a token next to each other) share tiles of 64 keys in LDS.
+#include "attn.h"
+
+using namespace sffn;
+
+namespace {
+
+constexpr int NT = 256, NW = 4, TK = 64;
+
+template <int DP>
+__device__ __forceinline__ int swz_k(int key) {   // slot of K's 16-byte chunk c: c ^ swz (16 rows, one column: all banks)
+  return DP >= 128 ? key & 15 : (key >> 1) & 7;
+}
+template <int DP>
+__device__ __forceinline__ int swz_v(int key) {   // V: 4 rows x 64 bytes of a transposing read on all banks
+  return DP >= 128 ? (key & 3) << 2 : ((key >> 1) & 1) << 2;
+}
+
+// Row tile -> sequence: tiles of the sequences in order, each ceil(n * G / MANY_ROWS). Every wave searches for
+// itself, 64 sequences at a step.
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, int want, int& s, int& tile, int& ntiles) {
+  int before = 0;
+  const int l = threadIdx.x & 63;
+  for (int s0 = 0; s0 < a.sq.S; s0 += 64) {
+    int nt = 0;
+    if (s0 + l < a.sq.S) {
+      const int x = min(max(a.sq.cu[s0 + l], 0), a.sq.T), y = min(a.sq.cu[s0 + l + 1], a.sq.T);
+      nt = (int)(((long)min(max(y - x, 0), a.max_q) * a.G + MANY_ROWS - 1) / MANY_ROWS);
+    }
+    int inc = nt;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int t = __shfl_up(inc, o, WAVE);
+      if (l >= o) inc += t;
+    }
+    const int all = __builtin_amdgcn_readlane(inc, 63);
+    if (want < before + all) {
+      const uint64_t hit = __ballot(before + inc > want);
+      const int k = __ffsll((unsigned long long)hit) - 1;
+      s = s0 + k;
+      ntiles = __builtin_amdgcn_readlane(nt, k);
+      tile = want - (before + __builtin_amdgcn_readlane(inc, k) - ntiles);
+      return true;
+    }
+    before += all;
+  }
+  return false;
+}
+
+template <bool BF, int KVM, int DP>
+__global__ __launch_bounds__(NT) void k_attn_many(AttnArgs a) {
+  constexpr bool C8 = KVM != 0, CB = BF && !C8;
+  constexpr int EB = C8 ? 1 : 2, RB = DP * 2, KS = DP / 16, DB = DP / 32;
+  constexpr int CPR = DP * EB / 16, RPI = 64 / CPR, LD = 16 / RPI;   // 16-byte chunks a cached row; rows, loads of a wave
+  __shared__ __align__(16) char kt[2][TK * RB], vt[2][TK * RB];
+  __shared__ __align__(16) float kf_[C8 ? 2 : 1][TK], lg_[C8 ? 2 : 1][TK], inv_[C8 ? 2 : 1][TK];
+  __shared__ int odd_[2];
+  __shared__ uint8_t vnan_[C8 ? 2 : 1][TK];
+  __shared__ float big_[NW];
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, h = l >> 5, ql = l & 31;
+  const int hk = blockIdx.x % a.kv.hkv, d = a.kv.d, G = a.G, split = blockIdx.y;
+  int s, tile, ntiles;
+  if (!find_tile(a, blockIdx.x / a.kv.hkv, s, tile, ntiles)) return;
+  tile = ntiles - 1 - tile;                        // the longest first
+  const Seq sq = load_seq(a.sq, s, a.kv.psh);
+  const int n = min(sq.n, a.max_q), r0 = tile * MANY_ROWS, rows = min(MANY_ROWS, n * G - r0);
+  const int p0 = sq.len - sq.n;
+  const int b_lo = p0 + r0 / G, b_hi = p0 + (r0 + rows - 1) / G;
+  const Units un = key_units(b_lo, b_hi, sq.len, a.window, a.sinks, MANY_USH);
+  const int per = share_units(un.tot, a.ns, MANY_LEAST, 1), used = max(1, (un.tot + per - 1) / per);
+  if (split >= used) return;
+  const int u0 = split * per, u1 = min(un.tot, u0 + per);
+
+  if (threadIdx.x < 2) odd_[threadIdx.x] = -1;
+  // this lane's row, and the wave's range of positions
+  const int r = r0 + w * 32 + ql, ri = r / G, rg = r - ri * G;
+  const bool mine = w * 32 + ql < rows;
+  const bool wave_on = w * 32 < rows;
+  const int p_lo = p0 + (r0 + w * 32) / G, p_hi = p0 + (r0 + min(w * 32 + 32, rows) - 1) / G;
+  const int pos = mine ? p0 + ri : p_hi;
+  uint4 qf[KS];
+  {
+    const char* qp = a.q + ((long)(sq.q0 + ri) * a.ldq + (long)(hk * G + rg) * d) * 2;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int ch = ks * 2 + h;
+      qf[ks] = mine && ch * 8 < d ? *reinterpret_cast<const uint4*>(qp + ch * 16) : make_uint4(0, 0, 0, 0);
+    }
+  }
+  float c = a.c;
+  if constexpr (C8 && BF) {   // bf16 queries into fp16's range, as in the few-row kernel
+    float big = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const uint32_t u[4] = {qf[ks].x, qf[ks].y, qf[ks].z, qf[ks].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) big = fmaxf(big, fmaxf(fabsf(lo16<true>(u[k])), fabsf(hi16<true>(u[k]))));
+    }
+    big = wave_max(big);
+    if (l == 0) big_[w] = big;
+    __syncthreads();
+    big = fmaxf(fmaxf(big_[0], big_[1]), fmaxf(big_[2], big_[3]));
+    const int e = big > 0.f && big < 3.4e38f ? 14 - ((int)((__float_as_uint(big) >> 23) & 255) - 127) : 0;
+    const int e1 = min(max(e, -126), 126);
+    const float up = __uint_as_float((uint32_t)(e1 + 127) << 23);
+    c = c * __uint_as_float((uint32_t)(127 - e1) << 23);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const uint4 t = qf[ks];
+      qf[ks] = make_uint4(pack2<false>(lo16<true>(t.x) * up, hi16<true>(t.x) * up),
+                          pack2<false>(lo16<true>(t.y) * up, hi16<true>(t.y) * up),
+                          pack2<false>(lo16<true>(t.z) * up, hi16<true>(t.z) * up),
+                          pack2<false>(lo16<true>(t.w) * up, hi16<true>(t.w) * up));
+    }
+  }
+
+  const int* trow = a.sq.table + (long)s * a.sq.ldt;
+  const uint32_t dB = (uint32_t)d * EB;
+  uint4 kr[LD], vr[LD];
+  float sk1 = 0.f, sv1 = 0.f;
+  int have = 0;
+  // this wave's 16 keys of the tile at t0 (one page); what does not exist reads as zeros
+  auto fetch = [&](int t0) {
+    const int t = t0 + w * 16, pg = t >> a.kv.psh;
+    const int pid = __builtin_amdgcn_readfirstlane(trow[min(pg, a.sq.cols - 1)]);
+    have = (unsigned)pid < (unsigned)a.kv.n_pages ? min(16, max(0, sq.len - t)) : 0;
+    const long row = (((long)(have ? pid : 0) * a.kv.hkv + hk) << a.kv.psh) + (t & ((1 << a.kv.psh) - 1));
+    const Buf bk(a.kv.k + row * dB, have * dB), bv(a.kv.v + row * dB, have * dB);
+#pragma unroll
+    for (int i = 0; i < LD; ++i) {
+      const uint32_t key = i * RPI + l / CPR, ch = l % CPR;
+      const uint32_t off = boff(ch * 16 < dB, key * dB + ch * 16);
+      kr[i] = bk.ld16(off);
+      vr[i] = bv.ld16(off);
+    }
+    if constexpr (C8) {
+      const Buf sk(a.kv.ks + row, have * 4), sv(a.kv.vs + row, have * 4);
+      sk1 = sk.ldf((l & 15) * 4);
+      sv1 = sv.ldf((l & 15) * 4);
+    }
+  };
+  // the fetched keys into LDS buffer b; 8-bit codes widened here, once a block
+  __shared__ int have_[2][NW];
+  auto store = [&](int b, int t0, int u) {
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < LD; ++i) {
+      const int key = w * 16 + i * RPI + l / CPR, ch = l % CPR;
+      if constexpr (C8) {
+        const uint2 k0 = codes4<KVM == 2>(kr[i].x), k1 = codes4<KVM == 2>(kr[i].y), k2 = codes4<KVM == 2>(kr[i].z),
+                    k3 = codes4<KVM == 2>(kr[i].w);
+        const uint2 v0 = codes4<KVM == 2>(vr[i].x), v1 = codes4<KVM == 2>(vr[i].y), v2 = codes4<KVM == 2>(vr[i].z),
+                    v3 = codes4<KVM == 2>(vr[i].w);
+        *reinterpret_cast<uint4*>(&kt[b][key * RB + (((2 * ch) ^ swz_k<DP>(key)) << 4)]) = make_uint4(k0.x, k0.y, k1.x, k1.y);
+        *reinterpret_cast<uint4*>(&kt[b][key * RB + (((2 * ch + 1) ^ swz_k<DP>(key)) << 4)]) = make_uint4(k2.x, k2.y, k3.x, k3.y);
+        *reinterpret_cast<uint4*>(&vt[b][key * RB + (((2 * ch) ^ swz_v<DP>(key)) << 4)]) = make_uint4(v0.x, v0.y, v1.x, v1.y);
+        *reinterpret_cast<uint4*>(&vt[b][key * RB + (((2 * ch + 1) ^ swz_v<DP>(key)) << 4)]) = make_uint4(v2.x, v2.y, v3.x, v3.y);
+      } else {
+        *reinterpret_cast<uint4*>(&kt[b][key * RB + ((ch ^ swz_k<DP>(key)) << 4)]) = kr[i];
+        *reinterpret_cast<uint4*>(&vt[b][key * RB + ((ch ^ swz_v<DP>(key)) << 4)]) = vr[i];
+        odd |= (nonfinite2<CB>(vr[i].x) | nonfinite2<CB>(vr[i].y) | nonfinite2<CB>(vr[i].z) | nonfinite2<CB>(vr[i].w)) != 0;
+      }
+    }
+    if constexpr (C8) {
+      if (l < 16) {
+        const VScale v = v_scale(sv1);
+        kf_[b][w * 16 + l] = sk1 * c;
+        lg_[b][w * 16 + l] = v.lg;
+        inv_[b][w * 16 + l] = v.inv;
+        vnan_[b][w * 16 + l] = sv1 != sv1 ? 1 : 0;
+        odd = sv1 != sv1;
+      }
+    }
+    if (odd) odd_[b] = u;                          // the tile holds an infinity or NaN in V
+    if (l == 0) have_[b][w] = have;
+  };
+
+  float m = -INFINITY, ls = 0.f;
+  f32x16 o[DB];
+#pragma unroll
+  for (int db = 0; db < DB; ++db)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[db][i] = 0.f;
+
+  if (u0 < u1) {
+    fetch(un.key0(u0, MANY_USH));
+    __syncthreads();                               // odd_ is set up
+    store(0, un.key0(u0, MANY_USH), u0);
+  }
+  for (int u = u0; u < u1; ++u) {
+    const int b = (u - u0) & 1, t0 = un.key0(u, MANY_USH);
+    __syncthreads();
+    if (u + 1 < u1) fetch(un.key0(u + 1, MANY_USH));
+    const int hv[4] = {have_[b][0], have_[b][1], have_[b][2], have_[b][3]};
+    if (wave_on && t0 <= p_hi) {
+      f32x16 sc[2];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sc[kb][i] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          const int key = kb * 32 + ql;
+          const uint4 kf = *reinterpret_cast<const uint4*>(&kt[b][key * RB + (((ks * 2 + h) ^ swz_k<DP>(key)) << 4)]);
+          sc[kb] = mfma32<CB>(kf, qf[ks], sc[kb]);
+        }
+      const bool full = hv[0] + hv[1] + hv[2] + hv[3] == TK && t0 + TK - 1 <= p_lo &&
+                        (a.window <= 0 || t0 > p_hi - a.window || t0 + TK <= a.sinks);
+      float x[2][16], top = -INFINITY;
+      uint32_t vis = 0xFFFFFFFFu;                  // bit kb * 16 + i
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (C8) {
+            const f32x4 kf = *reinterpret_cast<const f32x4*>(&kf_[b][kb * 32 + 8 * e + 4 * h]);
+            const f32x4 lg = *reinterpret_cast<const f32x4*>(&lg_[b][kb * 32 + 8 * e + 4 * h]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[kb][e * 4 + i] = fmaf(sc[kb][e * 4 + i], kf[i], lg[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[kb][e * 4 + i] = sc[kb][e * 4 + i] * c;
+          }
+        }
+      if (!full) {
+        vis = 0;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int kk = kb * 32 + 8 * (i >> 2) + 4 * h + (i & 3), j = t0 + kk;
+            const bool see = (kk & 15) < hv[kb * 2 + (i >> 3)] && j <= pos &&
+                             (a.window <= 0 || j > pos - a.window || j < a.sinks);
+            x[kb][i] = see ? x[kb][i] : -INFINITY;
+            vis |= see ? 1u << (kb * 16 + i) : 0u;
+          }
+      }
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, x[kb][i]);
+      top = fmaxf(top, __shfl_xor(top, 32, WAVE));
+      const float mn = fmaxf(m, top), ms = mn == -INFINITY ? 0.f : mn;
+      const float al = fade(m, ms);
+      const bool any_vnan = C8 && odd_[b] == u;
+      float sum = 0.f;
+      uint4 pf[4];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float p[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[i] = exp2_fast(x[kb][e * 4 + i] - ms);
+          if constexpr (C8) {
+            const f32x4 iv = *reinterpret_cast<const f32x4*>(&inv_[b][kb * 32 + 8 * e + 4 * h]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum = fmaf(p[i], iv[i], sum);
+          } else {
+            sum += (p[0] + p[1]) + (p[2] + p[3]);
+          }
+          if (any_vnan) {                          // a V row without a scale: NaN for the rows that see it
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if ((vis >> (kb * 16 + e * 4 + i) & 1) && vnan_[b][kb * 32 + 8 * e + 4 * h + i]) p[i] = __uint_as_float(0x7FC00000u);
+          }
+          const uint32_t a0 = pack2<CB>(p[0], p[1]), a1 = pack2<CB>(p[2], p[3]);
+          if (e & 1) { pf[kb * 2 + (e >> 1)].z = a0; pf[kb * 2 + (e >> 1)].w = a1; }
+          else { pf[kb * 2 + (e >> 1)].x = a0; pf[kb * 2 + (e >> 1)].y = a1; }
+        }
+      ls = ls * al + sum;
+      if (__any(mn > m)) {
+#pragma unroll
+        for (int db = 0; db < DB; ++db) o[db] *= al;
+      }
+      m = mn;
+      const bool slow = !C8 && !full && odd_[b] == u;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int db = 0; db < DB; ++db) {
+          const int key = kk * 16 + 4 * h + ((l & 15) >> 2);
+          const int ch = db * 4 + ((l >> 4) & 1) * 2 + ((l & 3) >> 1);
+          const int at = ((ch ^ swz_v<DP>(key)) << 4) + (l & 1) * 8;   // keys 8 apart: the same slot
+          const fp16x4 y0 = __builtin_amdgcn_ds_read_tr16_b64_v4f16(
+              (__attribute__((address_space(3))) fp16x4*)(&vt[b][key * RB + at]));
+          const fp16x4 y1 = __builtin_amdgcn_ds_read_tr16_b64_v4f16(
+              (__attribute__((address_space(3))) fp16x4*)(&vt[b][(key + 8) * RB + at]));
+          const uint2 z0 = __builtin_bit_cast(uint2, y0), z1 = __builtin_bit_cast(uint2, y1);
+          const uint4 vf = make_uint4(z0.x, z0.y, z1.x, z1.y);
+          if (!slow) {
+            o[db] = mfma32<CB>(vf, pf[kk], o[db]);
+          } else {
+            // infinities and NaN only where a row sees them (see the few-row kernel)
+            uint32_t fin[4], ind[3][4], one[4];
+            const uint32_t raw[4] = {vf.x, vf.y, vf.z, vf.w};
+            constexpr uint32_t ONE = CB ? 0x3F80u : 0x3C00u, EXP = CB ? 0x7F80u : 0x7C00u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              fin[k] = ind[0][k] = ind[1][k] = ind[2][k] = 0;
+#pragma unroll
+              for (int sh = 0; sh < 32; sh += 16) {
+                const uint32_t v = (raw[k] >> sh) & 0xFFFFu;
+                fin[k] |= ((v & EXP) != EXP ? v : 0u) << sh;
+                ind[0][k] |= (v == EXP ? ONE : 0u) << sh;
+                ind[1][k] |= (v == (EXP | 0x8000u) ? ONE : 0u) << sh;
+                ind[2][k] |= ((v & 0x7FFFu) > EXP ? ONE : 0u) << sh;
+              }
+              const uint32_t vb = vis >> (kk * 8 + k * 2);
+              one[k] = (vb & 1 ? ONE : 0u) | (vb & 2 ? ONE << 16 : 0u);
+            }
+            o[db] = mfma32<CB>(make_uint4(fin[0], fin[1], fin[2], fin[3]), pf[kk], o[db]);
+#pragma unroll
+            for (int kind = 0; kind < 3; ++kind) {
+              f32x16 cnt;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) cnt[i] = 0.f;
+              cnt = mfma32<CB>(make_uint4(ind[kind][0], ind[kind][1], ind[kind][2], ind[kind][3]),
+                               make_uint4(one[0], one[1], one[2], one[3]), cnt);
+              const float add = __uint_as_float(kind == 0 ? 0x7F800000u : kind == 1 ? 0xFF800000u : 0x7FC00000u);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[db][i] += cnt[i] > 0.f ? add : 0.f;
+            }
+          }
+        }
+    }
+    if (u + 1 < u1) store(b ^ 1, un.key0(u + 1, MANY_USH), u + 1);
+  }
+
+  if (!wave_on) return;
+  ls += __shfl_xor(ls, 32, WAVE);
+  if (!mine) return;
+  const long row = (long)(sq.q0 + ri) * a.hq + hk * G + rg;
+  if (used == 1) {
+    const float iv = ls == 0.f ? 0.f : 1.f / ls;   // no key was visible: 0
+    char* op = a.out + ((long)(sq.q0 + ri) * a.ldo + (long)(hk * G + rg) * d) * 2;
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int d0 = db * 32 + e * 8 + h * 4;
+        if (d0 < d)
+          *reinterpret_cast<uint2*>(op + d0 * 2) = make_uint2(pack2<BF>(o[db][e * 4] * iv, o[db][e * 4 + 1] * iv),
+                                                              pack2<BF>(o[db][e * 4 + 2] * iv, o[db][e * 4 + 3] * iv));
+      }
+    if (a.lse && h == 0) a.lse[row] = log_sum(m, ls);
+  } else {
+    float* po = a.po + (row * a.ns + split) * d;
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int d0 = db * 32 + e * 8 + h * 4;
+        if (d0 < d)
+          *reinterpret_cast<f32x4*>(po + d0) = f32x4{o[db][e * 4], o[db][e * 4 + 1], o[db][e * 4 + 2], o[db][e * 4 + 3]};
+      }
+    if (h == 0) a.pml[row * a.ns + split] = make_float2(m, ls);
+  }
+}
+
+// Split results of a row added in the order of the shares: one wave a row, lanes over the head's elements. Which
+// shares exist follows from the same rule as in the kernels above.
+template <bool BF>
+__global__ __launch_bounds__(NT) void k_attn_join(AttnArgs a, int few) {
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
+  const long row = (long)blockIdx.x * NW + w;
+  if (row >= (long)a.sq.T * a.hq) return;
+  const int t = (int)(row / a.hq), hq = (int)(row - (long)t * a.hq), g = hq % a.G, d = a.kv.d;
+  const int s = __builtin_amdgcn_readfirstlane(find_seq<64>(a.sq.cu, a.sq.S, t));
+  if (s >= a.sq.S) return;
+  const Seq sq = load_seq(a.sq, s, a.kv.psh);
+  const int n = min(sq.n, a.max_q), i = t - sq.q0, p0 = sq.len - sq.n;
+  if (i < 0 || i >= n) return;
+  int lo, hi;                                      // positions of the row's tile
+  if (few) {
+    lo = p0;
+    hi = p0 + n - 1;
+  } else {
+    const int r0 = (i * a.G + g) / MANY_ROWS * MANY_ROWS;
+    lo = p0 + r0 / a.G;
+    hi = p0 + (min(n * a.G, r0 + MANY_ROWS) - 1) / a.G;
+  }
+  const Units un = key_units(lo, hi, sq.len, a.window, a.sinks, few ? FEW_USH : MANY_USH);
+  const int per = share_units(un.tot, a.ns, few ? FEW_LEAST : MANY_LEAST, few ? NW : 1);
+  const int used = (un.tot + per - 1) / per;
+  if (used <= 1) return;                           // the row's only block has written it
+  const float2* ml = a.pml + row * a.ns;
+  float M = -INFINITY;
+  for (int k = l; k < used; k += 64) M = fmaxf(M, ml[k].x);
+  M = wave_max(M);
+  const float ms = M == -INFINITY ? 0.f : M;
+  float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  const float* po = a.po + row * a.ns * d;
+  for (int k = 0; k < used; ++k) {
+    const float2 v = ml[k];
+    const float f = fade(v.x, ms);
+    L = fmaf(v.y, f, L);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (l + e * 64 < d) acc[e] = fmaf(po[(long)k * d + l + e * 64], f, acc[e]);
+  }
+  const float iv = L == 0.f ? 0.f : 1.f / L;
+  char* op = a.out + ((long)t * a.ldo + (long)hq * d) * 2;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (l + e * 64 < d) *reinterpret_cast<uint16_t*>(op + (l + e * 64) * 2) = (uint16_t)pack2<BF>(acc[e] * iv, 0.f);
+  if (a.lse && l == 0) a.lse[row] = log_sum(M, L);
+}
+
+}  // namespace
+
+hipError_t sffn_launch_attn_many(const AttnArgs& a, int qt, int kvt, hipStream_t st) {
+  // at most T * G / MANY_ROWS whole tiles, and one that is not whole for each sequence
+  const long tiles = (long)a.sq.T * a.G / MANY_ROWS + (a.sq.S < a.sq.T ? a.sq.S : a.sq.T);
+  const dim3 grid((unsigned)(tiles * a.kv.hkv), a.ns);
+  const bool bf = qt == T_BF16;
+  const int kvm = kvt == T_I8 ? 1 : kvt == T_E4M3 ? 2 : 0;
+#define GO(BF, KVM, DP) hipLaunchKernelGGL((k_attn_many<BF, KVM, DP>), grid, dim3(NT), 0, st, a)
+#define TYPES(DP)                                                                   \
+  if (bf) {                                                                         \
+    if (kvm == 0) GO(true, 0, DP); else if (kvm == 1) GO(true, 1, DP); else GO(true, 2, DP);    \
+  } else {                                                                          \
+    if (kvm == 0) GO(false, 0, DP); else if (kvm == 1) GO(false, 1, DP); else GO(false, 2, DP); \
+  }
+  if (a.kv.d <= 64) { TYPES(64) } else if (a.kv.d <= 128) { TYPES(128) } else { TYPES(256) }
+#undef TYPES
+#undef GO
+  return hipGetLastError();
+}
+
+hipError_t sffn_launch_attn_join(const AttnArgs& a, int qt, bool few, hipStream_t st) {
+  const dim3 grid((unsigned)(((long)a.sq.T * a.hq + NW - 1) / NW));
+  if (qt == T_BF16) hipLaunchKernelGGL((k_attn_join<true>), grid, dim3(NT), 0, st, a, (int)few);
+  else hipLaunchKernelGGL((k_attn_join<false>), grid, dim3(NT), 0, st, a, (int)few);
+  return hipGetLastError();
+}

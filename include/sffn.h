@@ -224,6 +224,91 @@ enum { SFFN_K_PRED_H = 0, SFFN_K_PRED_Z = 1, SFFN_K_ROWS = 2, SFFN_K_COLS = 3 };
 int sffn_profile_begin(int kernel, int max_launches);
 int sffn_profile_end(float* ms, int max);
 
+/* ---------------------------------------------------------------------------------------------------------------
+ * The attention half of a layer: residual norm, paged K/V cache, attention of new tokens over it.
+ *
+ * Element types. 16-bit tensors (queries, new K / V, outputs) are SFFN_F16 or SFFN_BF16. A cache holds the same
+ * 16-bit type, or 8-bit codes (SFFN_I8, SFFN_E4M3: OCP e4m3) with one fp32 scale per token and head:
+ *   scale = fp32(max|x| / top), top = 127 or 448;  code = x / scale rounded to nearest, ties to even (of the exact
+ *   quotient);  value = code * scale.
+ * Rows whose scale would be below 2^-100 are stored as zeros with scale 0; a row that holds an infinity or NaN is
+ * stored with scale NaN and codes 0. */
+typedef enum { SFFN_F32 = 0, SFFN_F16 = 1, SFFN_BF16 = 2, SFFN_I8 = 3, SFFN_E4M3 = 4 } sffn_type;
+
+/* One layer's cache (device pointers, contiguous): k, v [n_pages, n_kv_heads, page, head_dim], and for 8-bit types
+ * k_scale, v_scale [n_pages, n_kv_heads, page] fp32 (else ignored). page: a power of two, 16 .. 1024. head_dim: a
+ * multiple of 8 (16 for 8-bit types), 16 .. 256. n_pages * n_kv_heads * page < 2^31; n_kv_heads <= 65535. */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int type, n_pages, page, n_kv_heads, head_dim;
+} sffn_kv;
+
+/* The sequences of a call (device pointers to int32). Rows cu[s] .. cu[s + 1] - 1 of the call's token tensors (T rows
+ * in all; cu [S + 1] ascends from 0) are the newest tokens of sequence s, whose cache holds kv_len[s] tokens with
+ * them: the i-th of n stands at position kv_len[s] - n + i. Position p lies in slot p % page of page
+ * table[s * table_stride + p / page]; a table row holds max_pages entries. Rows at and behind cu[S] belong to no
+ * sequence: they are neither read nor written. The arrays are read on the device, so they are not checked on the
+ * host; whatever they hold, no access leaves the given tensors: a position outside the table row or a page id
+ * outside 0 .. n_pages - 1 holds no token (not written, not read, not seen). Tokens before a sequence's first
+ * (kv_len[s] < n) see nothing. 1 <= S <= 65535, 0 <= T <= 2^24 (T = 0: nothing is done), max_pages * page <= 2^30. */
+typedef struct {
+  const int32_t* cu;
+  const int32_t* kv_len;
+  const int32_t* table;
+  int S, T, max_pages, table_stride;
+} sffn_seqs;
+
+/* New tokens' K and V into the cache. k, v: [T, n_kv_heads, head_dim] of a 16-bit `type` (the cache's own if that has
+ * 16 bits), tokens k_stride and v_stride elements apart (multiples of 8, at least n_kv_heads * head_dim, so columns
+ * of a fused Q/K/V product serve as they are). Two tokens of one call that share a slot (sequences whose tables
+ * share the page that is written) leave it undefined. One kernel. */
+int sffn_kv_write(sffn_kv cache, sffn_seqs seqs, int type, const void* k, int64_t k_stride, const void* v,
+                  int64_t v_stride, void* stream);
+
+/* The other way: the rows named by seqs (cu[s + 1] - cu[s] = kv_len[s] takes whole sequences) as contiguous K and V,
+ * code * scale rounded once to `type`; a 16-bit cache is copied. Rows whose position holds no token stay as they
+ * were. One kernel. */
+int sffn_kv_read(sffn_kv cache, sffn_seqs seqs, int type, void* k, int64_t k_stride, void* v, int64_t v_stride,
+                 void* stream);
+
+/* Attention of the new tokens over the cache, which holds them already (sffn_kv_write first):
+ *   out[t, h, :] = sum_j softmax_j(scale * q[t, h, :] . K[j, h', :]) V[j, h', :],   h' = h / (Hq / n_kv_heads)
+ * over the positions j that token t at position p sees: j <= p, j < kv_len, and if window > 0 also j > p - window or
+ * j < sinks (a sliding window beside which the first `sinks` tokens stay visible). A token that sees nothing gets
+ * zeros. What lies in places a token does not see, infinities and NaN included, has no effect on it.
+ * q [T, Hq, head_dim] of a 16-bit `type` (the cache's own if that has 16 bits), out likewise, tokens q_stride and
+ * out_stride elements apart (multiples of 8). lse [T, Hq] fp32 or NULL: the natural logarithm of the softmax's sum
+ * (-infinity for a token that sees nothing). Scores, sums and accumulators are fp32; the weights enter the second
+ * product as 16-bit values, and 8-bit codes enter both products exactly.
+ * max_q: at least the largest number of new tokens of one sequence (tokens past it are not computed and their rows
+ * stay as they were). max_kv: about the largest kv_len; it decides only over how many workgroups a sequence's keys
+ * are spread. Up to 32 rows max_q * Hq / n_kv_heads (16 for head_dim > 128) run the few-row kernel
+ * (SFFN_ATTN_FEW), more run the tile kernel (SFFN_ATTN_MANY); where keys are spread a second kernel joins the parts
+ * in a fixed order, so the same call gives the same bits. The workspace needs sffn_attn_workspace_size bytes of
+ * the same sizes (0: none needed, ws may be NULL); it holds nothing between calls, and calls that overlap in time
+ * need separate ones. Hq * T < 2^31. */
+enum { SFFN_ATTN_FEW = 0, SFFN_ATTN_MANY = 1 };
+int sffn_attn_path(int Hq, int n_kv_heads, int head_dim, int max_q);   /* -1 for bad sizes */
+size_t sffn_attn_workspace_size(int T, int S, int Hq, int n_kv_heads, int head_dim, int max_q, int max_kv, int window,
+                                int sinks);
+int sffn_attn(sffn_kv cache, sffn_seqs seqs, int type, const void* q, int64_t q_stride, int Hq, int max_q, int max_kv,
+              float scale, int window, int sinks, void* out, int64_t out_stride, float* lse, void* ws, size_t ws_bytes,
+              void* stream);
+
+/* Root-mean-square norm with the residual's addition:
+ *   h = x + res (fp32; h = x if res is NULL);  res_out = h rounded to res_type (if non-NULL; may be res itself)
+ *   y = h / sqrt(mean(h^2) + eps) * w          (from the unrounded h)
+ * x, res, res_out [T, D] of SFFN_F32 / F16 / BF16 (res and res_out of one type), w [D] fp32 or NULL (1), y [T, D] of
+ * any type; 8-bit y is codes with y_scale [T] fp32 as in the cache, per row and without its lower limit, computed in
+ * 64 bits from h on. Row strides in elements, multiples of 8, at least D. D as elsewhere:
+ * 8 <= D <= 16384, D % 8 == 0. eps >= 0. y overlaps no input. 0 <= T <= 2^24. One kernel. */
+int sffn_add_rmsnorm(int x_type, const void* x, int64_t x_stride, int res_type, const void* res, int64_t res_stride,
+                     const float* w, double eps, int T, int D, int y_type, void* y, int64_t y_stride, float* y_scale,
+                     void* res_out, int64_t res_out_stride, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
