@@ -93,7 +93,8 @@ struct AttnArgs {
   Seqs sq;
   int hq, G, max_q, window, sinks, ns;
   long ldq, ldo;            // elements between tokens
-  float c;                  // softmax scale * log2(e)
+  float c;                  // |softmax scale| * log2(e)
+  int neg;                  // the scale is negative: the queries' signs are turned as they are loaded
   float* po;                // partial outputs [T * hq][ns][d], used when ns > 1
   float2* pml;              // their maxima (log2 domain) and sums [T * hq][ns]
 };
@@ -142,6 +143,46 @@ template <bool BF>
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t u) {
   constexpr uint32_t E = BF ? 0x7F807F80u : 0x7C007C00u, L = BF ? 0x00800080u : 0x04000400u;
   return ((u & E) + L) & 0x80008000u;
+}
+
+// eight 16-bit values: signs turned; largest magnitude; infinities and NaN replaced by 0
+__device__ __forceinline__ uint4 flip_signs(const uint4& t) {
+  return make_uint4(t.x ^ 0x80008000u, t.y ^ 0x80008000u, t.z ^ 0x80008000u, t.w ^ 0x80008000u);
+}
+template <bool BF>
+__device__ __forceinline__ float absmax8(const uint4& t) {
+  const uint32_t u[4] = {t.x, t.y, t.z, t.w};
+  float big = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) big = fmaxf(big, fmaxf(fabsf(lo16<BF>(u[k])), fabsf(hi16<BF>(u[k]))));
+  return big;
+}
+template <bool BF>
+__device__ __forceinline__ uint4 finite_only(const uint4& t) {
+  constexpr uint32_t E = BF ? 0x7F80u : 0x7C00u;
+  uint32_t u[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t a = u[k] & 0xFFFFu, b = u[k] >> 16;
+    u[k] = ((a & E) != E ? a : 0u) | ((b & E) != E ? b << 16 : 0u);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+// bf16 queries for fp16 products: all times one power of two that takes the largest, `big`, to 2^14 .. 2^15 (exact
+// but for elements below 2^-29 of it, which lose bits under 2^-40 of it); c takes the factor back.
+__device__ __forceinline__ float to_f16_range(float big, float& c) {
+  const int e = big > 0.f && big < 3.4e38f ? 14 - ((int)((__float_as_uint(big) >> 23) & 255) - 127) : 0;
+  const int e1 = min(max(e, -126), 126);
+  c = c * __uint_as_float((uint32_t)(127 - e1) << 23);
+  return __uint_as_float((uint32_t)(e1 + 127) << 23);
+}
+__device__ __forceinline__ uint4 bf16_to_f16(const uint4& t, float f) {
+  const uint32_t u[4] = {t.x, t.y, t.z, t.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    o[k] = __builtin_bit_cast(uint32_t, half2v{(_Float16)(lo16<true>(u[k]) * f), (_Float16)(hi16<true>(u[k]) * f)});
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // Four 8-bit codes as four fp16 values (exact). int8: the code + 128 in the low byte of 0x64xx is 1024 + code + 128;

@@ -175,7 +175,8 @@ int sffn_attn(sffn_kv c, sffn_seqs q, int type, const void* qp, int64_t q_stride
   a.ns = ns;
   a.ldq = q_stride;
   a.ldo = out_stride;
-  a.c = scale * 1.4426950408889634f;
+  a.c = fabsf(scale) * 1.4426950408889634f;
+  a.neg = scale < 0.f;
   a.po = (float*)ws;
   a.pml = (float2*)((char*)ws + (ns > 1 ? po_bytes(q.T, Hq, c.head_dim, ns) : 0));
   hipStream_t st = (hipStream_t)stream;

@@ -51,15 +51,28 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int want, int& s, i
   return false;
 }
 
+// One 16-byte direct load per lane from `off` (a lane past the descriptor's bytes gets zeros) to LDS at dst + 16 * lane.
+__device__ __forceinline__ void load_lds(const Buf& b, char* dst, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b.r, (__attribute__((address_space(3))) void*)dst, 16, (int)off, 0, 0, 0);
+}
+
+// LDS of one tile of 64 keys.
+template <int DP, bool C8>
+struct Tile {
+  alignas(16) char k[TK * DP * 2];
+  alignas(16) char v[TK * DP * 2];
+  alignas(16) float kf[C8 ? TK : 4], lg[C8 ? TK : 4], inv[C8 ? TK : 4];   // see VScale; kf: K scale * softmax scale
+  int have[NW];                                  // keys of each 16 that exist
+  int odd;                                       // the last unit with an infinity or NaN in V that was stored here
+  uint8_t vnan[C8 ? TK : 4];
+};
+
 template <bool BF, int KVM, int DP>
-__global__ __launch_bounds__(NT) void k_attn_many(AttnArgs a) {
+__global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a) {
   constexpr bool C8 = KVM != 0, CB = BF && !C8;
   constexpr int EB = C8 ? 1 : 2, RB = DP * 2, KS = DP / 16, DB = DP / 32;
   constexpr int CPR = DP * EB / 16, RPI = 64 / CPR, LD = 16 / RPI;   // 16-byte chunks a cached row; rows, loads of a wave
-  __shared__ __align__(16) char kt[2][TK * RB], vt[2][TK * RB];
-  __shared__ __align__(16) float kf_[C8 ? 2 : 1][TK], lg_[C8 ? 2 : 1][TK], inv_[C8 ? 2 : 1][TK];
-  __shared__ int odd_[2];
-  __shared__ uint8_t vnan_[C8 ? 2 : 1][TK];
+  __shared__ Tile<DP, C8> tile0, tile1;
   __shared__ float big_[NW];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, h = l >> 5, ql = l & 31;
   const int hk = blockIdx.x % a.kv.hkv, d = a.kv.d, G = a.G, split = blockIdx.y;
@@ -75,7 +88,7 @@ __global__ __launch_bounds__(NT) void k_attn_many(AttnArgs a) {
   if (split >= used) return;
   const int u0 = split * per, u1 = min(un.tot, u0 + per);
 
-  if (threadIdx.x < 2) odd_[threadIdx.x] = -1;
+  if (threadIdx.x == 0) tile0.odd = tile1.odd = -1;
   // this lane's row, and the wave's range of positions
   const int r = r0 + w * 32 + ql, ri = r / G, rg = r - ri * G;
   const bool mine = w * 32 + ql < rows;
@@ -89,94 +102,89 @@ __global__ __launch_bounds__(NT) void k_attn_many(AttnArgs a) {
     for (int ks = 0; ks < KS; ++ks) {
       const int ch = ks * 2 + h;
       qf[ks] = mine && ch * 8 < d ? *reinterpret_cast<const uint4*>(qp + ch * 16) : make_uint4(0, 0, 0, 0);
+      if (a.neg) qf[ks] = flip_signs(qf[ks]);
     }
   }
   float c = a.c;
   if constexpr (C8 && BF) {   // bf16 queries into fp16's range, as in the few-row kernel
     float big = 0.f;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const uint32_t u[4] = {qf[ks].x, qf[ks].y, qf[ks].z, qf[ks].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) big = fmaxf(big, fmaxf(fabsf(lo16<true>(u[k])), fabsf(hi16<true>(u[k]))));
-    }
+    for (int ks = 0; ks < KS; ++ks) big = fmaxf(big, absmax8<true>(qf[ks]));
     big = wave_max(big);
     if (l == 0) big_[w] = big;
     __syncthreads();
-    big = fmaxf(fmaxf(big_[0], big_[1]), fmaxf(big_[2], big_[3]));
-    const int e = big > 0.f && big < 3.4e38f ? 14 - ((int)((__float_as_uint(big) >> 23) & 255) - 127) : 0;
-    const int e1 = min(max(e, -126), 126);
-    const float up = __uint_as_float((uint32_t)(e1 + 127) << 23);
-    c = c * __uint_as_float((uint32_t)(127 - e1) << 23);
+    const float up = to_f16_range(fmaxf(fmaxf(big_[0], big_[1]), fmaxf(big_[2], big_[3])), c);
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const uint4 t = qf[ks];
-      qf[ks] = make_uint4(pack2<false>(lo16<true>(t.x) * up, hi16<true>(t.x) * up),
-                          pack2<false>(lo16<true>(t.y) * up, hi16<true>(t.y) * up),
-                          pack2<false>(lo16<true>(t.z) * up, hi16<true>(t.z) * up),
-                          pack2<false>(lo16<true>(t.w) * up, hi16<true>(t.w) * up));
-    }
+    for (int ks = 0; ks < KS; ++ks) qf[ks] = bf16_to_f16(qf[ks], up);
   }
+  if (threadIdx.x == 0) { tile0.odd = -1; tile1.odd = -1; }
+  __syncthreads();
 
   const int* trow = a.sq.table + (long)s * a.sq.ldt;
   const uint32_t dB = (uint32_t)d * EB;
-  uint4 kr[LD], vr[LD];
+  // A wave brings 16 keys of a tile (they share a page); what does not exist reads as zeros. 16-bit rows go straight
+  // to LDS: the lane for slot l % CPR of a row loads the chunk that belongs there. 8-bit codes pass through
+  // registers and are widened once a block.
+  uint4 kr[C8 ? LD : 1], vr[C8 ? LD : 1];
   float sk1 = 0.f, sv1 = 0.f;
   int have = 0;
-  // this wave's 16 keys of the tile at t0 (one page); what does not exist reads as zeros
-  auto fetch = [&](int t0) {
-    const int t = t0 + w * 16, pg = t >> a.kv.psh;
-    const int pid = __builtin_amdgcn_readfirstlane(trow[min(pg, a.sq.cols - 1)]);
+  uint32_t ko[LD], vo[LD];
+#pragma unroll
+  for (int i = 0; i < LD; ++i) {
+    const uint32_t key = i * RPI + l / CPR, slot = l % CPR;
+    const uint32_t kc = C8 ? slot : slot ^ swz_k<DP>(key), vc = C8 ? slot : slot ^ swz_v<DP>(key);
+    ko[i] = boff(kc * 16 < dB, key * dB + kc * 16);
+    vo[i] = boff(vc * 16 < dB, key * dB + vc * 16);
+  }
+  auto page_of = [&](int t0) { return trow[min((t0 + w * 16) >> a.kv.psh, a.sq.cols - 1)]; };
+  auto fetch = [&](Tile<DP, C8>& tl, int t0, int page) {
+    const int t = t0 + w * 16;
+    const int pid = __builtin_amdgcn_readfirstlane(page);
     have = (unsigned)pid < (unsigned)a.kv.n_pages ? min(16, max(0, sq.len - t)) : 0;
     const long row = (((long)(have ? pid : 0) * a.kv.hkv + hk) << a.kv.psh) + (t & ((1 << a.kv.psh) - 1));
     const Buf bk(a.kv.k + row * dB, have * dB), bv(a.kv.v + row * dB, have * dB);
 #pragma unroll
     for (int i = 0; i < LD; ++i) {
-      const uint32_t key = i * RPI + l / CPR, ch = l % CPR;
-      const uint32_t off = boff(ch * 16 < dB, key * dB + ch * 16);
-      kr[i] = bk.ld16(off);
-      vr[i] = bv.ld16(off);
+      if constexpr (C8) {
+        kr[i] = bk.ld16(ko[i]);
+        vr[i] = bv.ld16(vo[i]);
+      } else {
+        load_lds(bk, tl.k + (w * 16 + i * RPI) * RB, ko[i]);
+        load_lds(bv, tl.v + (w * 16 + i * RPI) * RB, vo[i]);
+      }
     }
     if constexpr (C8) {
       const Buf sk(a.kv.ks + row, have * 4), sv(a.kv.vs + row, have * 4);
       sk1 = sk.ldf((l & 15) * 4);
       sv1 = sv.ldf((l & 15) * 4);
     }
+    if (!C8 && l == 0) tl.have[w] = have;
   };
-  // the fetched keys into LDS buffer b; 8-bit codes widened here, once a block
-  __shared__ int have_[2][NW];
-  auto store = [&](int b, int t0, int u) {
-    bool odd = false;
+  // 8-bit: the fetched codes into the tile
+  auto store = [&](Tile<DP, C8>& tl, int u) {
+    if constexpr (C8) {
 #pragma unroll
-    for (int i = 0; i < LD; ++i) {
-      const int key = w * 16 + i * RPI + l / CPR, ch = l % CPR;
-      if constexpr (C8) {
+      for (int i = 0; i < LD; ++i) {
+        const int key = w * 16 + i * RPI + l / CPR, ch = l % CPR;
         const uint2 k0 = codes4<KVM == 2>(kr[i].x), k1 = codes4<KVM == 2>(kr[i].y), k2 = codes4<KVM == 2>(kr[i].z),
                     k3 = codes4<KVM == 2>(kr[i].w);
         const uint2 v0 = codes4<KVM == 2>(vr[i].x), v1 = codes4<KVM == 2>(vr[i].y), v2 = codes4<KVM == 2>(vr[i].z),
                     v3 = codes4<KVM == 2>(vr[i].w);
-        *reinterpret_cast<uint4*>(&kt[b][key * RB + (((2 * ch) ^ swz_k<DP>(key)) << 4)]) = make_uint4(k0.x, k0.y, k1.x, k1.y);
-        *reinterpret_cast<uint4*>(&kt[b][key * RB + (((2 * ch + 1) ^ swz_k<DP>(key)) << 4)]) = make_uint4(k2.x, k2.y, k3.x, k3.y);
-        *reinterpret_cast<uint4*>(&vt[b][key * RB + (((2 * ch) ^ swz_v<DP>(key)) << 4)]) = make_uint4(v0.x, v0.y, v1.x, v1.y);
-        *reinterpret_cast<uint4*>(&vt[b][key * RB + (((2 * ch + 1) ^ swz_v<DP>(key)) << 4)]) = make_uint4(v2.x, v2.y, v3.x, v3.y);
-      } else {
-        *reinterpret_cast<uint4*>(&kt[b][key * RB + ((ch ^ swz_k<DP>(key)) << 4)]) = kr[i];
-        *reinterpret_cast<uint4*>(&vt[b][key * RB + ((ch ^ swz_v<DP>(key)) << 4)]) = vr[i];
-        odd |= (nonfinite2<CB>(vr[i].x) | nonfinite2<CB>(vr[i].y) | nonfinite2<CB>(vr[i].z) | nonfinite2<CB>(vr[i].w)) != 0;
+        *reinterpret_cast<uint4*>(&tl.k[key * RB + (((2 * ch) ^ swz_k<DP>(key)) << 4)]) = make_uint4(k0.x, k0.y, k1.x, k1.y);
+        *reinterpret_cast<uint4*>(&tl.k[key * RB + (((2 * ch + 1) ^ swz_k<DP>(key)) << 4)]) = make_uint4(k2.x, k2.y, k3.x, k3.y);
+        *reinterpret_cast<uint4*>(&tl.v[key * RB + (((2 * ch) ^ swz_v<DP>(key)) << 4)]) = make_uint4(v0.x, v0.y, v1.x, v1.y);
+        *reinterpret_cast<uint4*>(&tl.v[key * RB + (((2 * ch + 1) ^ swz_v<DP>(key)) << 4)]) = make_uint4(v2.x, v2.y, v3.x, v3.y);
       }
-    }
-    if constexpr (C8) {
       if (l < 16) {
         const VScale v = v_scale(sv1);
-        kf_[b][w * 16 + l] = sk1 * c;
-        lg_[b][w * 16 + l] = v.lg;
-        inv_[b][w * 16 + l] = v.inv;
-        vnan_[b][w * 16 + l] = sv1 != sv1 ? 1 : 0;
-        odd = sv1 != sv1;
+        tl.kf[w * 16 + l] = sk1 * c;
+        tl.lg[w * 16 + l] = v.lg;
+        tl.inv[w * 16 + l] = v.inv;
+        tl.vnan[w * 16 + l] = sv1 != sv1 ? 1 : 0;
+        if (sv1 != sv1) tl.odd = u;
       }
+      if (l == 0) tl.have[w] = have;
     }
-    if (odd) odd_[b] = u;                          // the tile holds an infinity or NaN in V
-    if (l == 0) have_[b][w] = have;
   };
 
   float m = -INFINITY, ls = 0.f;
@@ -186,151 +194,189 @@ __global__ __launch_bounds__(NT) void k_attn_many(AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[db][i] = 0.f;
 
-  if (u0 < u1) {
-    fetch(un.key0(u0, MANY_USH));
-    __syncthreads();                               // odd_ is set up
-    store(0, un.key0(u0, MANY_USH), u0);
-  }
-  for (int u = u0; u < u1; ++u) {
-    const int b = (u - u0) & 1, t0 = un.key0(u, MANY_USH);
-    __syncthreads();
-    if (u + 1 < u1) fetch(un.key0(u + 1, MANY_USH));
-    const int hv[4] = {have_[b][0], have_[b][1], have_[b][2], have_[b][3]};
-    if (wave_on && t0 <= p_hi) {
-      f32x16 sc[2];
+  auto v_frag = [&](const Tile<DP, C8>& tl, int kk, int db) {
+    const int key = kk * 16 + 4 * h + ((l & 15) >> 2);
+    const int ch = db * 4 + ((l >> 4) & 1) * 2 + ((l & 3) >> 1);
+    const int at = ((ch ^ swz_v<DP>(key)) << 4) + (l & 1) * 8;   // keys 8 apart: the same slot
+    const fp16x4 y0 = __builtin_amdgcn_ds_read_tr16_b64_v4f16((__attribute__((address_space(3))) fp16x4*)(&tl.v[key * RB + at]));
+    const fp16x4 y1 = __builtin_amdgcn_ds_read_tr16_b64_v4f16((__attribute__((address_space(3))) fp16x4*)(&tl.v[(key + 8) * RB + at]));
+    const uint2 z0 = __builtin_bit_cast(uint2, y0), z1 = __builtin_bit_cast(uint2, y1);
+    return make_uint4(z0.x, z0.y, z1.x, z1.y);
+  };
+
+  // one tile: scores, softmax, weighted sum
+  auto work = [&](const Tile<DP, C8>& tl, int u, int t0) {
+    f32x16 sc[2];
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sc[kb][i] = 0.f;
+      for (int i = 0; i < 16; ++i) sc[kb][i] = 0.f;
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
+    for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          const int key = kb * 32 + ql;
-          const uint4 kf = *reinterpret_cast<const uint4*>(&kt[b][key * RB + (((ks * 2 + h) ^ swz_k<DP>(key)) << 4)]);
-          sc[kb] = mfma32<CB>(kf, qf[ks], sc[kb]);
-        }
-      const bool full = hv[0] + hv[1] + hv[2] + hv[3] == TK && t0 + TK - 1 <= p_lo &&
-                        (a.window <= 0 || t0 > p_hi - a.window || t0 + TK <= a.sinks);
-      float x[2][16], top = -INFINITY;
-      uint32_t vis = 0xFFFFFFFFu;                  // bit kb * 16 + i
+      for (int kb = 0; kb < 2; ++kb) {
+        const int key = kb * 32 + ql;
+        const uint4 kf = *reinterpret_cast<const uint4*>(&tl.k[key * RB + (((ks * 2 + h) ^ swz_k<DP>(key)) << 4)]);
+        sc[kb] = mfma32<CB>(kf, qf[ks], sc[kb]);
+      }
+    if constexpr (C8) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if constexpr (C8) {
-            const f32x4 kf = *reinterpret_cast<const f32x4*>(&kf_[b][kb * 32 + 8 * e + 4 * h]);
-            const f32x4 lg = *reinterpret_cast<const f32x4*>(&lg_[b][kb * 32 + 8 * e + 4 * h]);
+          const f32x4 kf = *reinterpret_cast<const f32x4*>(&tl.kf[kb * 32 + 8 * e + 4 * h]);
+          const f32x4 lg = *reinterpret_cast<const f32x4*>(&tl.lg[kb * 32 + 8 * e + 4 * h]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[kb][e * 4 + i] = fmaf(sc[kb][e * 4 + i], kf[i], lg[i]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[kb][e * 4 + i] = sc[kb][e * 4 + i] * c;
-          }
+          for (int i = 0; i < 4; ++i) sc[kb][e * 4 + i] = fmaf(sc[kb][e * 4 + i], kf[i], lg[i]);
         }
-      if (!full) {
-        vis = 0;
+    }
+    const int hv0 = tl.have[0], hv1 = tl.have[1], hv2 = tl.have[2], hv3 = tl.have[3], nv = hv0 + hv1 + hv2 + hv3;
+    const bool full = nv == TK && t0 + TK - 1 <= p_lo &&
+                      (a.window <= 0 || t0 > p_hi - a.window || t0 + TK <= a.sinks);
+    if (!full) {
+      // element (kb, e, i) is key kb * 32 + 8 e + i of those that start at 4 h
+      const bool holes = (hv0 < 16 && hv1 + hv2 + hv3) || (hv1 < 16 && hv2 + hv3) || (hv2 < 16 && hv3);
+      const int hi = min(pos - t0, holes ? TK - 1 : nv - 1) - 4 * h;
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sc[kb][i] = kb * 32 + 8 * (i >> 2) + (i & 3) <= hi ? sc[kb][i] : -INFINITY;
+      if (a.window > 0) {
+        const int lo = pos - a.window - t0 - 4 * h, sk = a.sinks - t0 - 4 * h;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int kk = kb * 32 + 8 * (i >> 2) + 4 * h + (i & 3), j = t0 + kk;
-            const bool see = (kk & 15) < hv[kb * 2 + (i >> 3)] && j <= pos &&
-                             (a.window <= 0 || j > pos - a.window || j < a.sinks);
-            x[kb][i] = see ? x[kb][i] : -INFINITY;
-            vis |= see ? 1u << (kb * 16 + i) : 0u;
+            const int kk = kb * 32 + 8 * (i >> 2) + (i & 3);
+            sc[kb][i] = ((kk > lo) | (kk < sk)) ? sc[kb][i] : -INFINITY;
           }
       }
+      if (holes) {
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+        for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, x[kb][i]);
-      top = fmaxf(top, __shfl_xor(top, 32, WAVE));
-      const float mn = fmaxf(m, top), ms = mn == -INFINITY ? 0.f : mn;
-      const float al = fade(m, ms);
-      const bool any_vnan = C8 && odd_[b] == u;
-      float sum = 0.f;
-      uint4 pf[4];
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float p[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) p[i] = exp2_fast(x[kb][e * 4 + i] - ms);
-          if constexpr (C8) {
-            const f32x4 iv = *reinterpret_cast<const f32x4*>(&inv_[b][kb * 32 + 8 * e + 4 * h]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum = fmaf(p[i], iv[i], sum);
-          } else {
-            sum += (p[0] + p[1]) + (p[2] + p[3]);
+          for (int i = 0; i < 16; ++i) {
+            const int hv = kb == 0 ? (i < 8 ? hv0 : hv1) : (i < 8 ? hv2 : hv3);
+            sc[kb][i] = 8 * ((i >> 2) & 1) + (i & 3) + 4 * h < hv ? sc[kb][i] : -INFINITY;
           }
-          if (any_vnan) {                          // a V row without a scale: NaN for the rows that see it
+      }
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[kb][i]);
+    top = fmaxf(top, __shfl_xor(top, 32, WAVE));
+    if constexpr (!C8) top *= c;
+    // The maximum that weights refer to is only moved when a row's has grown by more than 2^8 (a weight of 2^8 is
+    // still far inside fp16, and relative precision does not depend on it): most tiles leave the sums alone.
+    if (__any(top > m + 8.f)) {
+      const float mn = fmaxf(m, top), f = fade(m, mn);
+      ls *= f;
+#pragma unroll
+      for (int db = 0; db < DB; ++db) o[db] *= f;
+      m = mn;
+    }
+    const float ms = m == -INFINITY ? 0.f : m;
+    uint4 pf[4];
+    const bool slow = tl.odd == u && (C8 || !full);
+    uint32_t vis = 0;
+    if (slow) {                                    // which elements are seen: bit kb * 16 + i
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) vis |= sc[kb][i] != -INFINITY ? 1u << (kb * 16 + i) : 0u;
+    }
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          p[i] = exp2_fast(C8 ? sc[kb][e * 4 + i] - ms : fmaf(sc[kb][e * 4 + i], c, -ms));
+        if constexpr (C8) {
+          const f32x4 iv = *reinterpret_cast<const f32x4*>(&tl.inv[kb * 32 + 8 * e + 4 * h]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ls = fmaf(p[i], iv[i], ls);
+          if (slow) {                              // a V row without a scale: NaN for the rows that see it
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if ((vis >> (kb * 16 + e * 4 + i) & 1) && vnan_[b][kb * 32 + 8 * e + 4 * h + i]) p[i] = __uint_as_float(0x7FC00000u);
+              if ((vis >> (kb * 16 + e * 4 + i) & 1) && tl.vnan[kb * 32 + 8 * e + 4 * h + i]) p[i] = __uint_as_float(0x7FC00000u);
           }
-          const uint32_t a0 = pack2<CB>(p[0], p[1]), a1 = pack2<CB>(p[2], p[3]);
-          if (e & 1) { pf[kb * 2 + (e >> 1)].z = a0; pf[kb * 2 + (e >> 1)].w = a1; }
-          else { pf[kb * 2 + (e >> 1)].x = a0; pf[kb * 2 + (e >> 1)].y = a1; }
+        } else {
+          ls += (p[0] + p[1]) + (p[2] + p[3]);
         }
-      ls = ls * al + sum;
-      if (__any(mn > m)) {
-#pragma unroll
-        for (int db = 0; db < DB; ++db) o[db] *= al;
+        const uint32_t a0 = pack2<CB>(p[0], p[1]), a1 = pack2<CB>(p[2], p[3]);
+        if (e & 1) { pf[kb * 2 + (e >> 1)].z = a0; pf[kb * 2 + (e >> 1)].w = a1; }
+        else { pf[kb * 2 + (e >> 1)].x = a0; pf[kb * 2 + (e >> 1)].y = a1; }
       }
-      m = mn;
-      const bool slow = !C8 && !full && odd_[b] == u;
+    if (C8 || !slow) {
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-        for (int db = 0; db < DB; ++db) {
-          const int key = kk * 16 + 4 * h + ((l & 15) >> 2);
-          const int ch = db * 4 + ((l >> 4) & 1) * 2 + ((l & 3) >> 1);
-          const int at = ((ch ^ swz_v<DP>(key)) << 4) + (l & 1) * 8;   // keys 8 apart: the same slot
-          const fp16x4 y0 = __builtin_amdgcn_ds_read_tr16_b64_v4f16(
-              (__attribute__((address_space(3))) fp16x4*)(&vt[b][key * RB + at]));
-          const fp16x4 y1 = __builtin_amdgcn_ds_read_tr16_b64_v4f16(
-              (__attribute__((address_space(3))) fp16x4*)(&vt[b][(key + 8) * RB + at]));
-          const uint2 z0 = __builtin_bit_cast(uint2, y0), z1 = __builtin_bit_cast(uint2, y1);
-          const uint4 vf = make_uint4(z0.x, z0.y, z1.x, z1.y);
-          if (!slow) {
-            o[db] = mfma32<CB>(vf, pf[kk], o[db]);
-          } else {
-            // infinities and NaN only where a row sees them (see the few-row kernel)
-            uint32_t fin[4], ind[3][4], one[4];
-            const uint32_t raw[4] = {vf.x, vf.y, vf.z, vf.w};
-            constexpr uint32_t ONE = CB ? 0x3F80u : 0x3C00u, EXP = CB ? 0x7F80u : 0x7C00u;
+        for (int db = 0; db < DB; ++db) o[db] = mfma32<CB>(v_frag(tl, kk, db), pf[kk], o[db]);
+    } else {
+      // infinities and NaN that only some rows see: left out of the products, then added key by key where they are seen
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              fin[k] = ind[0][k] = ind[1][k] = ind[2][k] = 0;
+      for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-              for (int sh = 0; sh < 32; sh += 16) {
-                const uint32_t v = (raw[k] >> sh) & 0xFFFFu;
-                fin[k] |= ((v & EXP) != EXP ? v : 0u) << sh;
-                ind[0][k] |= (v == EXP ? ONE : 0u) << sh;
-                ind[1][k] |= (v == (EXP | 0x8000u) ? ONE : 0u) << sh;
-                ind[2][k] |= ((v & 0x7FFFu) > EXP ? ONE : 0u) << sh;
-              }
-              const uint32_t vb = vis >> (kk * 8 + k * 2);
-              one[k] = (vb & 1 ? ONE : 0u) | (vb & 2 ? ONE << 16 : 0u);
-            }
-            o[db] = mfma32<CB>(make_uint4(fin[0], fin[1], fin[2], fin[3]), pf[kk], o[db]);
+        for (int db = 0; db < DB; ++db) o[db] = mfma32<CB>(finite_only<CB>(v_frag(tl, kk, db)), pf[kk], o[db]);
+      const uint32_t other = __shfl_xor(vis, 32, WAVE);
+#pragma unroll 1
+      for (int kk = 0; kk < TK; ++kk) {
+        const uint32_t owner = ((kk >> 2) & 1) == h ? vis : other;
+        const bool see = owner >> ((kk >> 5) * 16 + ((kk >> 3) & 3) * 4 + (kk & 3)) & 1;
 #pragma unroll
-            for (int kind = 0; kind < 3; ++kind) {
-              f32x16 cnt;
+        for (int db = 0; db < DB; ++db)
 #pragma unroll
-              for (int i = 0; i < 16; ++i) cnt[i] = 0.f;
-              cnt = mfma32<CB>(make_uint4(ind[kind][0], ind[kind][1], ind[kind][2], ind[kind][3]),
-                               make_uint4(one[0], one[1], one[2], one[3]), cnt);
-              const float add = __uint_as_float(kind == 0 ? 0x7F800000u : kind == 1 ? 0xFF800000u : 0x7FC00000u);
+          for (int e = 0; e < 4; ++e) {
+            const int ch = db * 4 + e;             // elements db * 32 + 8 e + 4 h ..
+            const uint2 v = *reinterpret_cast<const uint2*>(&tl.v[kk * RB + ((ch ^ swz_v<DP>(kk)) << 4) + 8 * h]);
+            if (nonfinite2<CB>(v.x) | nonfinite2<CB>(v.y)) {
+              const float f[4] = {lo16<CB>(v.x), hi16<CB>(v.x), lo16<CB>(v.y), hi16<CB>(v.y)};
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[db][i] += cnt[i] > 0.f ? add : 0.f;
+              for (int i = 0; i < 4; ++i) o[db][e * 4 + i] += see && !(fabsf(f[i]) < INFINITY) ? f[i] : 0.f;
             }
           }
-        }
+      }
     }
-    if (u + 1 < u1) store(b ^ 1, un.key0(u + 1, MANY_USH), u + 1);
+  };
+  // 16-bit tiles that some row may see only in part are looked through for infinities and NaN by one wave each
+  auto look = [&](Tile<DP, C8>& tl, int u, int t0) {
+    const bool inside = t0 + TK - 1 <= b_lo && (a.window <= 0 || t0 > b_hi - a.window || t0 + TK <= a.sinks) &&
+                        tl.have[0] + tl.have[1] + tl.have[2] + tl.have[3] == TK;
+    if (C8 || inside) return;                      // the same in every wave
+    uint32_t odd = 0;
+#pragma unroll
+    for (int i = 0; i < LD; ++i) {
+      const uint4 v = *reinterpret_cast<const uint4*>(&tl.v[(w * 16 + i * RPI) * RB + l * 16]);
+      odd |= nonfinite2<CB>(v.x) | nonfinite2<CB>(v.y) | nonfinite2<CB>(v.z) | nonfinite2<CB>(v.w);
+    }
+    if (odd) tl.odd = u;
+    __syncthreads();
+  };
+
+  if (u0 < u1) {
+    const int t0 = un.key0(u0, MANY_USH);
+    fetch(tile0, t0, page_of(t0));
+    store(tile0, u0);
+  }
+  int page = u0 + 1 < u1 ? page_of(un.key0(u0 + 1, MANY_USH)) : 0;
+  auto step = [&](Tile<DP, C8>& cur, Tile<DP, C8>& nxt, int u) {
+    const int t0 = un.key0(u, MANY_USH);
+    __syncthreads();                               // cur has arrived, nxt is free
+    if (u + 1 < u1) {
+      fetch(nxt, un.key0(u + 1, MANY_USH), page);
+      if (u + 2 < u1) page = page_of(un.key0(u + 2, MANY_USH));
+    }
+    look(cur, u, t0);
+    if (wave_on && t0 <= p_hi) work(cur, u, t0);
+    if (u + 1 < u1) store(nxt, u + 1);
+  };
+  for (int u = u0; u < u1; u += 2) {
+    step(tile0, tile1, u);
+    if (u + 1 < u1) step(tile1, tile0, u + 1);
   }
 
   if (!wave_on) return;
