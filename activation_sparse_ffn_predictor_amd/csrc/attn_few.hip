@@ -22,7 +22,7 @@ __device__ __forceinline__ int few_swz(int key, bool codes) {
 // KVM 0: cache of the query's 16-bit type, 1: int8, 2: e4m3 (both computed in fp16: codes are exact there, and bf16
 // queries are scaled by one power of two into fp16's range). DP: head size padded to 64, 128 or 256. QB: 16-row tiles.
 template <bool BF, int KVM, int DP, int QB>
-__global__ __launch_bounds__(NT) void k_attn_few(AttnArgs a) {
+__global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_few(AttnArgs a) {
   constexpr bool C8 = KVM != 0, CB = BF && !C8;
   constexpr int EB = C8 ? 1 : 2, RB = DP * EB, KS = DP / 32, DB = DP / 16, CPR = RB / 16;   // chunks a row
   constexpr int KL = RB / 64;                      // 16-byte K loads of a lane per 16 keys
@@ -56,35 +56,20 @@ __global__ __launch_bounds__(NT) void k_attn_few(AttnArgs a) {
     for (int ks = 0; ks < KS; ++ks) {
       const int ch = C8 ? ((ks >> 1) * 4 + g4) * 2 + (ks & 1) : ks * 4 + g4;
       qf[qb][ks] = r < rows && ch * 8 < d ? *reinterpret_cast<const uint4*>(qp + ch * 16) : make_uint4(0, 0, 0, 0);
+      if (a.neg) qf[qb][ks] = flip_signs(qf[qb][ks]);
     }
   }
   if constexpr (C8 && BF) {
-    // bf16 queries into fp16: times one power of two that takes the largest to 2^15 (exact but for elements below
-    // 2^-29 of it, which lose bits under 2^-40 of it)
     float big = 0.f;
 #pragma unroll
     for (int qb = 0; qb < QB; ++qb)
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const uint32_t u[4] = {qf[qb][ks].x, qf[qb][ks].y, qf[qb][ks].z, qf[qb][ks].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) big = fmaxf(big, fmaxf(fabsf(lo16<true>(u[k])), fabsf(hi16<true>(u[k]))));
-      }
-    big = wave_max(big);
-    const int e = big > 0.f && big < 3.4e38f ? 14 - ((int)((__float_as_uint(big) >> 23) & 255) - 127) : 0;
-    const int e1 = min(max(e, -126), 126);
-    const float up = __uint_as_float((uint32_t)(e1 + 127) << 23);
-    c = c * __uint_as_float((uint32_t)(127 - e1) << 23);
+      for (int ks = 0; ks < KS; ++ks) big = fmaxf(big, absmax8<true>(qf[qb][ks]));
+    const float up = to_f16_range(wave_max(big), c);
 #pragma unroll
     for (int qb = 0; qb < QB; ++qb)
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const uint4 t = qf[qb][ks];
-        qf[qb][ks] = make_uint4(pack2<false>(lo16<true>(t.x) * up, hi16<true>(t.x) * up),
-                                pack2<false>(lo16<true>(t.y) * up, hi16<true>(t.y) * up),
-                                pack2<false>(lo16<true>(t.z) * up, hi16<true>(t.z) * up),
-                                pack2<false>(lo16<true>(t.w) * up, hi16<true>(t.w) * up));
-      }
+      for (int ks = 0; ks < KS; ++ks) qf[qb][ks] = bf16_to_f16(qf[qb][ks], up);
   }
 
   float m[QB], ls[QB];
@@ -100,16 +85,20 @@ __global__ __launch_bounds__(NT) void k_attn_few(AttnArgs a) {
   const int* trow = a.sq.table + (long)s * a.sq.ldt;
   const uint32_t dB = (uint32_t)d * EB;
 
-  for (int u = split * per + w; u < u1; u += NW) {
+  // One unit's loads. 16 keys share a page; what does not exist (behind the sequence, a bad page) reads as zeros.
+  uint4 kr[2][KL], vr[2][VL];
+  float4 ksc[2], vsc[2];
+  int have[2], page[2];                            // keys of each 16 that exist; page ids of the next unit to load
+  auto pages = [&](int u) {
     const int t0 = un.key0(u, FEW_USH);
-    uint4 kr[2][KL], vr[2][VL];
-    float4 ksc[2], vsc[2];
-    int have[2];                                   // keys of each 16 that exist
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) page[kb] = trow[min((t0 + kb * 16) >> a.kv.psh, a.sq.cols - 1)];
+  };
+  auto load = [&](int u) {
+    const int t0 = un.key0(u, FEW_USH);
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      // 16 keys share a page; what does not exist (behind the sequence, a bad page) reads as zeros
-      const int t = t0 + kb * 16, pg = t >> a.kv.psh;
-      const int pid = __builtin_amdgcn_readfirstlane(trow[min(pg, a.sq.cols - 1)]);
+      const int t = t0 + kb * 16, pid = __builtin_amdgcn_readfirstlane(page[kb]);
       have[kb] = (unsigned)pid < (unsigned)a.kv.n_pages ? min(16, max(0, sq.len - t)) : 0;
       const long r = (((long)(have[kb] ? pid : 0) * a.kv.hkv + hk) << a.kv.psh) + (t & ((1 << a.kv.psh) - 1));
       const Buf bk(a.kv.k + r * dB, have[kb] * dB), bv(a.kv.v + r * dB, have[kb] * dB);
@@ -129,7 +118,19 @@ __global__ __launch_bounds__(NT) void k_attn_few(AttnArgs a) {
         vsc[kb] = sv.ldf4(g4 * 16);
       }
     }
-    // scores
+  };
+
+  int u = split * per + w;
+  if (u < u1) {
+    pages(u);
+    load(u);
+    if (u + NW < u1) pages(u + NW);
+  }
+  for (; u < u1; u += NW) {
+    const int t0 = un.key0(u, FEW_USH), h0 = have[0], h1 = have[1];
+    // every key of the unit visible to every row?
+    const bool full = h0 + h1 == 32 && t0 + 31 <= p0 && (a.window <= 0 || t0 > p1 - a.window || t0 + 32 <= a.sinks);
+    // scores: element (kb, i) is key kb * 16 + 4 * g4 + i of row ql
     f32x4 sc[QB][2];
 #pragma unroll
     for (int qb = 0; qb < QB; ++qb)
@@ -154,81 +155,6 @@ __global__ __launch_bounds__(NT) void k_attn_few(AttnArgs a) {
           for (int qb = 0; qb < QB; ++qb) sc[qb][kb] = mfma16<CB>(kr[kb][i], qf[qb][i], sc[qb][kb]);
         }
       }
-    // every key of the unit visible to every row?
-    const bool full = have[0] + have[1] == 32 && t0 + 31 <= p0 &&
-                      (a.window <= 0 || t0 > p1 - a.window || t0 + 32 <= a.sinks);
-    uint4 pf[QB];
-    uint32_t vis[QB];                              // bit kb * 4 + i: key kb * 16 + g4 * 4 + i is visible to row ql
-    float lg[2][4], inv[2][4], kf[2][4];
-    uint32_t vnan = 0;                             // as vis: the key's V row has no scale
-    if constexpr (C8) {
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        const float ka[4] = {ksc[kb].x, ksc[kb].y, ksc[kb].z, ksc[kb].w};
-        const float va[4] = {vsc[kb].x, vsc[kb].y, vsc[kb].z, vsc[kb].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const VScale v = v_scale(va[i]);
-          kf[kb][i] = ka[i] * c;
-          lg[kb][i] = v.lg;
-          inv[kb][i] = v.inv;
-          vnan |= va[i] != va[i] ? 1u << (kb * 4 + i) : 0u;
-        }
-      }
-    }
-    const bool any_vnan = C8 && __any(vnan != 0);
-#pragma unroll
-    for (int qb = 0; qb < QB; ++qb) {
-      float x[2][4], top = -INFINITY;
-      vis[qb] = 255u;
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          x[kb][i] = C8 ? fmaf(sc[qb][kb][i], kf[kb][i], lg[kb][i]) : sc[qb][kb][i] * c;
-      if (!full) {
-        vis[qb] = 0;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int kk = g4 * 4 + i, j = t0 + kb * 16 + kk;
-            const bool see = kk < have[kb] && j <= pos[qb] && (a.window <= 0 || j > pos[qb] - a.window || j < a.sinks);
-            x[kb][i] = see ? x[kb][i] : -INFINITY;
-            vis[qb] |= see ? 1u << (kb * 4 + i) : 0u;
-          }
-      }
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, x[kb][i]);
-      top = fmaxf(top, __shfl_xor(top, 16, WAVE));
-      top = fmaxf(top, __shfl_xor(top, 32, WAVE));
-      const float mn = fmaxf(m[qb], top), ms = mn == -INFINITY ? 0.f : mn;
-      const float al = fade(m[qb], ms);
-      float p[2][4], sum = 0.f;
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p[kb][i] = exp2_fast(x[kb][i] - ms);
-          sum = C8 ? fmaf(p[kb][i], inv[kb][i], sum) : sum + p[kb][i];
-        }
-      ls[qb] = ls[qb] * al + sum;
-      if (__any(mn > m[qb])) {
-#pragma unroll
-        for (int db = 0; db < DB; ++db) o[qb][db] *= al;
-      }
-      m[qb] = mn;
-      if (C8 && any_vnan) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if ((vnan & vis[qb]) >> e & 1) p[e >> 2][e & 3] = __uint_as_float(0x7FC00000u);
-      }
-      // weights of one rounding (half a step of the type each) enter the second product
-      pf[qb] = make_uint4(pack2<CB>(p[0][0], p[0][1]), pack2<CB>(p[0][2], p[0][3]), pack2<CB>(p[1][0], p[1][1]),
-                          pack2<CB>(p[1][2], p[1][3]));
-    }
     // V through the wave's own LDS tile (the LDS pipe keeps a wave's accesses in order)
     bool odd = false;                              // an infinity or NaN in a unit that some row sees only in part
 #pragma unroll
@@ -242,17 +168,98 @@ __global__ __launch_bounds__(NT) void k_attn_few(AttnArgs a) {
           odd |= (nonfinite2<CB>(t.x) | nonfinite2<CB>(t.y) | nonfinite2<CB>(t.z) | nonfinite2<CB>(t.w)) != 0;
         }
       }
-    asm volatile("" ::: "memory");
-    const bool slow = !C8 && !full && __any(odd);
+    f32x4 inv[2];
+    uint32_t vnan = 0;                             // bit kb * 4 + i: the key's V row has no scale
+    if constexpr (C8) {
 #pragma unroll
-    for (int db = 0; db < DB; ++db) {
-      uint4 vf;
+      for (int kb = 0; kb < 2; ++kb) {
+        const float ka[4] = {ksc[kb].x, ksc[kb].y, ksc[kb].z, ksc[kb].w};
+        const float va[4] = {vsc[kb].x, vsc[kb].y, vsc[kb].z, vsc[kb].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const VScale v = v_scale(va[i]);
+          inv[kb][i] = v.inv;
+          vnan |= va[i] != va[i] ? 1u << (kb * 4 + i) : 0u;
+          const float kf = ka[i] * c;
+#pragma unroll
+          for (int qb = 0; qb < QB; ++qb) sc[qb][kb][i] = fmaf(sc[qb][kb][i], kf, v.lg);
+        }
+      }
+    }
+    // the next unit's loads run under the rest of this one
+    if (u + NW < u1) {
+      load(u + NW);
+      if (u + 2 * NW < u1) pages(u + 2 * NW);
+    }
+    const bool slow = C8 ? __any(vnan != 0) : !full && __any(odd);
+    uint4 pf[QB];
+    uint32_t vis[QB];
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb) {
+      if (!full) {
+        const int hi = pos[qb] - t0 - 4 * g4;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool see = (kb * 16 + i <= hi) & (4 * g4 + i < (kb ? h1 : h0));
+            sc[qb][kb][i] = see ? sc[qb][kb][i] : -INFINITY;
+          }
+        if (a.window > 0) {
+          const int lo = hi - a.window, sk = a.sinks - t0 - 4 * g4;
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              sc[qb][kb][i] = ((kb * 16 + i > lo) | (kb * 16 + i < sk)) ? sc[qb][kb][i] : -INFINITY;
+        }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[qb][kb][i]);
+      top = fmaxf(top, __shfl_xor(top, 16, WAVE));
+      top = fmaxf(top, __shfl_xor(top, 32, WAVE));
+      if constexpr (!C8) top *= c;
+      // the maximum that weights refer to moves only when a row's has grown by more than 2^8 (see the tile kernel)
+      if (__any(top > m[qb] + 8.f)) {
+        const float mn = fmaxf(m[qb], top), f = fade(m[qb], mn);
+        ls[qb] *= f;
+#pragma unroll
+        for (int db = 0; db < DB; ++db) o[qb][db] *= f;
+        m[qb] = mn;
+      }
+      const float ms = m[qb] == -INFINITY ? 0.f : m[qb];
+      float p[2][4];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[kb][i] = exp2_fast(C8 ? sc[qb][kb][i] - ms : fmaf(sc[qb][kb][i], c, -ms));
+          ls[qb] = C8 ? fmaf(p[kb][i], inv[kb][i], ls[qb]) : ls[qb] + p[kb][i];
+        }
+      vis[qb] = 0;
+      if (slow) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const bool see = sc[qb][e >> 2][e & 3] != -INFINITY;
+          vis[qb] |= see ? 1u << e : 0u;
+          if (C8 && see && (vnan >> e & 1)) p[e >> 2][e & 3] = __uint_as_float(0x7FC00000u);
+        }
+      }
+      // weights of one rounding (half a step of the type each) enter the second product
+      pf[qb] = make_uint4(pack2<CB>(p[0][0], p[0][1]), pack2<CB>(p[0][2], p[0][3]), pack2<CB>(p[1][0], p[1][1]),
+                          pack2<CB>(p[1][2], p[1][3]));
+    }
+    asm volatile("" ::: "memory");
+    auto v_frag = [&](int db) {
       if constexpr (C8) {
         const int j = ql >> 1, key = (j < 4 ? 0 : 12) + g4 * 4 + j;   // rows 0-3: keys g4*4.., 4-7: 16 + g4*4..
         const i32x2 t = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)(
             vt + key * RB + ((db ^ few_swz<RB>(key, true)) << 4) + (ql & 1) * 8));
         const uint2 x0 = codes4<KVM == 2>((uint32_t)t.x), x1 = codes4<KVM == 2>((uint32_t)t.y);
-        vf = make_uint4(x0.x, x0.y, x1.x, x1.y);
+        return make_uint4(x0.x, x0.y, x1.x, x1.y);
       } else {
         const int key = g4 * 4 + (ql >> 2), ch = db * 2 + ((ql & 3) >> 1);
         const int at = ((ch ^ few_swz<RB>(key, false)) << 4) + (ql & 1) * 8;   // keys 16 apart: the same slot
@@ -261,43 +268,40 @@ __global__ __launch_bounds__(NT) void k_attn_few(AttnArgs a) {
         const fp16x4 t1v = __builtin_amdgcn_ds_read_tr16_b64_v4f16(
             (__attribute__((address_space(3))) fp16x4*)(vt + (key + 16) * RB + at));
         const uint2 y0 = __builtin_bit_cast(uint2, t0v), y1 = __builtin_bit_cast(uint2, t1v);
-        vf = make_uint4(y0.x, y0.y, y1.x, y1.y);
+        return make_uint4(y0.x, y0.y, y1.x, y1.y);
       }
-      if (!slow) {
+    };
+    if (C8 || !slow) {
+#pragma unroll
+      for (int db = 0; db < DB; ++db) {
+        const uint4 vf = v_frag(db);
 #pragma unroll
         for (int qb = 0; qb < QB; ++qb) o[qb][db] = mfma16<CB>(vf, pf[qb], o[qb][db]);
-      } else {
-        // finite values as usual; infinities and NaN only where a row sees them: counted by products of 0 / 1
-        // operands, one for each kind, and added to the rows whose count is not 0
-        uint32_t fin[4], ind[3][4];
-        const uint32_t raw[4] = {vf.x, vf.y, vf.z, vf.w};
-        constexpr uint32_t ONE = CB ? 0x3F80u : 0x3C00u, EXP = CB ? 0x7F80u : 0x7C00u;
+      }
+    } else {
+      // infinities and NaN that only some rows see: left out of the products, then added key by key where they are seen
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          fin[k] = ind[0][k] = ind[1][k] = ind[2][k] = 0;
+      for (int db = 0; db < DB; ++db) {
+        const uint4 vf = finite_only<CB>(v_frag(db));
 #pragma unroll
-          for (int sh = 0; sh < 32; sh += 16) {
-            const uint32_t v = (raw[k] >> sh) & 0xFFFFu;
-            fin[k] |= ((v & EXP) != EXP ? v : 0u) << sh;
-            ind[0][k] |= (v == EXP ? ONE : 0u) << sh;
-            ind[1][k] |= (v == (EXP | 0x8000u) ? ONE : 0u) << sh;
-            ind[2][k] |= ((v & 0x7FFFu) > EXP ? ONE : 0u) << sh;
-          }
-        }
+        for (int qb = 0; qb < QB; ++qb) o[qb][db] = mfma16<CB>(vf, pf[qb], o[qb][db]);
+      }
+#pragma unroll 1
+      for (int kk = 0; kk < 32; ++kk) {
+        bool see[QB];
 #pragma unroll
-        for (int qb = 0; qb < QB; ++qb) {
-          uint32_t one[4];
+        for (int qb = 0; qb < QB; ++qb)            // the lane of this row that holds the key's score
+          see[qb] = __shfl((int)vis[qb], ((kk >> 2) & 3) * 16 + ql, WAVE) >> ((kk >> 4) * 4 + (kk & 3)) & 1;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            one[k] = ((vis[qb] >> (2 * k)) & 1 ? ONE : 0u) | ((vis[qb] >> (2 * k + 1)) & 1 ? ONE << 16 : 0u);
-          o[qb][db] = mfma16<CB>(make_uint4(fin[0], fin[1], fin[2], fin[3]), pf[qb], o[qb][db]);
+        for (int db = 0; db < DB; ++db) {          // elements db * 16 + 4 * g4 ..
+          const int ch = db * 2 + (g4 >> 1);
+          const uint2 v = *reinterpret_cast<const uint2*>(vt + kk * RB + ((ch ^ few_swz<RB>(kk, false)) << 4) + (g4 & 1) * 8);
+          if (nonfinite2<CB>(v.x) | nonfinite2<CB>(v.y)) {
+            const float f[4] = {lo16<CB>(v.x), hi16<CB>(v.x), lo16<CB>(v.y), hi16<CB>(v.y)};
 #pragma unroll
-          for (int kind = 0; kind < 3; ++kind) {
-            const f32x4 cnt = mfma16<CB>(make_uint4(ind[kind][0], ind[kind][1], ind[kind][2], ind[kind][3]),
-                                         make_uint4(one[0], one[1], one[2], one[3]), f32x4{0.f, 0.f, 0.f, 0.f});
-            const float add = __uint_as_float(kind == 0 ? 0x7F800000u : kind == 1 ? 0xFF800000u : 0x7FC00000u);
+            for (int qb = 0; qb < QB; ++qb)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[qb][db][i] += cnt[i] > 0.f ? add : 0.f;
+              for (int i = 0; i < 4; ++i) o[qb][db][i] += see[qb] && !(fabsf(f[i]) < INFINITY) ? f[i] : 0.f;
           }
         }
       }
@@ -357,13 +361,13 @@ __global__ __launch_bounds__(NT) void k_attn_few(AttnArgs a) {
 
 }  // namespace
 
-int sffn_attn_few_rows(int d) { return d <= 128 ? 32 : 16; }
+int sffn_attn_few_rows(int d) { return d <= 64 ? 64 : d <= 128 ? 32 : 16; }
 
 hipError_t sffn_launch_attn_few(const AttnArgs& a, int qt, int kvt, hipStream_t st) {
   const dim3 grid(a.ns, a.kv.hkv, a.sq.S);
   const bool bf = qt == T_BF16;
   const int kvm = kvt == T_I8 ? 1 : kvt == T_E4M3 ? 2 : 0;
-  const bool two = a.max_q * a.G > 16;
+  const int rows = a.max_q * a.G;
 #define GO(BF, KVM, DP, QB) hipLaunchKernelGGL((k_attn_few<BF, KVM, DP, QB>), grid, dim3(NT), 0, st, a)
 #define TYPES(DP, QB)                                                                        \
   if (bf) {                                                                                  \
@@ -371,8 +375,8 @@ hipError_t sffn_launch_attn_few(const AttnArgs& a, int qt, int kvt, hipStream_t 
   } else {                                                                                   \
     if (kvm == 0) GO(false, 0, DP, QB); else if (kvm == 1) GO(false, 1, DP, QB); else GO(false, 2, DP, QB); \
   }
-  if (a.kv.d <= 64) { if (two) { TYPES(64, 2) } else { TYPES(64, 1) } }
-  else if (a.kv.d <= 128) { if (two) { TYPES(128, 2) } else { TYPES(128, 1) } }
+  if (a.kv.d <= 64) { if (rows > 32) { TYPES(64, 4) } else if (rows > 16) { TYPES(64, 2) } else { TYPES(64, 1) } }
+  else if (a.kv.d <= 128) { if (rows > 16) { TYPES(128, 2) } else { TYPES(128, 1) } }
   else { TYPES(256, 1) }
 #undef TYPES
 #undef GO

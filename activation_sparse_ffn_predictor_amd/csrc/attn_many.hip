@@ -299,11 +299,6 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
           const f32x4 iv = *reinterpret_cast<const f32x4*>(&tl.inv[kb * 32 + 8 * e + 4 * h]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) ls = fmaf(p[i], iv[i], ls);
-          if (slow) {                              // a V row without a scale: NaN for the rows that see it
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if ((vis >> (kb * 16 + e * 4 + i) & 1) && tl.vnan[kb * 32 + 8 * e + 4 * h + i]) p[i] = __uint_as_float(0x7FC00000u);
-          }
         } else {
           ls += (p[0] + p[1]) + (p[2] + p[3]);
         }
@@ -311,6 +306,22 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
         if (e & 1) { pf[kb * 2 + (e >> 1)].z = a0; pf[kb * 2 + (e >> 1)].w = a1; }
         else { pf[kb * 2 + (e >> 1)].x = a0; pf[kb * 2 + (e >> 1)].y = a1; }
       }
+    if (C8 && slow) {                              // a V row without a scale: NaN for the rows that see it
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        uint32_t nan[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          nan[k] = 0;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int e = kk * 8 + k * 2 + j;      // element kb * 16 + i
+            if ((vis >> e & 1) && tl.vnan[(e >> 4) * 32 + 8 * ((e >> 2) & 3) + 4 * h + (e & 3)]) nan[k] |= 0x7E00u << (16 * j);
+          }
+        }
+        pf[kk] = make_uint4(pf[kk].x | nan[0], pf[kk].y | nan[1], pf[kk].z | nan[2], pf[kk].w | nan[3]);
+      }
+    }
     if (C8 || !slow) {
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)

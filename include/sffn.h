@@ -285,7 +285,7 @@ int sffn_kv_read(sffn_kv cache, sffn_seqs seqs, int type, void* k, int64_t k_str
  * product as 16-bit values, and 8-bit codes enter both products exactly.
  * max_q: at least the largest number of new tokens of one sequence (tokens past it are not computed and their rows
  * stay as they were). max_kv: about the largest kv_len; it decides only over how many workgroups a sequence's keys
- * are spread. Up to 32 rows max_q * Hq / n_kv_heads (16 for head_dim > 128) run the few-row kernel
+ * are spread. Up to 32 rows max_q * Hq / n_kv_heads (64 for head_dim <= 64, 16 for head_dim > 128) run the few-row kernel
  * (SFFN_ATTN_FEW), more run the tile kernel (SFFN_ATTN_MANY); where keys are spread a second kernel joins the parts
  * in a fixed order, so the same call gives the same bits. The workspace needs sffn_attn_workspace_size bytes of
  * the same sizes (0: none needed, ws may be NULL); it holds nothing between calls, and calls that overlap in time
