@@ -99,8 +99,11 @@ struct AttnArgs {
   float2* pml;              // their maxima (log2 domain) and sums [T * hq][ns]
 };
 
-constexpr int FEW_USH = 5, FEW_LEAST = 8;       // few-row kernel: units of 32 keys, at least 8 of them a share
+// few-row kernel: units of 32 keys; a share has at least FEW_LEAST of them and a multiple of FEW_STEP
+constexpr int FEW_USH = 5, FEW_LEAST = 16, FEW_STEP = 4;
+// tile kernel: units of 64 keys, 128 rows
 constexpr int MANY_USH = 6, MANY_LEAST = 4, MANY_ROWS = 128;
+constexpr int MAX_SHARES = 64;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -223,6 +226,21 @@ __device__ __forceinline__ float fade(float m, float to) {
 // natural logarithm of L * 2^M (-infinity for a row without visible keys)
 __device__ __forceinline__ float log_sum(float M, float L) {
   return L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * 0.6931471805599453f;
+}
+
+// v of this lane and of the one 32 (16) lanes away, combined: lanes of both halves (of neighbouring rows of 16) change
+// places in registers, without the LDS crossbar
+template <bool MAX>
+__device__ __forceinline__ float over32(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  const float a = __uint_as_float(r[0]), b = __uint_as_float(r[1]);
+  return MAX ? fmaxf(a, b) : a + b;
+}
+template <bool MAX>
+__device__ __forceinline__ float over16(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  const float a = __uint_as_float(r[0]), b = __uint_as_float(r[1]);
+  return MAX ? fmaxf(a, b) : a + b;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }

@@ -85,8 +85,8 @@ int shares(int T, int S, int Hkv, int G, int d, int max_q, int max_kv, int windo
   const int unit = few ? 1 << sffn::FEW_USH : 1 << sffn::MANY_USH, least = few ? sffn::FEW_LEAST : sffn::MANY_LEAST;
   const int64_t most = std::max<int64_t>(1, (see + (int64_t)unit * least - 1) / ((int64_t)unit * least));
   const int64_t blocks = (few ? (int64_t)S : (int64_t)T * G / sffn::MANY_ROWS + std::min(S, T)) * Hkv;
-  const int64_t want = few ? 1024 : 512;
-  return (int)std::min<int64_t>({(want + blocks - 1) / std::max<int64_t>(1, blocks), most, 64});
+    const int64_t want = few ? 2048 : 512;
+  return (int)std::min<int64_t>({(want + blocks - 1) / std::max<int64_t>(1, blocks), most, sffn::MAX_SHARES});
 }
 size_t po_bytes(int T, int Hq, int d, int ns) { return align256((size_t)T * Hq * ns * d * sizeof(float)); }
 

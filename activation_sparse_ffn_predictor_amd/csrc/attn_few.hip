@@ -9,8 +9,6 @@ using namespace sffn;
 
 namespace {
 
-constexpr int NT = 256, NW = 4;
-
 // A 16-byte slot of V's tile in LDS: key's 16-byte chunk c goes to slot c ^ few_swz(key), so that the 16 (32) rows
 // that a transposing read touches at one column spread over the banks.
 template <int RB>   // bytes of a tile row
@@ -21,27 +19,26 @@ __device__ __forceinline__ int few_swz(int key, bool codes) {
 
 // KVM 0: cache of the query's 16-bit type, 1: int8, 2: e4m3 (both computed in fp16: codes are exact there, and bf16
 // queries are scaled by one power of two into fp16's range). DP: head size padded to 64, 128 or 256. QB: 16-row tiles.
-template <bool BF, int KVM, int DP, int QB>
-__global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_few(AttnArgs a) {
+// The sequence and share of a block.
+struct Place {
+  Seq sq;
+  Units un;
+  int n, rows, p0, p1, hk, s, split, used, u0, u1;
+};
+
+template <bool BF, int KVM, int DP, int QB, int NW>
+__device__ __forceinline__ void few_rows(const AttnArgs& a, const Place& pl, char* lds, float (*mlw)[2], uint4* qlds) {
+  constexpr int NT = NW * 64;
   constexpr bool C8 = KVM != 0, CB = BF && !C8;
   constexpr int EB = C8 ? 1 : 2, RB = DP * EB, KS = DP / 32, DB = DP / 16, CPR = RB / 16;   // chunks a row
   constexpr int KL = RB / 64;                      // 16-byte K loads of a lane per 16 keys
   constexpr int RPI = 64 / CPR, VL = 16 / RPI;     // V rows a load instruction covers; V loads per 16 keys
   constexpr int VT = 32 * RB, OS = DP + 4;         // V tile of a wave; row stride of the merge (floats)
-  constexpr int LDS = NW * VT > NW * QB * 16 * OS * 4 ? NW * VT : NW * QB * 16 * OS * 4;
-  __shared__ __align__(16) char lds[LDS];
-  __shared__ float mlw[NW][QB * 16][2];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, g4 = l >> 4, ql = l & 15;
-  const int hk = blockIdx.y, s = blockIdx.z, d = a.kv.d, G = a.G;
-  const Seq sq = load_seq(a.sq, s, a.kv.psh);
-  const int n = min(sq.n, a.max_q), rows = n * G;
-  if (rows == 0) return;
-  const int p0 = sq.len - sq.n, p1 = p0 + n - 1;   // positions of the first and last new token
-  const Units un = key_units(p0, p1, sq.len, a.window, a.sinks, FEW_USH);
-  const int per = share_units(un.tot, a.ns, FEW_LEAST, NW), used = max(1, (un.tot + per - 1) / per);
-  const int split = blockIdx.x;
-  if (split >= used) return;
-  const int u1 = min(un.tot, (split + 1) * per);
+  const int d = a.kv.d, G = a.G, hk = pl.hk, s = pl.s, rows = pl.rows, p0 = pl.p0, p1 = pl.p1, used = pl.used;
+  const int split = pl.split, u1 = pl.u1;
+  const Seq sq = pl.sq;
+  const Units un = pl.un;
 
   // queries: 8 consecutive elements of row ql per product step
   uint4 qf[QB][KS];
@@ -71,6 +68,20 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_few(AttnArgs a) 
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) qf[qb][ks] = bf16_to_f16(qf[qb][ks], up);
   }
+
+  // Many rows: the query operands (the same in every wave) wait in LDS, 16 bytes a lane, instead of registers. Kept in
+  // registers they are spilled, and a spilled value's load waits for the cache loads in flight before it.
+  constexpr bool QL = QB * DP >= 256 && QB > 1;
+  if constexpr (QL) {
+    if (w == 0) {
+#pragma unroll
+      for (int qb = 0; qb < QB; ++qb)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) qlds[(qb * KS + ks) * 64 + l] = qf[qb][ks];
+    }
+    __syncthreads();
+  }
+  auto q_frag = [&](int qb, int ks) { return QL ? qlds[(qb * KS + ks) * 64 + l] : qf[qb][ks]; };
 
   float m[QB], ls[QB];
   f32x4 o[QB][DB];
@@ -120,7 +131,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_few(AttnArgs a) 
     }
   };
 
-  int u = split * per + w;
+  int u = pl.u0 + w;
   if (u < u1) {
     pages(u);
     load(u);
@@ -137,9 +148,9 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_few(AttnArgs a) 
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) sc[qb][kb] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int i = 0; i < KL; ++i)
 #pragma unroll
-      for (int i = 0; i < KL; ++i) {
+      for (int kb = 0; kb < 2; ++kb) {
         if constexpr (C8) {
           const uint4 t = kr[kb][i];
           const uint2 x0 = codes4<KVM == 2>(t.x), x1 = codes4<KVM == 2>(t.y), x2 = codes4<KVM == 2>(t.z),
@@ -147,12 +158,12 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_few(AttnArgs a) 
           const uint4 ka = make_uint4(x0.x, x0.y, x1.x, x1.y), kc = make_uint4(x2.x, x2.y, x3.x, x3.y);
 #pragma unroll
           for (int qb = 0; qb < QB; ++qb) {
-            sc[qb][kb] = mfma16<false>(ka, qf[qb][2 * i], sc[qb][kb]);
-            sc[qb][kb] = mfma16<false>(kc, qf[qb][2 * i + 1], sc[qb][kb]);
+            sc[qb][kb] = mfma16<false>(ka, q_frag(qb, 2 * i), sc[qb][kb]);
+            sc[qb][kb] = mfma16<false>(kc, q_frag(qb, 2 * i + 1), sc[qb][kb]);
           }
         } else {
 #pragma unroll
-          for (int qb = 0; qb < QB; ++qb) sc[qb][kb] = mfma16<CB>(kr[kb][i], qf[qb][i], sc[qb][kb]);
+          for (int qb = 0; qb < QB; ++qb) sc[qb][kb] = mfma16<CB>(kr[kb][i], q_frag(qb, i), sc[qb][kb]);
         }
       }
     // V through the wave's own LDS tile (the LDS pipe keeps a wave's accesses in order)
@@ -219,8 +230,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_few(AttnArgs a) 
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[qb][kb][i]);
-      top = fmaxf(top, __shfl_xor(top, 16, WAVE));
-      top = fmaxf(top, __shfl_xor(top, 32, WAVE));
+      top = over32<true>(over16<true>(top));
       if constexpr (!C8) top *= c;
       // the maximum that weights refer to moves only when a row's has grown by more than 2^8 (see the tile kernel)
       if (__any(top > m[qb] + 8.f)) {
@@ -251,6 +261,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_few(AttnArgs a) 
       // weights of one rounding (half a step of the type each) enter the second product
       pf[qb] = make_uint4(pack2<CB>(p[0][0], p[0][1]), pack2<CB>(p[0][2], p[0][3]), pack2<CB>(p[1][0], p[1][1]),
                           pack2<CB>(p[1][2], p[1][3]));
+      if (QL) __builtin_amdgcn_sched_barrier(0);   // one row tile after the other: registers are short
     }
     asm volatile("" ::: "memory");
     auto v_frag = [&](int db) {
@@ -314,12 +325,10 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_few(AttnArgs a) 
   float* om = reinterpret_cast<float*>(lds);
 #pragma unroll
   for (int qb = 0; qb < QB; ++qb) {
-    float t = ls[qb];
-    t += __shfl_xor(t, 16, WAVE);
-    t += __shfl_xor(t, 32, WAVE);
+    const float t = over32<false>(over16<false>(ls[qb]));
     if (g4 == 0) {
-      mlw[w][qb * 16 + ql][0] = m[qb];
-      mlw[w][qb * 16 + ql][1] = t;
+      mlw[w * QB * 16 + qb * 16 + ql][0] = m[qb];
+      mlw[w * QB * 16 + qb * 16 + ql][1] = t;
     }
 #pragma unroll
     for (int db = 0; db < DB; ++db)
@@ -331,12 +340,12 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_few(AttnArgs a) 
     if (d0 >= d) continue;
     float M = -INFINITY, L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < NW; ++k) M = fmaxf(M, mlw[k][r][0]);
+    for (int k = 0; k < NW; ++k) M = fmaxf(M, mlw[k * QB * 16 + r][0]);
     const float ms = M == -INFINITY ? 0.f : M;
 #pragma unroll
     for (int k = 0; k < NW; ++k) {
-      const float f = fade(mlw[k][r][0], ms);
-      L = fmaf(mlw[k][r][1], f, L);
+      const float f = fade(mlw[k * QB * 16 + r][0], ms);
+      L = fmaf(mlw[k * QB * 16 + r][1], f, L);
       const float* src = om + ((k * QB) * 16 + r) * OS + d0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] = fmaf(src[j], f, acc[j]);
@@ -359,6 +368,34 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_few(AttnArgs a) 
   }
 }
 
+// One sequence, K/V head and share of the keys; a sequence with fewer rows than the call's most takes fewer tiles.
+template <bool BF, int KVM, int DP, int QB, int NW>
+__global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void k_attn_few(AttnArgs a) {
+  constexpr int VT = NW * 32 * DP * (KVM ? 1 : 2), MG = NW * QB * 16 * (DP + 4) * 4;
+  __shared__ __align__(16) char lds[VT > MG ? VT : MG];
+  __shared__ float mlw[NW * QB * 16][2];
+  __shared__ uint4 qlds[QB * DP >= 256 && QB > 1 ? QB * DP * 2 : 1];   // QB * DP / 32 operands of 64 lanes
+  Place pl;
+  pl.split = blockIdx.x;
+  pl.hk = blockIdx.y;
+  pl.s = blockIdx.z;
+  pl.sq = load_seq(a.sq, pl.s, a.kv.psh);
+  pl.n = min(pl.sq.n, a.max_q);
+  pl.rows = pl.n * a.G;
+  if (pl.rows == 0) return;
+  pl.p0 = pl.sq.len - pl.sq.n;                     // positions of the first and last new token
+  pl.p1 = pl.p0 + pl.n - 1;
+  pl.un = key_units(pl.p0, pl.p1, pl.sq.len, a.window, a.sinks, FEW_USH);
+  const int per = share_units(pl.un.tot, a.ns, FEW_LEAST, FEW_STEP);
+  pl.used = max(1, (pl.un.tot + per - 1) / per);
+  if (pl.split >= pl.used) return;
+  pl.u0 = pl.split * per;
+  pl.u1 = min(pl.un.tot, pl.u0 + per);
+  if (QB >= 4 && pl.rows > 32) few_rows<BF, KVM, DP, QB >= 4 ? 4 : 1, NW>(a, pl, lds, mlw, qlds);
+  else if (QB >= 2 && pl.rows > 16) few_rows<BF, KVM, DP, QB >= 2 ? 2 : 1, NW>(a, pl, lds, mlw, qlds);
+  else few_rows<BF, KVM, DP, 1, NW>(a, pl, lds, mlw, qlds);
+}
+
 }  // namespace
 
 int sffn_attn_few_rows(int d) { return d <= 64 ? 64 : d <= 128 ? 32 : 16; }
@@ -368,16 +405,19 @@ hipError_t sffn_launch_attn_few(const AttnArgs& a, int qt, int kvt, hipStream_t 
   const bool bf = qt == T_BF16;
   const int kvm = kvt == T_I8 ? 1 : kvt == T_E4M3 ? 2 : 0;
   const int rows = a.max_q * a.G;
-#define GO(BF, KVM, DP, QB) hipLaunchKernelGGL((k_attn_few<BF, KVM, DP, QB>), grid, dim3(NT), 0, st, a)
-#define TYPES(DP, QB)                                                                        \
-  if (bf) {                                                                                  \
-    if (kvm == 0) GO(true, 0, DP, QB); else if (kvm == 1) GO(true, 1, DP, QB); else GO(true, 2, DP, QB); \
-  } else {                                                                                   \
-    if (kvm == 0) GO(false, 0, DP, QB); else if (kvm == 1) GO(false, 1, DP, QB); else GO(false, 2, DP, QB); \
+  const bool wide = (long)grid.x * grid.y * grid.z <= 256;
+#define GO(BF, KVM, DP, QB, NW) hipLaunchKernelGGL((k_attn_few<BF, KVM, DP, QB, NW>), grid, dim3(NW * 64), 0, st, a)
+#define TYPES(DP, QB, NW)                                                                                          \
+  if (bf) {                                                                                                        \
+    if (kvm == 0) GO(true, 0, DP, QB, NW); else if (kvm == 1) GO(true, 1, DP, QB, NW); else GO(true, 2, DP, QB, NW); \
+  } else {                                                                                                         \
+    if (kvm == 0) GO(false, 0, DP, QB, NW); else if (kvm == 1) GO(false, 1, DP, QB, NW); else GO(false, 2, DP, QB, NW); \
   }
-  if (a.kv.d <= 64) { if (rows > 32) { TYPES(64, 4) } else if (rows > 16) { TYPES(64, 2) } else { TYPES(64, 1) } }
-  else if (a.kv.d <= 128) { if (rows > 16) { TYPES(128, 2) } else { TYPES(128, 1) } }
-  else { TYPES(256, 1) }
+#define WAVES(DP, QB) if (wide) { TYPES(DP, QB, 8) } else { TYPES(DP, QB, 4) }
+  if (a.kv.d <= 64) { if (rows > 32) { WAVES(64, 4) } else if (rows > 16) { WAVES(64, 2) } else { WAVES(64, 1) } }
+  else if (a.kv.d <= 128) { if (rows > 16) { WAVES(128, 2) } else { WAVES(128, 1) } }
+  else { WAVES(256, 1) }
+#undef WAVES
 #undef TYPES
 #undef GO
   return hipGetLastError();

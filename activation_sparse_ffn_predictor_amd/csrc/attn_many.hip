@@ -163,9 +163,11 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
   // 8-bit: the fetched codes into the tile
   auto store = [&](Tile<DP, C8>& tl, int u) {
     if constexpr (C8) {
+      int lx = l;                                  // places worked out anew per tile: registers are short
+      asm volatile("" : "+v"(lx));
 #pragma unroll
       for (int i = 0; i < LD; ++i) {
-        const int key = w * 16 + i * RPI + l / CPR, ch = l % CPR;
+        const int key = w * 16 + i * RPI + lx / CPR, ch = lx % CPR;
         const uint2 k0 = codes4<KVM == 2>(kr[i].x), k1 = codes4<KVM == 2>(kr[i].y), k2 = codes4<KVM == 2>(kr[i].z),
                     k3 = codes4<KVM == 2>(kr[i].w);
         const uint2 v0 = codes4<KVM == 2>(vr[i].x), v1 = codes4<KVM == 2>(vr[i].y), v2 = codes4<KVM == 2>(vr[i].z),
@@ -266,7 +268,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[kb][i]);
-    top = fmaxf(top, __shfl_xor(top, 32, WAVE));
+    top = over32<true>(top);
     if constexpr (!C8) top *= c;
     // The maximum that weights refer to is only moved when a row's has grown by more than 2^8 (a weight of 2^8 is
     // still far inside fp16, and relative precision does not depend on it): most tiles leave the sums alone.
@@ -391,7 +393,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
   }
 
   if (!wave_on) return;
-  ls += __shfl_xor(ls, 32, WAVE);
+  ls = over32<false>(ls);
   if (!mine) return;
   const long row = (long)(sq.q0 + ri) * a.hq + hk * G + rg;
   if (used == 1) {
@@ -421,12 +423,15 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
   }
 }
 
-// Split results of a row added in the order of the shares: one wave a row, lanes over the head's elements. Which
-// shares exist follows from the same rule as in the kernels above.
-template <bool BF>
+// Split results of a row added in a fixed order. WPR waves a row: lanes hold 4 elements each, the lanes that are left
+// take the shares in turn (groups of shares are summed, then the groups). Which shares exist follows from the same
+// rule as in the kernels above.
+template <bool BF, int DP, int WPR>
 __global__ __launch_bounds__(NT) void k_attn_join(AttnArgs a, int few) {
+  constexpr int LE = DP / 4, GR = WPR * 64 / LE;   // lanes of a row's elements; groups
+  __shared__ f32x4 part[WPR > 1 ? WPR : 1][64];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
-  const long row = (long)blockIdx.x * NW + w;
+  const long row = WPR > 1 ? (long)blockIdx.x : (long)blockIdx.x * NW + w;
   if (row >= (long)a.sq.T * a.hq) return;
   const int t = (int)(row / a.hq), hq = (int)(row - (long)t * a.hq), g = hq % a.G, d = a.kv.d;
   const int s = __builtin_amdgcn_readfirstlane(find_seq<64>(a.sq.cu, a.sq.S, t));
@@ -444,29 +449,42 @@ __global__ __launch_bounds__(NT) void k_attn_join(AttnArgs a, int few) {
     hi = p0 + (min(n * a.G, r0 + MANY_ROWS) - 1) / a.G;
   }
   const Units un = key_units(lo, hi, sq.len, a.window, a.sinks, few ? FEW_USH : MANY_USH);
-  const int per = share_units(un.tot, a.ns, few ? FEW_LEAST : MANY_LEAST, few ? NW : 1);
-  const int used = (un.tot + per - 1) / per;
+  const int per = share_units(un.tot, a.ns, few ? FEW_LEAST : MANY_LEAST, few ? FEW_STEP : 1);
+  const int used = (un.tot + per - 1) / per;       // at most MAX_SHARES
   if (used <= 1) return;                           // the row's only block has written it
-  const float2* ml = a.pml + row * a.ns;
-  float M = -INFINITY;
-  for (int k = l; k < used; k += 64) M = fmaxf(M, ml[k].x);
-  M = wave_max(M);
-  const float ms = M == -INFINITY ? 0.f : M;
-  float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  const float* po = a.po + row * a.ns * d;
-  for (int k = 0; k < used; ++k) {
-    const float2 v = ml[k];
-    const float f = fade(v.x, ms);
-    L = fmaf(v.y, f, L);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (l + e * 64 < d) acc[e] = fmaf(po[(long)k * d + l + e * 64], f, acc[e]);
-  }
+  const float2 ml = l < used ? a.pml[row * a.ns + l] : make_float2(-INFINITY, 0.f);
+  const float M = wave_max(ml.x), f = fade(ml.x, M == -INFINITY ? 0.f : M), L = wave_sum(ml.y * f);
   const float iv = L == 0.f ? 0.f : 1.f / L;
-  char* op = a.out + ((long)t * a.ldo + (long)hq * d) * 2;
+  const int e = (l % LE) * 4, gr = (w % WPR) * (64 / LE) + l / LE;
+  const float* po = a.po + row * a.ns * d + e;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int k0 = 0; k0 < used; k0 += 4 * GR) {
+    f32x4 x[4];
+    float fk[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (l + e * 64 < d) *reinterpret_cast<uint16_t*>(op + (l + e * 64) * 2) = (uint16_t)pack2<BF>(acc[e] * iv, 0.f);
+    for (int j = 0; j < 4; ++j) {
+      const int k = k0 + j * GR + gr;
+      const bool in = k < used && e < d;
+      x[j] = in ? *reinterpret_cast<const f32x4*>(po + (long)k * d) : f32x4{0.f, 0.f, 0.f, 0.f};
+      fk[j] = __shfl(f, k, WAVE);                  // k < 64 wherever x is not 0
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc += x[j] * (k0 + j * GR + gr < used ? fk[j] : 0.f);
+  }
+#pragma unroll
+  for (int x = LE; x < 64; x <<= 1)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] += __shfl_xor(acc[j], x, WAVE);
+  if constexpr (WPR > 1) {
+    part[w][l] = acc;
+    __syncthreads();
+    if (w) return;
+#pragma unroll
+    for (int k = 1; k < WPR; ++k) acc += part[k][l];
+  }
+  if (l < LE && e < d)
+    *reinterpret_cast<uint2*>(a.out + ((long)t * a.ldo + (long)hq * d + e) * 2) =
+        make_uint2(pack2<BF>(acc[0] * iv, acc[1] * iv), pack2<BF>(acc[2] * iv, acc[3] * iv));
   if (a.lse && l == 0) a.lse[row] = log_sum(M, L);
 }
 
@@ -492,8 +510,14 @@ hipError_t sffn_launch_attn_many(const AttnArgs& a, int qt, int kvt, hipStream_t
 }
 
 hipError_t sffn_launch_attn_join(const AttnArgs& a, int qt, bool few, hipStream_t st) {
-  const dim3 grid((unsigned)(((long)a.sq.T * a.hq + NW - 1) / NW));
-  if (qt == T_BF16) hipLaunchKernelGGL((k_attn_join<true>), grid, dim3(NT), 0, st, a, (int)few);
-  else hipLaunchKernelGGL((k_attn_join<false>), grid, dim3(NT), 0, st, a, (int)few);
+  const long rows = (long)a.sq.T * a.hq;
+  const bool bf = qt == T_BF16, wide = a.ns > 8;   // four waves a row from 9 shares on
+  const dim3 grid((unsigned)(wide ? rows : (rows + NW - 1) / NW));
+#define GO(BF, DP, WPR) hipLaunchKernelGGL((k_attn_join<BF, DP, WPR>), grid, dim3(NT), 0, st, a, (int)few)
+#define PICK(DP) \
+  if (bf) { if (wide) GO(true, DP, 4); else GO(true, DP, 1); } else { if (wide) GO(false, DP, 4); else GO(false, DP, 1); }
+  if (a.kv.d <= 64) { PICK(64) } else if (a.kv.d <= 128) { PICK(128) } else { PICK(256) }
+#undef PICK
+#undef GO
   return hipGetLastError();
 }
