@@ -230,100 +230,28 @@ def profile_end(max_launches: int):
 
 
 # ------------------------------------------------------------- residual norm, paged K/V cache, attention over it
-# These take types, sizes and strides from the tensors, so they check what the C entry points cannot see: devices,
-# dtypes and layouts. A bad argument raises ValueError before anything is enqueued. Work goes to the current stream of
-# the tensors' own device, whichever device is current.
-def _types():
-    import torch
-    return {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int8: 3, torch.float8_e4m3fn: 4}
+# These go through the C++ binding _bind.so (csrc/bind.cpp), which takes types, sizes and strides from the tensors and
+# checks what the C entry points cannot see: devices, dtypes and layouts. A bad argument raises ValueError, one that the
+# library turns away SffnError, before anything is enqueued. Work goes to the current stream of the tensors' own
+# device, whichever device is current.
+_bound = None
 
 
-_type_ids = None
+def _fast():
+    """The C++ binding, given the loaded library's entry points."""
+    global _bound
+    if _bound is None:
+        import torch  # noqa: F401  (its libraries have to be loaded first)
+        from . import _bind
+        h = lib()
+        _bind.bind(*(ctypes.cast(getattr(h, n), ctypes.c_void_p).value
+                     for n in ("sffn_kv_write", "sffn_kv_read", "sffn_attn", "sffn_add_rmsnorm")))
+        _bound = _bind
+    return _bound
 
 
-def _type(t, what: str, allowed) -> int:
-    global _type_ids
-    if _type_ids is None:
-        _type_ids = _types()
-    n = _type_ids.get(t.dtype)
-    if n not in allowed:
-        raise ValueError(f"{what}: dtype {t.dtype} is not supported here")
-    return n
-
-
-def _on(dev, what: str, *tensors):
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{what}: tensors on {t.device} and {dev}")
-
-
-def _call(fn, where: str, ref, stream, args):
-    """One entry point, with ref's device current and its stream (torch's current one unless given)."""
-    import torch
-    dev = ref.device
-    if dev.type != "cuda":
-        raise ValueError(f"{where}: tensors must be on the GPU, not on {dev}")
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            rc = fn(*args, _stream(stream, ref))
-    else:
-        rc = fn(*args, _stream(stream, ref))
-    if rc:
-        _check(rc, where)
-
-
-def _rows(t, what: str, heads: int, d: int) -> int:
-    """Elements between the tokens of t [T, heads, d], whose tokens are dense."""
-    T, h, e = t.shape if t.dim() == 3 else (None, None, None)
-    if h != heads or e != d:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, not [tokens, {heads}, {d}]")
-    st = t.stride()
-    if T and (st[2] != 1 or (h > 1 and st[1] != d)):
-        raise ValueError(f"{what}: the heads of a token must be dense (strides {st})")
-    return st[0] if T > 1 else h * d
-
-
-def _cache(kv, where: str):
-    """(struct, page, heads, head size, K tensor) of a cache (K, V) or (K, V, K_scale, V_scale)."""
-    K, V = kv[0], kv[1]
-    ks, vs = (kv[2], kv[3]) if len(kv) == 4 else (None, None)
-    ty = _type(K, where + ": K", (1, 2, 3, 4))
-    if K.dim() != 4 or K.shape != V.shape or V.dtype != K.dtype or not K.is_contiguous() or not V.is_contiguous():
-        raise ValueError(f"{where}: K and V are contiguous [pages, heads, page, head size] of one type")
-    n, h, page, d = K.shape
-    if ty >= 3:
-        for sc in (ks, vs):
-            if sc is None or tuple(sc.shape) != (n, h, page) or _type(sc, where + ": scales", (0,)) or not sc.is_contiguous():
-                raise ValueError(f"{where}: an 8-bit cache needs contiguous fp32 scales [pages, heads, page]")
-    else:
-        ks = vs = None
-    _on(K.device, where, V, ks, vs)
-    return _KV(K.data_ptr(), V.data_ptr(), _p(ks), _p(vs), ty, n, page, h, d), K
-
-
-def _seqs(cu, kv_len, table, T: int, dev, where: str):
-    import torch
-    S = kv_len.shape[0]
-    if cu.dtype != torch.int32 or kv_len.dtype != torch.int32 or table.dtype != torch.int32:
-        raise ValueError(f"{where}: cu, kv_len and table are int32")
-    if cu.dim() != 1 or kv_len.dim() != 1 or table.dim() != 2 or cu.shape[0] != S + 1 or table.shape[0] != S:
-        raise ValueError(f"{where}: cu [S + 1], kv_len [S], table [S, max_pages]")
-    if not cu.is_contiguous() or not kv_len.is_contiguous() or (table.stride(1) != 1 and table.shape[1] > 1):
-        raise ValueError(f"{where}: cu, kv_len and the rows of table must be dense")
-    _on(dev, where, cu, kv_len, table)
-    cols = table.shape[1]
-    return _Seqs(cu.data_ptr(), kv_len.data_ptr(), table.data_ptr(), S, T, cols, table.stride(0) if S > 1 else cols)
-
-
-def _kv_move(fn, where, k, v, kv, cu, kv_len, table, stream):
-    c, K = _cache(kv, where)
-    ty = _type(k, where + ": k", (1, 2))
-    if v.dtype != k.dtype or v.shape != k.shape:
-        raise ValueError(f"{where}: k and v differ in type or shape")
-    lk, lv = _rows(k, where + ": k", c.n_kv_heads, c.head_dim), _rows(v, where + ": v", c.n_kv_heads, c.head_dim)
-    _on(K.device, where, k, v)
-    q = _seqs(cu, kv_len, table, k.shape[0], K.device, where)
-    _call(fn, where, K, stream, (c, q, ty, k.data_ptr(), lk, v.data_ptr(), lv))
+def _handle_of(stream):
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def kv_write(k, v, kv, cu, kv_len, table, stream=None):
@@ -331,12 +259,16 @@ def kv_write(k, v, kv, cu, kv_len, table, stream=None):
     8) into the paged cache kv = (K, V) of the same type, or (K, V, K_scale, V_scale) in int8 or float8_e4m3fn.
     K, V [pages, heads, page, head size]; scales [pages, heads, page] fp32. cu [S + 1], kv_len [S] (with the new
     tokens) and table [S, max_pages] int32 name the places."""
-    _kv_move(lib().sffn_kv_write, "sffn_kv_write", k, v, kv, cu, kv_len, table, stream)
+    rc = (_bound or _fast()).kv_write(k, v, kv, cu, kv_len, table, _handle_of(stream))
+    if rc:
+        _check(rc, "sffn_kv_write")
 
 
 def kv_read(kv, cu, kv_len, table, k, v, stream=None):
     """sffn_kv_read: the newest cu[s + 1] - cu[s] cached tokens of every sequence into k, v [T, heads, head size]."""
-    _kv_move(lib().sffn_kv_read, "sffn_kv_read", k, v, kv, cu, kv_len, table, stream)
+    rc = (_bound or _fast()).kv_read(k, v, kv, cu, kv_len, table, _handle_of(stream))
+    if rc:
+        _check(rc, "sffn_kv_read")
 
 
 ATTN_FEW, ATTN_MANY = 0, 1
@@ -358,52 +290,17 @@ def attn(q, kv, cu, kv_len, table, max_q: int, max_kv: int, out, ws, scale: Opti
     """sffn_attn: attention of the new tokens q [T, Hq, head size] (fp16 or bf16) over the cache (see kv_write), causal,
     with an optional window and always-visible first tokens. out as q; lse [T, Hq] fp32 or None; ws a uint8 tensor of
     attn_workspace_size bytes (or None if that is 0); scale: 1 / sqrt(head size) unless given."""
-    c, K = _cache(kv, "sffn_attn")
-    ty = _type(q, "sffn_attn: q", (1, 2))
-    if out.dtype != q.dtype or out.shape != q.shape or q.dim() != 3:
-        raise ValueError("sffn_attn: q and out are [tokens, heads, head size] of one type")
-    T, Hq, d = q.shape
-    lq, lo = _rows(q, "sffn_attn: q", Hq, c.head_dim), _rows(out, "sffn_attn: out", Hq, c.head_dim)
-    if lse is not None and (tuple(lse.shape) != (T, Hq) or _type(lse, "sffn_attn: lse", (0,)) or not lse.is_contiguous()):
-        raise ValueError("sffn_attn: lse is contiguous fp32 [tokens, heads]")
-    if ws is not None and not ws.is_contiguous():
-        raise ValueError("sffn_attn: the workspace must be contiguous")
-    _on(K.device, "sffn_attn", q, out, lse, ws)
-    sq = _seqs(cu, kv_len, table, T, K.device, "sffn_attn")
-    wsp, wsn = (ws.data_ptr(), _nbytes(ws)) if ws is not None else (None, 0)
-    _call(lib().sffn_attn, "sffn_attn", K, stream,
-          (c, sq, ty, q.data_ptr(), lq, Hq, max_q, max_kv, d ** -0.5 if scale is None else scale, window, sinks,
-           out.data_ptr(), lo, _p(lse), wsp, wsn))
-
-
-def _mat(t, what: str, T: int, D: int) -> int:
-    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != D or (t.stride(1) != 1 and T):
-        raise ValueError(f"{what}: not [{T}, {D}] with dense rows")
-    return t.stride(0) if T > 1 else D
+    rc = (_bound or _fast()).attn(q, kv, cu, kv_len, table, max_q, max_kv, out, ws,
+                                  q.shape[-1] ** -0.5 if scale is None else scale, window, sinks, lse,
+                                  _handle_of(stream))
+    if rc:
+        _check(rc, "sffn_attn")
 
 
 def add_rmsnorm(x, res, w, eps: float, y, res_out=None, y_scale=None, stream=None):
     """sffn_add_rmsnorm: h = x + res, res_out = h, y = h / sqrt(mean(h^2) + eps) * w for rows of [T, D]. x, res (None:
     0) and res_out (None, or as res, also res itself) fp32, fp16 or bf16; w [D] fp32 or None (1); y any of these or
     int8 / float8_e4m3fn with y_scale [T] fp32."""
-    where = "sffn_add_rmsnorm"
-    if x.dim() != 2:
-        raise ValueError(f"{where}: x is [tokens, D]")
-    T, D = x.shape
-    xt, yt = _type(x, where + ": x", (0, 1, 2)), _type(y, where + ": y", (0, 1, 2, 3, 4))
-    r = res if res is not None else res_out
-    rt = 0 if r is None else _type(r, where + ": res", (0, 1, 2))
-    if res is not None and res_out is not None and res.dtype != res_out.dtype:
-        raise ValueError(f"{where}: res and res_out differ in type")
-    lx, ly = _mat(x, where + ": x", T, D), _mat(y, where + ": y", T, D)
-    lr = 0 if res is None else _mat(res, where + ": res", T, D)
-    lro = 0 if res_out is None else _mat(res_out, where + ": res_out", T, D)
-    if w is not None and (_type(w, where + ": w", (0,)) or w.shape != (D,) or not w.is_contiguous()):
-        raise ValueError(f"{where}: w is contiguous fp32 [{D}]")
-    if yt >= 3 and (y_scale is None or _type(y_scale, where + ": y_scale", (0,)) or y_scale.shape != (T,)
-                    or not y_scale.is_contiguous()):
-        raise ValueError(f"{where}: an 8-bit y needs y_scale, contiguous fp32 [{T}]")
-    _on(x.device, where, res, w, y, res_out, y_scale)
-    _call(lib().sffn_add_rmsnorm, where, x, stream,
-          (xt, x.data_ptr(), lx, rt, _p(res), lr, _p(w), eps, T, D, yt, y.data_ptr(), ly, _p(y_scale), _p(res_out),
-           lro))
+    rc = (_bound or _fast()).add_rmsnorm(x, res, w, eps, y, res_out, y_scale, _handle_of(stream))
+    if rc:
+        _check(rc, "sffn_add_rmsnorm")
