@@ -101,8 +101,9 @@ struct AttnArgs {
 
 // few-row kernel: units of 32 keys; a share has at least FEW_LEAST of them and a multiple of FEW_STEP
 constexpr int FEW_USH = 5, FEW_LEAST = 16, FEW_STEP = 4;
-// tile kernel: units of 64 keys, 128 rows
-constexpr int MANY_USH = 6, MANY_LEAST = 4, MANY_ROWS = 128;
+// tile kernel: units of 64 keys (32 for head sizes over 128: the accumulators leave no registers for more), 128 rows
+__host__ __device__ constexpr int many_ush(int d) { return d <= 128 ? 6 : 5; }
+constexpr int MANY_LEAST = 4, MANY_ROWS = 128;
 constexpr int MAX_SHARES = 64;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -123,6 +124,11 @@ template <bool BF>
 __device__ __forceinline__ f32x16 mfma32(const uint4& a, const uint4& b, f32x16 c) {
   if constexpr (BF) return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
   else return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
+}
+// buffer load at voff + soff (a wave-uniform part): voff = OOB still reads zeros
+__device__ __forceinline__ uint4 ld16(const Buf& b, uint32_t voff, uint32_t soff) {
+  const v4u32 v = __builtin_amdgcn_raw_buffer_load_b128(b.r, (int)voff, (int)soff, 0);
+  return make_uint4(v.x, v.y, v.z, v.w);
 }
 // two fp32 values as 16 bits each, rounded to nearest even
 template <bool BF>

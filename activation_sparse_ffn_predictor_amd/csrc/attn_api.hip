@@ -82,7 +82,7 @@ int shares(int T, int S, int Hkv, int G, int d, int max_q, int max_kv, int windo
     const int64_t rows = few ? max_q : sffn::MANY_ROWS / G + 2;      // tokens of one tile
     see = std::min(see, (int64_t)window + rows + std::min<int64_t>(sinks, see) + 128);
   }
-  const int unit = few ? 1 << sffn::FEW_USH : 1 << sffn::MANY_USH, least = few ? sffn::FEW_LEAST : sffn::MANY_LEAST;
+  const int unit = few ? 1 << sffn::FEW_USH : 1 << sffn::many_ush(d), least = few ? sffn::FEW_LEAST : sffn::MANY_LEAST;
   const int64_t most = std::max<int64_t>(1, (see + (int64_t)unit * least - 1) / ((int64_t)unit * least));
   const int64_t blocks = (few ? (int64_t)S : (int64_t)T * G / sffn::MANY_ROWS + std::min(S, T)) * Hkv;
     const int64_t want = few ? 2048 : 512;

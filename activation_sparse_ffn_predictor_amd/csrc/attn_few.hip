@@ -107,6 +107,10 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const Place& pl, cha
   };
   auto load = [&](int u) {
     const int t0 = un.key0(u, FEW_USH);
+    int lx = l;                                    // places worked out anew per unit: registers are short
+    asm volatile("" : "+v"(lx));
+    const uint32_t ko = (lx & 15) * dB + (lx >> 4) * 16, vc = lx % CPR;
+    const uint32_t vo = boff(vc * 16 < dB, (lx / CPR) * dB + vc * 16);
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       const int t = t0 + kb * 16, pid = __builtin_amdgcn_readfirstlane(page[kb]);
@@ -114,15 +118,9 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const Place& pl, cha
       const long r = (((long)(have[kb] ? pid : 0) * a.kv.hkv + hk) << a.kv.psh) + (t & ((1 << a.kv.psh) - 1));
       const Buf bk(a.kv.k + r * dB, have[kb] * dB), bv(a.kv.v + r * dB, have[kb] * dB);
 #pragma unroll
-      for (int i = 0; i < KL; ++i) {
-        const uint32_t ch = i * 4 + g4;
-        kr[kb][i] = bk.ld16(boff(ch * 16 < dB, ql * dB + ch * 16));
-      }
+      for (int i = 0; i < KL; ++i) kr[kb][i] = bk.ld16(boff((i * 4 + (lx >> 4)) * 16 < (int)dB, ko) + i * 64);
 #pragma unroll
-      for (int i = 0; i < VL; ++i) {
-        const uint32_t key = i * RPI + l / CPR, ch = l % CPR;
-        vr[kb][i] = bv.ld16(boff(ch * 16 < dB, key * dB + ch * 16));
-      }
+      for (int i = 0; i < VL; ++i) vr[kb][i] = ld16(bv, vo, i * RPI * dB);
       if constexpr (C8) {
         const Buf sk(a.kv.ks + r, have[kb] * 4), sv(a.kv.vs + r, have[kb] * 4);
         ksc[kb] = sk.ldf4(g4 * 16);
@@ -168,11 +166,13 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const Place& pl, cha
       }
     // V through the wave's own LDS tile (the LDS pipe keeps a wave's accesses in order)
     bool odd = false;                              // an infinity or NaN in a unit that some row sees only in part
+    int lv = l;                                    // as in load: worked out anew
+    asm volatile("" : "+v"(lv));
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
       for (int i = 0; i < VL; ++i) {
-        const int key = kb * 16 + i * RPI + l / CPR, ch = l % CPR;
+        const int key = kb * 16 + i * RPI + lv / CPR, ch = lv % CPR;
         *reinterpret_cast<uint4*>(vt + key * RB + ((ch ^ few_swz<RB>(key, C8)) << 4)) = vr[kb][i];
         if (!C8 && !full) {
           const uint4 t = vr[kb][i];
@@ -197,7 +197,8 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const Place& pl, cha
         }
       }
     }
-    // the next unit's loads run under the rest of this one
+    // the next unit's loads run under the rest of this one (not earlier: both units' registers would be alive)
+    __builtin_amdgcn_sched_barrier(0);
     if (u + NW < u1) {
       load(u + NW);
       if (u + 2 * NW < u1) pages(u + 2 * NW);

@@ -9,7 +9,7 @@ using namespace sffn;
 
 namespace {
 
-constexpr int NT = 256, NW = 4, TK = 64;
+constexpr int NT = 256, NW = 4;
 
 template <int DP>
 __device__ __forceinline__ int swz_k(int key) {   // slot of K's 16-byte chunk c: c ^ swz (16 rows, one column: all banks)
@@ -56,9 +56,10 @@ __device__ __forceinline__ void load_lds(const Buf& b, char* dst, uint32_t off) 
   __builtin_amdgcn_raw_ptr_buffer_load_lds(b.r, (__attribute__((address_space(3))) void*)dst, 16, (int)off, 0, 0, 0);
 }
 
-// LDS of one tile of 64 keys.
+// LDS of one tile of keys.
 template <int DP, bool C8>
 struct Tile {
+  static constexpr int TK = 1 << many_ush(DP);
   alignas(16) char k[TK * DP * 2];
   alignas(16) char v[TK * DP * 2];
   alignas(16) float kf[C8 ? TK : 4], lg[C8 ? TK : 4], inv[C8 ? TK : 4];   // see VScale; kf: K scale * softmax scale
@@ -72,6 +73,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
   constexpr bool C8 = KVM != 0, CB = BF && !C8;
   constexpr int EB = C8 ? 1 : 2, RB = DP * 2, KS = DP / 16, DB = DP / 32;
   constexpr int CPR = DP * EB / 16, RPI = 64 / CPR, LD = 16 / RPI;   // 16-byte chunks a cached row; rows, loads of a wave
+  constexpr int USH = many_ush(DP), TK = 1 << USH, KB = TK / 32, NG = TK / 16;   // keys of a tile, by 32 and by 16
   __shared__ Tile<DP, C8> tile0, tile1;
   __shared__ float big_[NW];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, h = l >> 5, ql = l & 31;
@@ -83,7 +85,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
   const int n = min(sq.n, a.max_q), r0 = tile * MANY_ROWS, rows = min(MANY_ROWS, n * G - r0);
   const int p0 = sq.len - sq.n;
   const int b_lo = p0 + r0 / G, b_hi = p0 + (r0 + rows - 1) / G;
-  const Units un = key_units(b_lo, b_hi, sq.len, a.window, a.sinks, MANY_USH);
+  const Units un = key_units(b_lo, b_hi, sq.len, a.window, a.sinks, USH);
   const int per = share_units(un.tot, a.ns, MANY_LEAST, 1), used = max(1, (un.tot + per - 1) / per);
   if (split >= used) return;
   const int u0 = split * per, u1 = min(un.tot, u0 + per);
@@ -122,9 +124,12 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
 
   const int* trow = a.sq.table + (long)s * a.sq.ldt;
   const uint32_t dB = (uint32_t)d * EB;
-  // A wave brings 16 keys of a tile (they share a page); what does not exist reads as zeros. 16-bit rows go straight
+  // A wave brings K and V of 16 keys of a 64-key tile (they share a page), of a 32-key tile one of the two; what does
+  // not exist reads as zeros. 16-bit rows go straight
   // to LDS: the lane for slot l % CPR of a row loads the chunk that belongs there. 8-bit codes pass through
   // registers and are widened once a block.
+  const int grp = w & (NG - 1);
+  const bool do_k = NG == NW || w < NG, do_v = NG == NW || w >= NG;
   uint4 kr[C8 ? LD : 1], vr[C8 ? LD : 1];
   float sk1 = 0.f, sv1 = 0.f;
   int have = 0;
@@ -136,9 +141,9 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
     ko[i] = boff(kc * 16 < dB, key * dB + kc * 16);
     vo[i] = boff(vc * 16 < dB, key * dB + vc * 16);
   }
-  auto page_of = [&](int t0) { return trow[min((t0 + w * 16) >> a.kv.psh, a.sq.cols - 1)]; };
+  auto page_of = [&](int t0) { return trow[min((t0 + grp * 16) >> a.kv.psh, a.sq.cols - 1)]; };
   auto fetch = [&](Tile<DP, C8>& tl, int t0, int page) {
-    const int t = t0 + w * 16;
+    const int t = t0 + grp * 16;
     const int pid = __builtin_amdgcn_readfirstlane(page);
     have = (unsigned)pid < (unsigned)a.kv.n_pages ? min(16, max(0, sq.len - t)) : 0;
     const long row = (((long)(have ? pid : 0) * a.kv.hkv + hk) << a.kv.psh) + (t & ((1 << a.kv.psh) - 1));
@@ -146,11 +151,11 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
 #pragma unroll
     for (int i = 0; i < LD; ++i) {
       if constexpr (C8) {
-        kr[i] = bk.ld16(ko[i]);
-        vr[i] = bv.ld16(vo[i]);
+        if (do_k) kr[i] = bk.ld16(ko[i]);
+        if (do_v) vr[i] = bv.ld16(vo[i]);
       } else {
-        load_lds(bk, tl.k + (w * 16 + i * RPI) * RB, ko[i]);
-        load_lds(bv, tl.v + (w * 16 + i * RPI) * RB, vo[i]);
+        if (do_k) load_lds(bk, tl.k + (grp * 16 + i * RPI) * RB, ko[i]);
+        if (do_v) load_lds(bv, tl.v + (grp * 16 + i * RPI) * RB, vo[i]);
       }
     }
     if constexpr (C8) {
@@ -158,7 +163,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
       sk1 = sk.ldf((l & 15) * 4);
       sv1 = sv.ldf((l & 15) * 4);
     }
-    if (!C8 && l == 0) tl.have[w] = have;
+    if (!C8 && l == 0) tl.have[grp] = have;
   };
   // 8-bit: the fetched codes into the tile
   auto store = [&](Tile<DP, C8>& tl, int u) {
@@ -167,25 +172,29 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
       asm volatile("" : "+v"(lx));
 #pragma unroll
       for (int i = 0; i < LD; ++i) {
-        const int key = w * 16 + i * RPI + lx / CPR, ch = lx % CPR;
+        const int key = grp * 16 + i * RPI + lx / CPR, ch = lx % CPR;
         const uint2 k0 = codes4<KVM == 2>(kr[i].x), k1 = codes4<KVM == 2>(kr[i].y), k2 = codes4<KVM == 2>(kr[i].z),
                     k3 = codes4<KVM == 2>(kr[i].w);
         const uint2 v0 = codes4<KVM == 2>(vr[i].x), v1 = codes4<KVM == 2>(vr[i].y), v2 = codes4<KVM == 2>(vr[i].z),
                     v3 = codes4<KVM == 2>(vr[i].w);
-        *reinterpret_cast<uint4*>(&tl.k[key * RB + (((2 * ch) ^ swz_k<DP>(key)) << 4)]) = make_uint4(k0.x, k0.y, k1.x, k1.y);
-        *reinterpret_cast<uint4*>(&tl.k[key * RB + (((2 * ch + 1) ^ swz_k<DP>(key)) << 4)]) = make_uint4(k2.x, k2.y, k3.x, k3.y);
-        *reinterpret_cast<uint4*>(&tl.v[key * RB + (((2 * ch) ^ swz_v<DP>(key)) << 4)]) = make_uint4(v0.x, v0.y, v1.x, v1.y);
-        *reinterpret_cast<uint4*>(&tl.v[key * RB + (((2 * ch + 1) ^ swz_v<DP>(key)) << 4)]) = make_uint4(v2.x, v2.y, v3.x, v3.y);
+        if (do_k) {
+          *reinterpret_cast<uint4*>(&tl.k[key * RB + (((2 * ch) ^ swz_k<DP>(key)) << 4)]) = make_uint4(k0.x, k0.y, k1.x, k1.y);
+          *reinterpret_cast<uint4*>(&tl.k[key * RB + (((2 * ch + 1) ^ swz_k<DP>(key)) << 4)]) = make_uint4(k2.x, k2.y, k3.x, k3.y);
+        }
+        if (do_v) {
+          *reinterpret_cast<uint4*>(&tl.v[key * RB + (((2 * ch) ^ swz_v<DP>(key)) << 4)]) = make_uint4(v0.x, v0.y, v1.x, v1.y);
+          *reinterpret_cast<uint4*>(&tl.v[key * RB + (((2 * ch + 1) ^ swz_v<DP>(key)) << 4)]) = make_uint4(v2.x, v2.y, v3.x, v3.y);
+        }
       }
       if (l < 16) {
         const VScale v = v_scale(sv1);
-        tl.kf[w * 16 + l] = sk1 * c;
-        tl.lg[w * 16 + l] = v.lg;
-        tl.inv[w * 16 + l] = v.inv;
-        tl.vnan[w * 16 + l] = sv1 != sv1 ? 1 : 0;
+        tl.kf[grp * 16 + l] = sk1 * c;
+        tl.lg[grp * 16 + l] = v.lg;
+        tl.inv[grp * 16 + l] = v.inv;
+        tl.vnan[grp * 16 + l] = sv1 != sv1 ? 1 : 0;
         if (sv1 != sv1) tl.odd = u;
       }
-      if (l == 0) tl.have[w] = have;
+      if (l == 0) tl.have[grp] = have;
     }
   };
 
@@ -208,22 +217,22 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
 
   // one tile: scores, softmax, weighted sum
   auto work = [&](const Tile<DP, C8>& tl, int u, int t0) {
-    f32x16 sc[2];
+    f32x16 sc[KB];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) sc[kb][i] = 0.f;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
+      for (int kb = 0; kb < KB; ++kb) {
         const int key = kb * 32 + ql;
         const uint4 kf = *reinterpret_cast<const uint4*>(&tl.k[key * RB + (((ks * 2 + h) ^ swz_k<DP>(key)) << 4)]);
         sc[kb] = mfma32<CB>(kf, qf[ks], sc[kb]);
       }
     if constexpr (C8) {
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+      for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const f32x4 kf = *reinterpret_cast<const f32x4*>(&tl.kf[kb * 32 + 8 * e + 4 * h]);
@@ -232,7 +241,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
           for (int i = 0; i < 4; ++i) sc[kb][e * 4 + i] = fmaf(sc[kb][e * 4 + i], kf[i], lg[i]);
         }
     }
-    const int hv0 = tl.have[0], hv1 = tl.have[1], hv2 = tl.have[2], hv3 = tl.have[3], nv = hv0 + hv1 + hv2 + hv3;
+    const int hv0 = tl.have[0], hv1 = tl.have[1], hv2 = NG > 2 ? tl.have[2] : 0, hv3 = NG > 2 ? tl.have[3] : 0, nv = hv0 + hv1 + hv2 + hv3;
     const bool full = nv == TK && t0 + TK - 1 <= p_lo &&
                       (a.window <= 0 || t0 > p_hi - a.window || t0 + TK <= a.sinks);
     if (!full) {
@@ -240,13 +249,13 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
       const bool holes = (hv0 < 16 && hv1 + hv2 + hv3) || (hv1 < 16 && hv2 + hv3) || (hv2 < 16 && hv3);
       const int hi = min(pos - t0, holes ? TK - 1 : nv - 1) - 4 * h;
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+      for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int i = 0; i < 16; ++i) sc[kb][i] = kb * 32 + 8 * (i >> 2) + (i & 3) <= hi ? sc[kb][i] : -INFINITY;
       if (a.window > 0) {
         const int lo = pos - a.window - t0 - 4 * h, sk = a.sinks - t0 - 4 * h;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int kk = kb * 32 + 8 * (i >> 2) + (i & 3);
@@ -255,7 +264,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
       }
       if (holes) {
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int hv = kb == 0 ? (i < 8 ? hv0 : hv1) : (i < 8 ? hv2 : hv3);
@@ -265,7 +274,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
     }
     float top = -INFINITY;
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[kb][i]);
     top = over32<true>(top);
@@ -280,17 +289,17 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
       m = mn;
     }
     const float ms = m == -INFINITY ? 0.f : m;
-    uint4 pf[4];
+    uint4 pf[NG];
     const bool slow = tl.odd == u && (C8 || !full);
     uint32_t vis = 0;
     if (slow) {                                    // which elements are seen: bit kb * 16 + i
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+      for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int i = 0; i < 16; ++i) vis |= sc[kb][i] != -INFINITY ? 1u << (kb * 16 + i) : 0u;
     }
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float p[4];
@@ -310,7 +319,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
       }
     if (C8 && slow) {                              // a V row without a scale: NaN for the rows that see it
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
+      for (int kk = 0; kk < NG; ++kk) {
         uint32_t nan[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -326,13 +335,13 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
     }
     if (C8 || !slow) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
+      for (int kk = 0; kk < NG; ++kk)
 #pragma unroll
         for (int db = 0; db < DB; ++db) o[db] = mfma32<CB>(v_frag(tl, kk, db), pf[kk], o[db]);
     } else {
       // infinities and NaN that only some rows see: left out of the products, then added key by key where they are seen
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
+      for (int kk = 0; kk < NG; ++kk)
 #pragma unroll
         for (int db = 0; db < DB; ++db) o[db] = mfma32<CB>(finite_only<CB>(v_frag(tl, kk, db)), pf[kk], o[db]);
       const uint32_t other = __shfl_xor(vis, 32, WAVE);
@@ -358,12 +367,12 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
   // 16-bit tiles that some row may see only in part are looked through for infinities and NaN by one wave each
   auto look = [&](Tile<DP, C8>& tl, int u, int t0) {
     const bool inside = t0 + TK - 1 <= b_lo && (a.window <= 0 || t0 > b_hi - a.window || t0 + TK <= a.sinks) &&
-                        tl.have[0] + tl.have[1] + tl.have[2] + tl.have[3] == TK;
+                        tl.have[0] + tl.have[1] + (NG > 2 ? tl.have[2] + tl.have[3] : 0) == TK;
     if (C8 || inside) return;                      // the same in every wave
     uint32_t odd = 0;
 #pragma unroll
     for (int i = 0; i < LD; ++i) {
-      const uint4 v = *reinterpret_cast<const uint4*>(&tl.v[(w * 16 + i * RPI) * RB + l * 16]);
+      const uint4 v = *reinterpret_cast<const uint4*>(&tl.v[(grp * 16 + i * RPI) * RB + l * 16]);
       odd |= nonfinite2<CB>(v.x) | nonfinite2<CB>(v.y) | nonfinite2<CB>(v.z) | nonfinite2<CB>(v.w);
     }
     if (odd) tl.odd = u;
@@ -371,17 +380,17 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
   };
 
   if (u0 < u1) {
-    const int t0 = un.key0(u0, MANY_USH);
+    const int t0 = un.key0(u0, USH);
     fetch(tile0, t0, page_of(t0));
     store(tile0, u0);
   }
-  int page = u0 + 1 < u1 ? page_of(un.key0(u0 + 1, MANY_USH)) : 0;
+  int page = u0 + 1 < u1 ? page_of(un.key0(u0 + 1, USH)) : 0;
   auto step = [&](Tile<DP, C8>& cur, Tile<DP, C8>& nxt, int u) {
-    const int t0 = un.key0(u, MANY_USH);
+    const int t0 = un.key0(u, USH);
     __syncthreads();                               // cur has arrived, nxt is free
     if (u + 1 < u1) {
-      fetch(nxt, un.key0(u + 1, MANY_USH), page);
-      if (u + 2 < u1) page = page_of(un.key0(u + 2, MANY_USH));
+      fetch(nxt, un.key0(u + 1, USH), page);
+      if (u + 2 < u1) page = page_of(un.key0(u + 2, USH));
     }
     look(cur, u, t0);
     if (wave_on && t0 <= p_hi) work(cur, u, t0);
@@ -448,7 +457,7 @@ __global__ __launch_bounds__(NT) void k_attn_join(AttnArgs a, int few) {
     lo = p0 + r0 / a.G;
     hi = p0 + (min(n * a.G, r0 + MANY_ROWS) - 1) / a.G;
   }
-  const Units un = key_units(lo, hi, sq.len, a.window, a.sinks, few ? FEW_USH : MANY_USH);
+  const Units un = key_units(lo, hi, sq.len, a.window, a.sinks, few ? FEW_USH : many_ush(d));
   const int per = share_units(un.tot, a.ns, few ? FEW_LEAST : MANY_LEAST, few ? FEW_STEP : 1);
   const int used = (un.tot + per - 1) / per;       // at most MAX_SHARES
   if (used <= 1) return;                           // the row's only block has written it
