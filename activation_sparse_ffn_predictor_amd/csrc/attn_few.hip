@@ -129,6 +129,7 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const Place& pl, cha
     }
   };
 
+  bool left_out = false;
   int u = pl.u0 + w;
   if (u < u1) {
     pages(u);
@@ -164,8 +165,8 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const Place& pl, cha
           for (int qb = 0; qb < QB; ++qb) sc[qb][kb] = mfma16<CB>(kr[kb][i], q_frag(qb, i), sc[qb][kb]);
         }
       }
-    // V through the wave's own LDS tile (the LDS pipe keeps a wave's accesses in order)
-    bool odd = false;                              // an infinity or NaN in a unit that some row sees only in part
+    // V through the wave's own LDS tile (the LDS pipe keeps a wave's accesses in order). Infinities and NaN in a unit
+    // that some row sees only in part are left out here and added where they are seen after the last unit.
     int lv = l;                                    // as in load: worked out anew
     asm volatile("" : "+v"(lv));
 #pragma unroll
@@ -173,11 +174,12 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const Place& pl, cha
 #pragma unroll
       for (int i = 0; i < VL; ++i) {
         const int key = kb * 16 + i * RPI + lv / CPR, ch = lv % CPR;
-        *reinterpret_cast<uint4*>(vt + key * RB + ((ch ^ few_swz<RB>(key, C8)) << 4)) = vr[kb][i];
+        uint4 t = vr[kb][i];
         if (!C8 && !full) {
-          const uint4 t = vr[kb][i];
-          odd |= (nonfinite2<CB>(t.x) | nonfinite2<CB>(t.y) | nonfinite2<CB>(t.z) | nonfinite2<CB>(t.w)) != 0;
+          left_out |= (nonfinite2<CB>(t.x) | nonfinite2<CB>(t.y) | nonfinite2<CB>(t.z) | nonfinite2<CB>(t.w)) != 0;
+          t = finite_only<CB>(t);
         }
+        *reinterpret_cast<uint4*>(vt + key * RB + ((ch ^ few_swz<RB>(key, C8)) << 4)) = t;
       }
     f32x4 inv[2];
     uint32_t vnan = 0;                             // bit kb * 4 + i: the key's V row has no scale
@@ -203,9 +205,8 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const Place& pl, cha
       load(u + NW);
       if (u + 2 * NW < u1) pages(u + 2 * NW);
     }
-    const bool slow = C8 ? __any(vnan != 0) : !full && __any(odd);
+    const bool slow = C8 && __any(vnan != 0);
     uint4 pf[QB];
-    uint32_t vis[QB];
 #pragma unroll
     for (int qb = 0; qb < QB; ++qb) {
       if (!full) {
@@ -250,14 +251,10 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const Place& pl, cha
           p[kb][i] = exp2_fast(C8 ? sc[qb][kb][i] - ms : fmaf(sc[qb][kb][i], c, -ms));
           ls[qb] = C8 ? fmaf(p[kb][i], inv[kb][i], ls[qb]) : ls[qb] + p[kb][i];
         }
-      vis[qb] = 0;
-      if (slow) {
+      if (slow) {                            // a V row without a scale: NaN for the rows that see it
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const bool see = sc[qb][e >> 2][e & 3] != -INFINITY;
-          vis[qb] |= see ? 1u << e : 0u;
-          if (C8 && see && (vnan >> e & 1)) p[e >> 2][e & 3] = __uint_as_float(0x7FC00000u);
-        }
+        for (int e = 0; e < 8; ++e)
+          if (sc[qb][e >> 2][e & 3] != -INFINITY && (vnan >> e & 1)) p[e >> 2][e & 3] = __uint_as_float(0x7FC00000u);
       }
       // weights of one rounding (half a step of the type each) enter the second product
       pf[qb] = make_uint4(pack2<CB>(p[0][0], p[0][1]), pack2<CB>(p[0][2], p[0][3]), pack2<CB>(p[1][0], p[1][1]),
@@ -283,42 +280,48 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const Place& pl, cha
         return make_uint4(y0.x, y0.y, y1.x, y1.y);
       }
     };
-    if (C8 || !slow) {
 #pragma unroll
-      for (int db = 0; db < DB; ++db) {
-        const uint4 vf = v_frag(db);
+    for (int db = 0; db < DB; ++db) {
+      const uint4 vf = v_frag(db);
 #pragma unroll
-        for (int qb = 0; qb < QB; ++qb) o[qb][db] = mfma16<CB>(vf, pf[qb], o[qb][db]);
-      }
-    } else {
-      // infinities and NaN that only some rows see: left out of the products, then added key by key where they are seen
-#pragma unroll
-      for (int db = 0; db < DB; ++db) {
-        const uint4 vf = finite_only<CB>(v_frag(db));
-#pragma unroll
-        for (int qb = 0; qb < QB; ++qb) o[qb][db] = mfma16<CB>(vf, pf[qb], o[qb][db]);
-      }
-#pragma unroll 1
-      for (int kk = 0; kk < 32; ++kk) {
-        bool see[QB];
-#pragma unroll
-        for (int qb = 0; qb < QB; ++qb)            // the lane of this row that holds the key's score
-          see[qb] = __shfl((int)vis[qb], ((kk >> 2) & 3) * 16 + ql, WAVE) >> ((kk >> 4) * 4 + (kk & 3)) & 1;
-#pragma unroll
-        for (int db = 0; db < DB; ++db) {          // elements db * 16 + 4 * g4 ..
-          const int ch = db * 2 + (g4 >> 1);
-          const uint2 v = *reinterpret_cast<const uint2*>(vt + kk * RB + ((ch ^ few_swz<RB>(kk, false)) << 4) + (g4 & 1) * 8);
-          if (nonfinite2<CB>(v.x) | nonfinite2<CB>(v.y)) {
-            const float f[4] = {lo16<CB>(v.x), hi16<CB>(v.x), lo16<CB>(v.y), hi16<CB>(v.y)};
-#pragma unroll
-            for (int qb = 0; qb < QB; ++qb)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[qb][db][i] += see[qb] && !(fabsf(f[i]) < INFINITY) ? f[i] : 0.f;
-          }
-        }
-      }
+      for (int qb = 0; qb < QB; ++qb) o[qb][db] = mfma16<CB>(vf, pf[qb], o[qb][db]);
     }
     asm volatile("" ::: "memory");
+  }
+
+  if (!C8 && __any(left_out)) {
+    // once more through the keys of the units that some row sees only in part
+#pragma unroll 1
+    for (u = pl.u0 + w; u < u1; u += NW) {
+      const int t0 = un.key0(u, FEW_USH);
+      int hv[2], pid[2];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        pid[kb] = trow[min((t0 + kb * 16) >> a.kv.psh, a.sq.cols - 1)];
+        hv[kb] = (unsigned)pid[kb] < (unsigned)a.kv.n_pages ? min(16, max(0, sq.len - (t0 + kb * 16))) : 0;
+      }
+      if (hv[0] + hv[1] == 32 && t0 + 31 <= p0 && (a.window <= 0 || t0 > p1 - a.window || t0 + 32 <= a.sinks)) continue;
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll 1
+        for (int kk = 0; kk < hv[kb]; ++kk) {
+          const int j = t0 + kb * 16 + kk;
+          const char* row = a.kv.v + ((((long)pid[kb] * a.kv.hkv + hk) << a.kv.psh) + (j & ((1 << a.kv.psh) - 1))) * dB;
+#pragma unroll
+          for (int db = 0; db < DB; ++db) {
+            const int d0 = db * 16 + g4 * 4;
+            if (d0 >= d) continue;
+            const uint2 v = *reinterpret_cast<const uint2*>(row + d0 * 2);
+            const float f[4] = {lo16<CB>(v.x), hi16<CB>(v.x), lo16<CB>(v.y), hi16<CB>(v.y)};
+#pragma unroll
+            for (int qb = 0; qb < QB; ++qb) {
+              const bool see = j <= pos[qb] && (a.window <= 0 || j > pos[qb] - a.window || j < a.sinks);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[qb][db][i] += see && !(fabsf(f[i]) < INFINITY) ? f[i] : 0.f;
+            }
+          }
+        }
+    }
   }
 
   // the waves' parts joined in wave order

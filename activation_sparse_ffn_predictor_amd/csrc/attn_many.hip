@@ -205,18 +205,25 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[db][i] = 0.f;
 
-  auto v_frag = [&](const Tile<DP, C8>& tl, int kk, int db) {
-    const int key = kk * 16 + 4 * h + ((l & 15) >> 2);
-    const int ch = db * 4 + ((l >> 4) & 1) * 2 + ((l & 3) >> 1);
-    const int at = ((ch ^ swz_v<DP>(key)) << 4) + (l & 1) * 8;   // keys 8 apart: the same slot
-    const fp16x4 y0 = __builtin_amdgcn_ds_read_tr16_b64_v4f16((__attribute__((address_space(3))) fp16x4*)(&tl.v[key * RB + at]));
-    const fp16x4 y1 = __builtin_amdgcn_ds_read_tr16_b64_v4f16((__attribute__((address_space(3))) fp16x4*)(&tl.v[(key + 8) * RB + at]));
+  // Operand places: a row's base with the swizzle of its key, and one exclusive or for the 16-byte column. The bases
+  // are made opaque once a tile, or the loop's invariants (one address a column) would be kept in registers that are
+  // not there; their spilled values' loads would wait for the tile loads in flight.
+  const int kb0 = ql * RB + ((h ^ swz_k<DP>(ql)) << 4);
+  const int vkey = 4 * h + ((l & 15) >> 2);
+  const int vb0 = vkey * RB + (((((l >> 4) & 1) * 2 + ((l & 3) >> 1)) ^ swz_v<DP>(vkey)) << 4) + (l & 1) * 8;
+  auto v_frag = [&](const Tile<DP, C8>& tl, int vb, int kk, int db) {
+    const char* at = tl.v + (vb ^ (db * 64));      // keys 8 and 16 apart: the same slot
+    const fp16x4 y0 = __builtin_amdgcn_ds_read_tr16_b64_v4f16((__attribute__((address_space(3))) fp16x4*)(at + kk * 16 * RB));
+    const fp16x4 y1 = __builtin_amdgcn_ds_read_tr16_b64_v4f16((__attribute__((address_space(3))) fp16x4*)(at + (kk * 16 + 8) * RB));
     const uint2 z0 = __builtin_bit_cast(uint2, y0), z1 = __builtin_bit_cast(uint2, y1);
     return make_uint4(z0.x, z0.y, z1.x, z1.y);
   };
 
+  bool left_out = false;
   // one tile: scores, softmax, weighted sum
   auto work = [&](const Tile<DP, C8>& tl, int u, int t0) {
+    int kb_ = kb0, vb = vb0;
+    asm volatile("" : "+v"(kb_), "+v"(vb));
     f32x16 sc[KB];
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb)
@@ -226,8 +233,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
-        const int key = kb * 32 + ql;
-        const uint4 kf = *reinterpret_cast<const uint4*>(&tl.k[key * RB + (((ks * 2 + h) ^ swz_k<DP>(key)) << 4)]);
+        const uint4 kf = *reinterpret_cast<const uint4*>(tl.k + (kb_ ^ (ks * 32)) + kb * 32 * RB);
         sc[kb] = mfma32<CB>(kf, qf[ks], sc[kb]);
       }
     if constexpr (C8) {
@@ -290,9 +296,9 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
     }
     const float ms = m == -INFINITY ? 0.f : m;
     uint4 pf[NG];
-    const bool slow = tl.odd == u && (C8 || !full);
+    const bool slow = C8 && tl.odd == u;
     uint32_t vis = 0;
-    if (slow) {                                    // which elements are seen: bit kb * 16 + i
+    if (slow) {                              // which elements are seen: bit kb * 16 + i
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
@@ -317,7 +323,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
         if (e & 1) { pf[kb * 2 + (e >> 1)].z = a0; pf[kb * 2 + (e >> 1)].w = a1; }
         else { pf[kb * 2 + (e >> 1)].x = a0; pf[kb * 2 + (e >> 1)].y = a1; }
       }
-    if (C8 && slow) {                              // a V row without a scale: NaN for the rows that see it
+    if (slow) {                                    // a V row without a scale: NaN for the rows that see it
 #pragma unroll
       for (int kk = 0; kk < NG; ++kk) {
         uint32_t nan[4];
@@ -326,57 +332,36 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
           nan[k] = 0;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int e = kk * 8 + k * 2 + j;      // element kb * 16 + i
-            if ((vis >> e & 1) && tl.vnan[(e >> 4) * 32 + 8 * ((e >> 2) & 3) + 4 * h + (e & 3)]) nan[k] |= 0x7E00u << (16 * j);
+            const int e = kk * 8 + k * 2 + j, kb = e >> 4, i = e & 15;
+            if ((vis >> e & 1) && tl.vnan[kb * 32 + 8 * (i >> 2) + 4 * h + (i & 3)]) nan[k] |= 0x7E00u << (16 * j);
           }
         }
         pf[kk] = make_uint4(pf[kk].x | nan[0], pf[kk].y | nan[1], pf[kk].z | nan[2], pf[kk].w | nan[3]);
       }
     }
-    if (C8 || !slow) {
 #pragma unroll
-      for (int kk = 0; kk < NG; ++kk)
+    for (int kk = 0; kk < NG; ++kk)
 #pragma unroll
-        for (int db = 0; db < DB; ++db) o[db] = mfma32<CB>(v_frag(tl, kk, db), pf[kk], o[db]);
-    } else {
-      // infinities and NaN that only some rows see: left out of the products, then added key by key where they are seen
+      for (int db = 0; db < DB; ++db) o[db] = mfma32<CB>(v_frag(tl, vb, kk, db), pf[kk], o[db]);
+  };
+  // Infinities and NaN in a 16-bit tile that some row may see only in part: set to 0 in LDS, and added after the last
+  // tile where they are seen.
+  auto inside = [&](int t0, int have) {
+    return t0 + TK - 1 <= b_lo && (a.window <= 0 || t0 > b_hi - a.window || t0 + TK <= a.sinks) && have == TK;
+  };
+  auto look = [&](Tile<DP, C8>& tl, int u, int t0) {
+    if (C8 || inside(t0, tl.have[0] + tl.have[1] + (NG > 2 ? tl.have[2] + tl.have[3] : 0))) return;   // the same in every wave
 #pragma unroll
-      for (int kk = 0; kk < NG; ++kk)
-#pragma unroll
-        for (int db = 0; db < DB; ++db) o[db] = mfma32<CB>(finite_only<CB>(v_frag(tl, kk, db)), pf[kk], o[db]);
-      const uint32_t other = __shfl_xor(vis, 32, WAVE);
-#pragma unroll 1
-      for (int kk = 0; kk < TK; ++kk) {
-        const uint32_t owner = ((kk >> 2) & 1) == h ? vis : other;
-        const bool see = owner >> ((kk >> 5) * 16 + ((kk >> 3) & 3) * 4 + (kk & 3)) & 1;
-#pragma unroll
-        for (int db = 0; db < DB; ++db)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int ch = db * 4 + e;             // elements db * 32 + 8 e + 4 h ..
-            const uint2 v = *reinterpret_cast<const uint2*>(&tl.v[kk * RB + ((ch ^ swz_v<DP>(kk)) << 4) + 8 * h]);
-            if (nonfinite2<CB>(v.x) | nonfinite2<CB>(v.y)) {
-              const float f[4] = {lo16<CB>(v.x), hi16<CB>(v.x), lo16<CB>(v.y), hi16<CB>(v.y)};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[db][e * 4 + i] += see && !(fabsf(f[i]) < INFINITY) ? f[i] : 0.f;
-            }
-          }
+    for (int i = 0; i < TK * RB / (NT * 16); ++i) {
+      uint4* p = reinterpret_cast<uint4*>(&tl.v[(i * NT + threadIdx.x) * 16]);
+      const uint4 v = *p;
+      if (nonfinite2<CB>(v.x) | nonfinite2<CB>(v.y) | nonfinite2<CB>(v.z) | nonfinite2<CB>(v.w)) {
+        *p = finite_only<CB>(v);
+        tl.odd = u;
       }
     }
-  };
-  // 16-bit tiles that some row may see only in part are looked through for infinities and NaN by one wave each
-  auto look = [&](Tile<DP, C8>& tl, int u, int t0) {
-    const bool inside = t0 + TK - 1 <= b_lo && (a.window <= 0 || t0 > b_hi - a.window || t0 + TK <= a.sinks) &&
-                        tl.have[0] + tl.have[1] + (NG > 2 ? tl.have[2] + tl.have[3] : 0) == TK;
-    if (C8 || inside) return;                      // the same in every wave
-    uint32_t odd = 0;
-#pragma unroll
-    for (int i = 0; i < LD; ++i) {
-      const uint4 v = *reinterpret_cast<const uint4*>(&tl.v[(grp * 16 + i * RPI) * RB + l * 16]);
-      odd |= nonfinite2<CB>(v.x) | nonfinite2<CB>(v.y) | nonfinite2<CB>(v.z) | nonfinite2<CB>(v.w);
-    }
-    if (odd) tl.odd = u;
     __syncthreads();
+    left_out |= tl.odd == u;
   };
 
   if (u0 < u1) {
@@ -402,6 +387,40 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
   }
 
   if (!wave_on) return;
+  if (!C8 && left_out) {
+    // once more through the keys of those tiles
+#pragma unroll 1
+    for (int u = u0; u < u1; ++u) {
+      const int t0 = un.key0(u, USH);
+      int have[NG], pid[NG], nv = 0;
+#pragma unroll
+      for (int k = 0; k < NG; ++k) {
+        pid[k] = trow[min((t0 + k * 16) >> a.kv.psh, a.sq.cols - 1)];
+        have[k] = (unsigned)pid[k] < (unsigned)a.kv.n_pages ? min(16, max(0, sq.len - (t0 + k * 16))) : 0;
+        nv += have[k];
+      }
+      if (inside(t0, nv)) continue;
+#pragma unroll
+      for (int k = 0; k < NG; ++k)
+#pragma unroll 1
+        for (int kk = 0; kk < have[k]; ++kk) {
+          const int j = t0 + k * 16 + kk;
+          const bool see = j <= pos && (a.window <= 0 || j > pos - a.window || j < a.sinks);
+          const char* row = a.kv.v + ((((long)pid[k] * a.kv.hkv + hk) << a.kv.psh) + (j & ((1 << a.kv.psh) - 1))) * dB;
+#pragma unroll
+          for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int d0 = db * 32 + e * 8 + h * 4;
+              if (d0 >= d) continue;
+              const uint2 v = *reinterpret_cast<const uint2*>(row + d0 * 2);
+              const float f[4] = {lo16<CB>(v.x), hi16<CB>(v.x), lo16<CB>(v.y), hi16<CB>(v.y)};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[db][e * 4 + i] += see && !(fabsf(f[i]) < INFINITY) ? f[i] : 0.f;
+            }
+        }
+    }
+  }
   ls = over32<false>(ls);
   if (!mine) return;
   const long row = (long)(sq.q0 + ri) * a.hq + hk * G + rg;
