@@ -8,9 +8,17 @@ is the FFN part of that, with the neuron order of every layer chosen hot-first (
 Layers may differ in predictor rank (Turkish article, "Adaptive sparsity predictors": the predictor is sized per
 layer), and with ``hot_prefix`` each layer's saturated neurons, stored first, are declared always active so the
 predictor reads no rows for them (sffn_predict_hot).
+
+With ``attn`` the layers are whole decoder layers: a residual stream in fp32, and before each sparse FFN a residual norm
+(sffn_add_rmsnorm), the Q/K/V product, the new tokens' K and V into the layer's paged cache (sffn_kv_write), attention
+over it (sffn_attn) and the output product; the FFN reads a second residual norm's output. Every sequence owns a row of
+the page table from the start (its pages are reserved for max_len tokens). ``step`` decodes one token of each of the
+first B sequences, ``prompt`` enters a chunk of one sequence's tokens. No positions are encoded: queries and keys are
+used as they are projected.
 """
 from __future__ import annotations
 
+import dataclasses
 from typing import Dict, List, Optional
 
 import numpy as np
@@ -22,9 +30,27 @@ from . import _lib
 from .pack import hot_first_perm, pack_layer
 
 
+@dataclasses.dataclass(frozen=True)
+class AttnConfig:
+    """Attention of a stack's layers: head layout, cache type ("f16", "i8" or "e4m3") and room, window and sinks."""
+    n_heads: int
+    n_kv_heads: int
+    head_dim: int
+    kv_type: str = "f16"
+    page: int = 64
+    max_len: int = 4096
+    window: int = 0
+    sinks: int = 0
+    eps: float = 1e-5
+
+
+KV_TYPES = {"f16": torch.float16, "i8": torch.int8, "e4m3": torch.float8_e4m3fn}
+
+
 class SparseFFNStack:
     def __init__(self, wl: sg.Workload, device="cuda:0", layers: Optional[List[int]] = None, with_c: bool = True,
-                 max_batch: int = 1, seed: int = sg.MASTER_SEED, hot_prefix: bool = False, fold_predictor: bool = True):
+                 max_batch: int = 1, seed: int = sg.MASTER_SEED, hot_prefix: bool = False, fold_predictor: bool = True,
+                 attn: Optional[AttnConfig] = None):
         self.wl = wl
         self.device = torch.device(device)
         self.layer_ids = list(range(wl.L)) if layers is None else list(layers)
@@ -47,10 +73,90 @@ class SparseFFNStack:
         self.active = torch.zeros((L, F), dtype=torch.int32, device=self.device)
         self.n_active = torch.zeros((L,), dtype=torch.int32, device=self.device)
         self.y = torch.zeros((L, max_batch, D), dtype=torch.float32, device=self.device)
-        self.ws = torch.zeros(_lib.workspace_size(max_batch, D, F, max(self.ranks)), dtype=torch.uint8,
-                              device=self.device)
+        # one token needs more than a few (a partial sum of y per workgroup), so the largest need is not max_batch's
+        need = max(_lib.workspace_size(b, D, F, max(self.ranks)) for b in range(1, max_batch + 1))
+        self.ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
         self.x_in = torch.zeros((max_batch, D), dtype=torch.float32, device=self.device)
         self.graphs = {}
+        self.attn = attn
+        if attn is not None:
+            self._attn_setup(seed)
+
+    # ------------------------------------------------------------------ attention half
+    def _attn_setup(self, seed: int):
+        """Projections and norm weights (synthetic, normal), caches, page table and buffers of the attention half."""
+        c, D, B, dev = self.attn, self.wl.D, self.max_batch, self.device
+        if c.kv_type not in KV_TYPES or c.max_len < 1 or c.n_heads % c.n_kv_heads:
+            raise ValueError(f"attention: {c}")
+        width, cols = (c.n_heads + 2 * c.n_kv_heads) * c.head_dim, -(-c.max_len // c.page)
+        kt, cache = KV_TYPES[c.kv_type], (B * cols, c.n_kv_heads, c.page, c.head_dim)
+        for l, t in zip(self.layer_ids, self.layers):
+            g = torch.Generator(device=dev)
+            g.manual_seed((seed * 1000003 + l) % (1 << 63))
+            t["W_qkv"] = (torch.randn((width, D), generator=g, device=dev) / D ** 0.5).half()
+            t["W_o"] = (torch.randn((D, c.n_heads * c.head_dim), generator=g, device=dev) / (c.n_heads * c.head_dim) ** 0.5).half()
+            t["w_attn"], t["w_ffn"] = (1 + 0.1 * torch.randn(D, generator=g, device=dev) for _ in range(2))
+            kv = [torch.zeros(cache, device=dev).to(kt) for _ in range(2)]
+            if c.kv_type != "f16":
+                kv += [torch.zeros(cache[:3], device=dev) for _ in range(2)]
+            t["kv"] = tuple(kv)
+        self.w_out = torch.ones(D, device=dev)
+        self.table = torch.arange(B * cols, dtype=torch.int32, device=dev).view(B, cols)
+        self.kv_len = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.lens = [0] * B                                    # the same on the host, to refuse what does not fit
+        self.cu_step = torch.arange(B + 1, dtype=torch.int32, device=dev)
+        self.cu_prompt = {}
+        self.h = torch.zeros((B, D), device=dev)               # residual stream
+        self.xn = torch.zeros((B, D), dtype=torch.float16, device=dev)
+        self.qkv = torch.zeros((B, width), dtype=torch.float16, device=dev)
+        self.o = torch.zeros((B, c.n_heads, c.head_dim), dtype=torch.float16, device=dev)
+        self.ao = torch.zeros((B, D), dtype=torch.float16, device=dev)
+        self.xf = torch.zeros((B, D), device=dev)
+        self.out = torch.zeros((B, D), device=dev)             # the last layer's normalised output
+        sizes = [_lib.attn_workspace_size(T, S, c.n_heads, c.n_kv_heads, c.head_dim, T // S, c.max_len, c.window, c.sinks)
+                 for T in range(1, B + 1) for S in (1, T)]
+        self.ws_attn = torch.zeros(max([256] + sizes), dtype=torch.uint8, device=dev)
+
+    def attn_layer(self, i: int, x, B: int, cu, kv_len, table, max_q: int):
+        """Attention half of stored layer i for B tokens: x (the FFN output before it, or the input with i = 0) joins the
+        residual stream self.h; leaves the FFN's input in self.xf."""
+        c, t = self.attn, self.layers[i]
+        h, xn, qkv, o, ao = self.h[:B], self.xn[:B], self.qkv[:B], self.o[:B], self.ao[:B]
+        _lib.add_rmsnorm(x, h if i else None, t["w_attn"], c.eps, xn, res_out=h)
+        torch.mm(xn, t["W_qkv"].t(), out=qkv)
+        parts = qkv.unflatten(1, (-1, c.head_dim))
+        q, k, v = parts.split([c.n_heads, c.n_kv_heads, c.n_kv_heads], dim=1)
+        _lib.kv_write(k, v, t["kv"], cu, kv_len, table)
+        _lib.attn(q, t["kv"], cu, kv_len, table, max_q, c.max_len, o, self.ws_attn, window=c.window, sinks=c.sinks)
+        torch.mm(o.flatten(1), t["W_o"].t(), out=ao)
+        _lib.add_rmsnorm(ao, h, t["w_ffn"], c.eps, self.xf[:B], res_out=h)
+
+    def _layers(self, x, B: int, cu, kv_len, table, max_q: int):
+        for i in range(len(self.layers)):
+            self.attn_layer(i, x, B, cu, kv_len, table, max_q)
+            x = self.y[i, :B]
+            self.layer_call(i, self.xf[:B], False, x)
+        _lib.add_rmsnorm(x, self.h[:B], self.w_out, self.attn.eps, self.out[:B], res_out=self.h[:B])
+
+    def _room(self, s: int, n: int):
+        if self.lens[s] + n > self.attn.max_len:
+            raise ValueError(f"sequence {s}: {self.lens[s]} + {n} tokens exceed max_len = {self.attn.max_len}")
+
+    def prompt(self, s: int, x: torch.Tensor):
+        """Enter x [T, D] fp32 (T <= max_batch), the next tokens of sequence s; results in self.out[:T]."""
+        T = x.shape[0]
+        if self.attn is None or not 0 <= s < self.max_batch or not 1 <= T <= self.max_batch:
+            raise ValueError(f"prompt: sequence {s}, {T} tokens (at most {self.max_batch}; the stack needs attention)")
+        self._room(s, T)
+        cu = self.cu_prompt.setdefault(T, torch.tensor([0, T], dtype=torch.int32, device=self.device))
+        self.kv_len[s:s + 1] += T
+        self.lens[s] += T
+        self._layers(x, T, cu, self.kv_len[s:s + 1], self.table[s:s + 1], T)
+
+    def reset(self):
+        """Forget every sequence's tokens."""
+        self.kv_len.zero_()
+        self.lens = [0] * self.max_batch
 
     # ------------------------------------------------------------------ one layer
     def layer_call(self, i: int, x: torch.Tensor, x_norm: bool, y: torch.Tensor, logits=None):
@@ -86,24 +192,43 @@ class SparseFFNStack:
 
     # ------------------------------------------------------------------ decode step
     def step(self, B: int = 1):
-        """One pass through every layer for the B tokens in self.x_in[:B]; outputs land in self.y[:, :B]."""
+        """One pass through every layer for the B tokens in self.x_in[:B]; outputs land in self.y[:, :B]. With
+        attention: the next token of each of the first B sequences, the last layer's output in self.out[:B] too."""
         x = self.x_in[:B]
+        if self.attn is not None:
+            for s in range(B):
+                self._room(s, 1)
+            self.lens[:B] = [n + 1 for n in self.lens[:B]]
+            self.kv_len[:B] += 1
+            self._layers(x, B, self.cu_step[:B + 1], self.kv_len[:B], self.table[:B], 1)
+            return
         for i in range(len(self.layers)):
             y = self.y[i, :B]
             self.layer_call(i, x, i > 0, y)
             x = y
 
     def capture(self, B: int = 1):
-        """Capture step(B) into a HIP graph (after one eager warm-up)."""
+        """Capture step(B) into a HIP graph (after one eager warm-up). With attention the warm-up's tokens are taken
+        back: the sequences are as long afterwards as before."""
+        lens = None if self.attn is None else (list(self.lens), self.kv_len.clone())
         self.step(B)
         torch.cuda.synchronize(self.device)
+        if lens is not None:
+            self.lens = list(lens[0])
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             self.step(B)
+        if lens is not None:
+            self.lens = lens[0]
+            self.kv_len.copy_(lens[1])
         self.graphs[B] = g
         return g
 
     def replay(self, B: int = 1):
+        if self.attn is not None:
+            for s in range(B):
+                self._room(s, 1)
+            self.lens[:B] = [n + 1 for n in self.lens[:B]]
         self.graphs[B].replay()
 
     # ------------------------------------------------------------------ accounting
