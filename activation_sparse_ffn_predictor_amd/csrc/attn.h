@@ -30,7 +30,7 @@ struct Seqs {
 struct Seq {
   int q0, n, len;
 };
-__device__ __forceinline__ Seq load_seq(const Seqs& q, int s, int psh) {
+__host__ __device__ __forceinline__ Seq load_seq(const Seqs& q, int s, int psh) {
   Seq r;
   const int a = q.cu[s], b = q.cu[s + 1], l = q.len[s];
   r.q0 = min(max(a, 0), q.T);
@@ -65,9 +65,9 @@ __device__ __forceinline__ int find_seq(const int* __restrict__ cu, int S, int t
 // units of the always-visible first tokens that lie before the window, then those of the window itself.
 struct Units {
   int sink, w0, tot;        // units before the window; first window unit; all
-  __device__ __forceinline__ int key0(int u, int ush) const { return (u < sink ? u : u - sink + w0) << ush; }
+  __host__ __device__ __forceinline__ int key0(int u, int ush) const { return (u < sink ? u : u - sink + w0) << ush; }
 };
-__device__ __forceinline__ Units key_units(int p_lo, int p_hi, int len, int window, int sinks, int ush) {
+__host__ __device__ __forceinline__ Units key_units(int p_lo, int p_hi, int len, int window, int sinks, int ush) {
   const int end = min(len, p_hi + 1);          // keys at or after it are visible to no row
   Units u{0, 0, 0};
   if (end <= 0) return u;
@@ -79,7 +79,7 @@ __device__ __forceinline__ Units key_units(int p_lo, int p_hi, int len, int wind
 }
 // Units of each share when a list of `tot` is split into at most ns shares of at least `least` units, whole
 // multiples of `step`.
-__device__ __forceinline__ int share_units(int tot, int ns, int least, int step) {
+__host__ __device__ __forceinline__ int share_units(int tot, int ns, int least, int step) {
   const int per = max(least, (tot + ns - 1) / ns);
   return (per + step - 1) / step * step;
 }
