@@ -56,7 +56,16 @@ __device__ __forceinline__ void load_lds(const Buf& b, char* dst, uint32_t off) 
   __builtin_amdgcn_raw_ptr_buffer_load_lds(b.r, (__attribute__((address_space(3))) void*)dst, 16, (int)off, 0, 0, 0);
 }
 
-// LDS of one tile of keys.
+// Barrier after which every wave's direct loads to LDS have arrived: each wave waits for its own first. (A plain barrier
+// waits for LDS accesses, not for loads on their way there.)
+__device__ __forceinline__ void arrive() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0F70);              // vmcnt(0); the other counters at their maximum (no wait)
+  __syncthreads();
+}
+
+// LDS of one tile of keys. The two tiles of a block are separate objects: the compiler then sees that the loads on
+// their way into one do not concern the reads of the other.
 template <int DP, bool C8>
 struct Tile {
   static constexpr int TK = 1 << many_ush(DP);
@@ -90,7 +99,6 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
   if (split >= used) return;
   const int u0 = split * per, u1 = min(un.tot, u0 + per);
 
-  if (threadIdx.x == 0) tile0.odd = tile1.odd = -1;
   // this lane's row, and the wave's range of positions
   const int r = r0 + w * 32 + ql, ri = r / G, rg = r - ri * G;
   const bool mine = w * 32 + ql < rows;
@@ -125,9 +133,8 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
   const int* trow = a.sq.table + (long)s * a.sq.ldt;
   const uint32_t dB = (uint32_t)d * EB;
   // A wave brings K and V of 16 keys of a 64-key tile (they share a page), of a 32-key tile one of the two; what does
-  // not exist reads as zeros. 16-bit rows go straight
-  // to LDS: the lane for slot l % CPR of a row loads the chunk that belongs there. 8-bit codes pass through
-  // registers and are widened once a block.
+  // not exist reads as zeros. 16-bit rows go straight to LDS: the lane for slot l % CPR of a row loads the chunk that
+  // belongs there. 8-bit codes pass through registers and are widened once a block.
   const int grp = w & (NG - 1);
   const bool do_k = NG == NW || w < NG, do_v = NG == NW || w >= NG;
   uint4 kr[C8 ? LD : 1], vr[C8 ? LD : 1];
@@ -360,7 +367,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
         tl.odd = u;
       }
     }
-    __syncthreads();
+    lds_barrier();                                 // the next tile's loads stay in flight
     left_out |= tl.odd == u;
   };
 
@@ -372,7 +379,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
   int page = u0 + 1 < u1 ? page_of(un.key0(u0 + 1, USH)) : 0;
   auto step = [&](Tile<DP, C8>& cur, Tile<DP, C8>& nxt, int u) {
     const int t0 = un.key0(u, USH);
-    __syncthreads();                               // cur has arrived, nxt is free
+    arrive();                                      // cur is there, nxt is free
     if (u + 1 < u1) {
       fetch(nxt, un.key0(u + 1, USH), page);
       if (u + 2 < u1) page = page_of(un.key0(u + 2, USH));
