@@ -6,9 +6,9 @@ namespace sffn {
 
 enum { T_F32 = 0, T_F16 = 1, T_BF16 = 2, T_I8 = 3, T_E4M3 = 4 };   // sffn_type
 
-// Rows whose scale would be below this are stored as zeros with scale 0, so that the attention can work with the
+// Rows whose scale would be below this are stored as zeros with scale 0, so that quotients by it have exact remainders and the attention can work with the
 // scales' logarithms and reciprocals in normal fp32 numbers.
-constexpr float KV_MIN_SCALE = 7.888609052210118e-31f;   // 2^-100
+constexpr float KV_MIN_SCALE = 8.673617379884035e-19f;   // 2^-60
 
 // A cache as the kernels take it: pages [n_pages, hkv, 1 << psh, d], scales [n_pages, hkv, 1 << psh].
 struct Kv {

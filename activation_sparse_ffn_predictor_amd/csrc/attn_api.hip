@@ -102,7 +102,7 @@ int sffn_kv_write(sffn_kv c, sffn_seqs q, int type, const void* k, int64_t k_str
   if (!s && q.T) s = check_rows("k", k, k_stride, (int64_t)c.n_kv_heads * c.head_dim);
   if (!s && q.T) s = check_rows("v", v, v_stride, (int64_t)c.n_kv_heads * c.head_dim);
   if (s || q.T == 0) return s;
-  if ((int64_t)((q.T + 15) / 16) * c.n_kv_heads >= ((int64_t)1 << 31)) return fail(SFFN_ERR_SHAPE, "T * n_kv_heads too large");
+  if ((int64_t)((q.T + 7) / 8) * c.n_kv_heads >= ((int64_t)1 << 31)) return fail(SFFN_ERR_SHAPE, "T * n_kv_heads too large");
   const hipError_t e = sffn_launch_kv_write(kv_of(c), c.type, seqs_of(q), k, v, type, k_stride, v_stride, (hipStream_t)stream);
   return e == hipSuccess ? SFFN_OK : sffn_err_hip(e, "kv_write launch");
 }
@@ -114,7 +114,7 @@ int sffn_kv_read(sffn_kv c, sffn_seqs q, int type, void* k, int64_t k_stride, vo
   if (!s && q.T) s = check_rows("k", k, k_stride, (int64_t)c.n_kv_heads * c.head_dim);
   if (!s && q.T) s = check_rows("v", v, v_stride, (int64_t)c.n_kv_heads * c.head_dim);
   if (s || q.T == 0) return s;
-  if ((int64_t)((q.T + 15) / 16) * c.n_kv_heads >= ((int64_t)1 << 31)) return fail(SFFN_ERR_SHAPE, "T * n_kv_heads too large");
+  if ((int64_t)((q.T + 7) / 8) * c.n_kv_heads >= ((int64_t)1 << 31)) return fail(SFFN_ERR_SHAPE, "T * n_kv_heads too large");
   const hipError_t e = sffn_launch_kv_read(kv_of(c), c.type, seqs_of(q), k, v, type, k_stride, v_stride, (hipStream_t)stream);
   return e == hipSuccess ? SFFN_OK : sffn_err_hip(e, "kv_read launch");
 }

@@ -5,32 +5,62 @@ using namespace sffn;
 
 namespace {
 
-constexpr int TOK = 16;     // consecutive tokens of one head that a block takes: their slots and scales are neighbours
+// max over aligned groups of G lanes
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  if (G >= 2) v = max(v, dpp_u<0xB1>(v));
+  if (G >= 4) v = max(v, dpp_u<0x4E>(v));
+  if (G >= 8) v = max(v, dpp_u<0x141>(v));
+  if (G >= 16) v = max(v, dpp_u<0x140>(v));
+  if (G >= 32) v = max(v, (uint32_t)__shfl_xor((int)v, 16, WAVE));
+  return v;
+}
 
-// x / s rounded so that a later rounding to fewer bits is that of the exact quotient: the fp32 quotient is cut
-// towards zero and its last bit set if anything was cut off (s > 0, quotient far from overflow).
-__device__ __forceinline__ float div_sticky(float x, float s) {
-  float q = x / s;
-  const float e = fmaf(-q, s, x);                            // exact remainder of the rounded quotient
+// x / s rounded so that rounding the result to a code rounds the exact quotient: cut towards zero, the last bit set if
+// anything was cut off. inv: 1 / s to within a few steps.
+__device__ __forceinline__ float div_sticky(float x, float s, float inv) {
+  float q = x * inv;
+  q = fmaf(fmaf(-q, s, x), inv, q);                          // within one step of the quotient
+  const float e = fmaf(-q, s, x);                            // exact remainder
   if (e != 0.f && q != 0.f) {
     uint32_t b = __float_as_uint(q);
-    if ((e < 0.f) != (q < 0.f)) b -= 1;                      // |q| was rounded up: back to the value below
+    if ((e < 0.f) != (q < 0.f)) b -= 1;                      // |q| is too large: the value below
     q = __uint_as_float(b | 1u);
   }
   return q;
 }
-
+// four codes of x * f, rounded to nearest even
 template <bool E4M3>
-__device__ __forceinline__ uint32_t encode4(const float* v) {
+__device__ __forceinline__ uint32_t encode4(const float* x, float f) {
   if constexpr (E4M3) {
-    int u = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], u, true);
+    const int u = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * f, x[1] * f, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[2] * f, x[3] * f, u, true);
   } else {
-    uint32_t u = 0;
+    uint32_t b[4];                                           // x f + 1.5 * 2^23 has the rounded x f in its low byte
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u |= (uint32_t)((int)rintf(v[i]) & 255) << (8 * i);
-    return u;
+    for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(fmaf(x[i], f, 12582912.f));
+    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0C0C0400u),
+                                 __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u), 0x05040100u);
   }
+}
+// Codes of x[0 .. 8) / s, rounded to nearest even from the exact quotients. 1 / s lies between two fp32 factors; where
+// both give the same codes, these are the quotients' codes, and almost always they do. Else (in one of the wave's rows)
+// exact remainders decide. Quotients are at most top (1 + 2^-23) by the scale's making: nothing needs a limit.
+template <bool E4M3>
+__device__ __forceinline__ uint2 encode8(const float* x, float s) {
+  const float inv = __builtin_amdgcn_rcpf(s), lo = inv * (1.f - 0x1p-20f), hi = inv * (1.f + 0x1p-20f);
+  uint2 c = make_uint2(encode4<E4M3>(x, lo), encode4<E4M3>(x + 4, lo));
+  if (__any(((c.x ^ encode4<E4M3>(x, hi)) | (c.y ^ encode4<E4M3>(x + 4, hi))) != 0)) {
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = div_sticky(x[i], s, inv);
+    c = make_uint2(encode4<E4M3>(q, 1.f), encode4<E4M3>(q + 4, 1.f));
+  }
+  return c;
 }
 
 // The slot of token t in the cache (row index of head 0's slot 0 of its page is pid * hkv << psh), or false.
@@ -43,106 +73,150 @@ __device__ __forceinline__ bool find_slot(const Kv& kv, const Seqs& sq, int s, i
   return (unsigned)pid < (unsigned)kv.n_pages;
 }
 
-// LPR lanes a row, 8 elements each (16 bytes of input). KVM 0: same 16-bit type, 1: int8, 2: e4m3.
-template <int LPR, int KVM, bool BF>
+// The rows (cache row index of head 0's copy, or -1) of the PASS tokens t0, t0 + step, ...: neighbours mostly belong to
+// one sequence, so it is searched for once.
+template <int LPR, int PASS>
+__device__ __forceinline__ void find_rows(const Kv& kv, const Seqs& sq, int h, int t0, int step, long (&row)[PASS]) {
+  int s = 0, a = 0, end = -1, first = 0;           // sequence, its tokens a .. end - 1, position of the first
+#pragma unroll
+  for (int p = 0; p < PASS; ++p) {
+    const int t = t0 + p * step;
+    row[p] = -1;
+    if (t >= sq.T) continue;
+    if (t >= end || t < a) {
+      s = find_seq<LPR>(sq.cu, sq.S, t);
+      if (s >= sq.S) continue;                     // behind the last sequence
+      a = sq.cu[s];
+      end = sq.cu[s + 1];
+      first = sq.len[s] - (end - a);
+    }
+    const int pos = first + (t - a);
+    if (t < a || t >= end || pos < 0 || (pos >> kv.psh) >= sq.cols) continue;
+    const int pid = sq.table[(long)s * sq.ldt + (pos >> kv.psh)];
+    if ((unsigned)pid >= (unsigned)kv.n_pages) continue;
+    row[p] = (((long)pid * kv.hkv + h) << kv.psh) + (pos & ((1 << kv.psh) - 1));
+  }
+}
+
+// LPR lanes a row, 8 elements each (16 bytes of input); a block takes PASS * 256 / LPR consecutive tokens of one head,
+// whose slots and scales are neighbours. KVM 0: same 16-bit type, 1: int8, 2: e4m3.
+template <int LPR, int KVM, bool BF, int PASS>
 __global__ __launch_bounds__(256) void k_kv_write(Kv kv, Seqs sq, const char* __restrict__ k,
                                                   const char* __restrict__ v, long ldk, long ldv) {
-  constexpr int RPB = 256 / LPR, PASS = RPB < TOK ? TOK / RPB : 1;   // rows a block holds at once
+  constexpr int RPB = 256 / LPR;
   const int h = blockIdx.x % kv.hkv, lane = threadIdx.x % LPR;
+  const int t0 = (blockIdx.x / kv.hkv) * (RPB * PASS) + threadIdx.x / LPR;
   const bool act = lane * 8 < kv.d;
+  uint4 x[PASS][2];
 #pragma unroll
-  for (int ps = 0; ps < PASS; ++ps) {
-    const int row = ps * RPB + threadIdx.x / LPR;
-    const int t = (blockIdx.x / kv.hkv) * (RPB < TOK ? TOK : RPB) + row;
-    const bool in = t < sq.T && act;
-    uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (in) {
-      x[0] = *reinterpret_cast<const uint4*>(k + ((long)t * ldk + (long)h * kv.d + lane * 8) * 2);
-      x[1] = *reinterpret_cast<const uint4*>(v + ((long)t * ldv + (long)h * kv.d + lane * 8) * 2);
+  for (int p = 0; p < PASS; ++p) {
+    const int t = t0 + p * RPB;
+    x[p][0] = x[p][1] = make_uint4(0, 0, 0, 0);
+    if (t < sq.T && act) {
+      x[p][0] = *reinterpret_cast<const uint4*>(k + ((long)t * ldk + (long)h * kv.d + lane * 8) * 2);
+      x[p][1] = *reinterpret_cast<const uint4*>(v + ((long)t * ldv + (long)h * kv.d + lane * 8) * 2);
     }
-    const int s = find_seq<LPR>(sq.cu, sq.S, t);
-    int pid = 0, slot = 0;
-    const bool ok = find_slot(kv, sq, s, t, pid, slot) && t < sq.T;
-    const long r = (((long)pid * kv.hkv + h) << kv.psh) + slot;
+  }
+  long row[PASS];
+  find_rows<LPR, PASS>(kv, sq, h, t0, RPB, row);
+#pragma unroll
+  for (int p = 0; p < PASS; ++p)
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       char* dst = m ? kv.v : kv.k;
+      const uint4 xv = x[p][m];
       if constexpr (KVM == 0) {
-        if (ok && in) *reinterpret_cast<uint4*>(dst + (r * kv.d + lane * 8) * 2) = x[m];
+        if (row[p] >= 0 && act) *reinterpret_cast<uint4*>(dst + (row[p] * kv.d + lane * 8) * 2) = xv;
       } else {
-        const uint32_t u[4] = {x[m].x, x[m].y, x[m].z, x[m].w};
-        float f[8], big = 0.f;
-        bool bad = false;
+        // the largest magnitude, as a bit pattern: those of 16-bit values ascend with them, infinity and NaN on top
+        typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+        const uint32_t u[4] = {xv.x, xv.y, xv.z, xv.w};
+        float f[8];
+        u16x2 mx = {0, 0};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           f[2 * i] = lo16<BF>(u[i]);
           f[2 * i + 1] = hi16<BF>(u[i]);
-          big = fmaxf(big, fmaxf(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));
-          bad |= nonfinite2<BF>(u[i]) != 0;
+          mx = __builtin_elementwise_max(mx, __builtin_bit_cast(u16x2, u[i] & 0x7FFF7FFFu));
         }
-        if (bad) big = __uint_as_float(0x7F800000u);
-#pragma unroll
-        for (int o = 1; o < LPR; o <<= 1) big = fmaxf(big, __shfl_xor(big, o, WAVE));
+        const uint32_t big = group_max<LPR>((uint32_t)max(mx.x, mx.y));
         // a row that holds an infinity or NaN has no scale: it is stored as NaN (scale NaN, codes 0)
-        const bool fin = big < __uint_as_float(0x7F800000u);
-        float sc = big / (KVM == 1 ? 127.f : 448.f);
+        const bool fin = big < (BF ? 0x7F80u : 0x7C00u);
+        float sc = lo16<BF>(big) / (KVM == 1 ? 127.f : 448.f);
         if (sc < KV_MIN_SCALE) sc = 0.f;
-        uint2 c = make_uint2(0, 0);
-        if (fin && sc > 0.f) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            f[i] = fminf(fmaxf(div_sticky(f[i], sc), KVM == 1 ? -127.f : -448.f), KVM == 1 ? 127.f : 448.f);
-          c = make_uint2(encode4<KVM == 2>(f), encode4<KVM == 2>(f + 4));
-        }
-        if (ok && in) {
-          *reinterpret_cast<uint2*>(dst + r * kv.d + lane * 8) = c;
-          if (lane == 0) (m ? kv.vs : kv.ks)[r] = fin ? sc : __uint_as_float(0x7FC00000u);
+        const bool some = fin && sc > 0.f;
+        uint2 c = encode8<KVM == 2>(f, some ? sc : 1.f);
+        if (!some) c = make_uint2(0, 0);
+        if (row[p] >= 0 && act) {
+          *reinterpret_cast<uint2*>(dst + row[p] * kv.d + lane * 8) = c;
+          if (lane == 0) (m ? kv.vs : kv.ks)[row[p]] = fin ? sc : __uint_as_float(0x7FC00000u);
         }
       }
     }
-  }
 }
 
 // The other way: value = code * scale in fp32, rounded once to the 16-bit type (16-bit caches: copied).
-template <int LPR, int KVM, bool BF>
+template <int LPR, int KVM, bool BF, int PASS>
 __global__ __launch_bounds__(256) void k_kv_read(Kv kv, Seqs sq, char* __restrict__ k, char* __restrict__ v, long ldk,
                                                  long ldv) {
-  constexpr int RPB = 256 / LPR, PASS = RPB < TOK ? TOK / RPB : 1;
+  constexpr int RPB = 256 / LPR;
   const int h = blockIdx.x % kv.hkv, lane = threadIdx.x % LPR;
+  const int t0 = (blockIdx.x / kv.hkv) * (RPB * PASS) + threadIdx.x / LPR;
   const bool act = lane * 8 < kv.d;
+  long row[PASS];
+  find_rows<LPR, PASS>(kv, sq, h, t0, RPB, row);
+  uint4 x[PASS][2];
+  float sc[PASS][2];
 #pragma unroll
-  for (int ps = 0; ps < PASS; ++ps) {
-    const int t = (blockIdx.x / kv.hkv) * (RPB < TOK ? TOK : RPB) + ps * RPB + threadIdx.x / LPR;
-    const int s = find_seq<LPR>(sq.cu, sq.S, t);
-    int pid = 0, slot = 0;
-    if (!find_slot(kv, sq, s, t, pid, slot) || t >= sq.T || !act) continue;
-    const long r = (((long)pid * kv.hkv + h) << kv.psh) + slot;
+  for (int p = 0; p < PASS; ++p)
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       const char* src = m ? kv.v : kv.k;
-      uint4 o;
+      x[p][m] = make_uint4(0, 0, 0, 0);
+      sc[p][m] = 0.f;
+      if (row[p] < 0 || !act) continue;
       if constexpr (KVM == 0) {
-        o = *reinterpret_cast<const uint4*>(src + (r * kv.d + lane * 8) * 2);
+        x[p][m] = *reinterpret_cast<const uint4*>(src + (row[p] * kv.d + lane * 8) * 2);
       } else {
-        const uint2 c = *reinterpret_cast<const uint2*>(src + r * kv.d + lane * 8);
-        const float sc = (m ? kv.vs : kv.ks)[r];
-        const uint2 a = codes4<KVM == 2>(c.x), b = codes4<KVM == 2>(c.y);
-        o.x = pack2<BF>(lo16<false>(a.x) * sc, hi16<false>(a.x) * sc);
-        o.y = pack2<BF>(lo16<false>(a.y) * sc, hi16<false>(a.y) * sc);
-        o.z = pack2<BF>(lo16<false>(b.x) * sc, hi16<false>(b.x) * sc);
-        o.w = pack2<BF>(lo16<false>(b.y) * sc, hi16<false>(b.y) * sc);
+        const uint2 c = *reinterpret_cast<const uint2*>(src + row[p] * kv.d + lane * 8);
+        x[p][m].x = c.x;
+        x[p][m].y = c.y;
+        sc[p][m] = (m ? kv.vs : kv.ks)[row[p]];
       }
+    }
+#pragma unroll
+  for (int p = 0; p < PASS; ++p)
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      if (row[p] < 0 || !act) continue;
+      uint4 o = x[p][m];
+      if constexpr (KVM != 0) {
+        const uint2 a = codes4<KVM == 2>(o.x), b = codes4<KVM == 2>(o.y);
+        const float g = sc[p][m];
+        o.x = pack2<BF>(lo16<false>(a.x) * g, hi16<false>(a.x) * g);
+        o.y = pack2<BF>(lo16<false>(a.y) * g, hi16<false>(a.y) * g);
+        o.z = pack2<BF>(lo16<false>(b.x) * g, hi16<false>(b.x) * g);
+        o.w = pack2<BF>(lo16<false>(b.y) * g, hi16<false>(b.y) * g);
+      }
+      const int t = t0 + p * RPB;
       *reinterpret_cast<uint4*>((m ? v : k) + ((long)t * (m ? ldv : ldk) + (long)h * kv.d + lane * 8) * 2) = o;
     }
-  }
 }
 
 template <int LPR>
 hipError_t go(bool write, const Kv& kv, int kvm, bool bf, const Seqs& sq, char* k, char* v, long ldk, long ldv,
               hipStream_t st) {
-  constexpr int PER = 256 / LPR < TOK ? TOK : 256 / LPR;
-  const dim3 grid((unsigned)((sq.T + PER - 1) / PER) * kv.hkv);
-#define GO(K, KVM, BF) hipLaunchKernelGGL((K<LPR, KVM, BF>), grid, dim3(256), 0, st, kv, sq, k, v, ldk, ldv)
+  constexpr int RPB = 256 / LPR;
+  // four tokens a thread where that still leaves 16 workgroups a compute unit
+  const long one = (long)((sq.T + RPB - 1) / RPB) * kv.hkv;
+  const bool four = one >= 4 * 16 * 256;
+  const int per = four ? 4 * RPB : RPB;
+  const dim3 grid((unsigned)((sq.T + per - 1) / per) * kv.hkv);
+#define GO(K, KVM, BF)                                                                                        \
+  do {                                                                                                        \
+    if (four) hipLaunchKernelGGL((K<LPR, KVM, BF, 4>), grid, dim3(256), 0, st, kv, sq, k, v, ldk, ldv);       \
+    else hipLaunchKernelGGL((K<LPR, KVM, BF, 1>), grid, dim3(256), 0, st, kv, sq, k, v, ldk, ldv);            \
+  } while (0)
 #define PICK(K)                                    \
   if (kvm == 0) GO(K, 0, false);                   \
   else if (kvm == 1 && !bf) GO(K, 1, false);       \

@@ -71,17 +71,18 @@ __device__ __forceinline__ uint32_t code4(const double* v) {
   }
 }
 
-// WPR waves a row (1 or 4), CH chunks of 8 elements per lane: D <= 512 * WPR * CH. The row stays in registers
+// WPR waves a row, CH chunks of 8 elements per lane: D <= 512 * WPR * CH. One chunk a lane wherever 1024 threads hold a
+// row (4099 rows of 8192 to int8: 97 us on 4 waves, 93 on 8, 81 on 16). The row stays in registers
 // between its sum and its output, so every byte is read and written once. YQ: 0 = 16 / 32 bits out, 1 = int8,
 // 2 = e4m3. An 8-bit output is computed in 64 bits from the fp32 sums h on (the fp64 units are idle in a kernel that
 // waits for memory): codes are then those of the formula, whatever the order of the sum, but for quotients within
 // 1e-15 of a border.
 template <int WPR, int CH, int YQ>
-__global__ __launch_bounds__(256) void k_add_rmsnorm(const void* __restrict__ x, int xt, const void* res, int rt,
+__global__ __launch_bounds__(WPR > 4 ? WPR * 64 : 256) void k_add_rmsnorm(const void* __restrict__ x, int xt, const void* res, int rt,
                                                      const float* __restrict__ w, double eps, int T, int D, long ldx,
                                                      long ldr, void* __restrict__ y, int yt, float* __restrict__ ys,
                                                      void* res_out, long ldy, long ldro) {
-  __shared__ double red[2][4];
+  __shared__ double red[2][WPR > 1 ? WPR : 1];
   const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int row = WPR == 1 ? blockIdx.x * 4 + wv : blockIdx.x;
   if (WPR == 1 && row >= T) return;
@@ -135,7 +136,9 @@ __global__ __launch_bounds__(256) void k_add_rmsnorm(const void* __restrict__ x,
       float* r = reinterpret_cast<float*>(red[0]);
       if (lane == 0) r[wv] = q;
       __syncthreads();
-      q = (r[0] + r[1]) + (r[2] + r[3]);
+      q = r[0];
+#pragma unroll
+      for (int k = 1; k < WPR; ++k) q += r[k];
     }
     const float rs = 1.0f / sqrtf(q / (float)D + (float)eps);
 #pragma unroll
@@ -156,7 +159,9 @@ __global__ __launch_bounds__(256) void k_add_rmsnorm(const void* __restrict__ x,
     if (WPR > 1) {
       if (lane == 0) red[0][wv] = q;
       __syncthreads();
-      q = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
+      q = red[0][0];
+#pragma unroll
+      for (int k = 1; k < WPR; ++k) q += red[0][k];
     }
     const double rs = 1.0 / sqrt(q / (double)D + eps);
     double big = 0.0;                       // largest |h w| (times rs below); NaN is looked for apart
@@ -176,7 +181,8 @@ __global__ __launch_bounds__(256) void k_add_rmsnorm(const void* __restrict__ x,
     if (WPR > 1) {
       if (lane == 0) red[1][wv] = bad ? __longlong_as_double(0x7FF0000000000000ll) : big;
       __syncthreads();
-      big = fmax(fmax(red[1][0], red[1][1]), fmax(red[1][2], red[1][3]));
+#pragma unroll
+      for (int k = 0; k < WPR; ++k) big = fmax(big, red[1][k]);
       bad = !(big < 1.7e308);
     }
     // the scale is the fp32 rounding of max|y| / top; a row with an infinity or NaN gets the scale NaN and codes 0
@@ -201,15 +207,16 @@ hipError_t sffn_launch_add_rmsnorm(const void* x, int xt, const void* res, int r
                                    long ldro, hipStream_t st) {
   const int yq = yt == T_I8 ? 1 : yt == T_E4M3 ? 2 : 0;
 #define GO(WPR, CH, YQ)                                                                                           \
-  hipLaunchKernelGGL((k_add_rmsnorm<WPR, CH, YQ>), dim3(WPR == 1 ? (T + 3) / 4 : T), dim3(256), 0, st, x, xt, res, rt, \
+  hipLaunchKernelGGL((k_add_rmsnorm<WPR, CH, YQ>), dim3(WPR == 1 ? (T + 3) / 4 : T), dim3(WPR > 4 ? WPR * 64 : 256), 0, st, x, xt, \
+                     res, rt, \
                      w, eps, T, D, ldx, ldr, y, yt, ys, res_out, ldy, ldro)
 #define PICK(WPR, CH) \
   if (yq == 0) GO(WPR, CH, 0); else if (yq == 1) GO(WPR, CH, 1); else GO(WPR, CH, 2)
   if (D <= 512) { PICK(1, 1); }
   else if (D <= 2048) { PICK(4, 1); }
-  else if (D <= 4096) { PICK(4, 2); }
-  else if (D <= 8192) { PICK(4, 4); }
-  else { PICK(4, 8); }
+  else if (D <= 4096) { PICK(8, 1); }
+  else if (D <= 8192) { PICK(16, 1); }
+  else { PICK(16, 2); }
 #undef PICK
 #undef GO
   return hipGetLastError();

@@ -231,7 +231,7 @@ int sffn_profile_end(float* ms, int max);
  * 16-bit type, or 8-bit codes (SFFN_I8, SFFN_E4M3: OCP e4m3) with one fp32 scale per token and head:
  *   scale = fp32(max|x| / top), top = 127 or 448;  code = x / scale rounded to nearest, ties to even (of the exact
  *   quotient);  value = code * scale.
- * Rows whose scale would be below 2^-100 are stored as zeros with scale 0; a row that holds an infinity or NaN is
+ * Rows whose scale would be below 2^-60 are stored as zeros with scale 0; a row that holds an infinity or NaN is
  * stored with scale NaN and codes 0. */
 typedef enum { SFFN_F32 = 0, SFFN_F16 = 1, SFFN_BF16 = 2, SFFN_I8 = 3, SFFN_E4M3 = 4 } sffn_type;
 

@@ -6,7 +6,7 @@ import torch
 DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16, "i8": torch.int8,
       "e4m3": torch.float8_e4m3fn}
 TOP = {"i8": 127.0, "e4m3": 448.0}
-MIN_SCALE = 2.0 ** -100
+MIN_SCALE = 2.0 ** -60
 
 
 def half_step(t):
