@@ -73,8 +73,8 @@ bool attn_sizes_ok(int Hq, int Hkv, int d, int max_q) {
 }
 bool few_rows(int G, int d, int max_q) { return (int64_t)max_q * G <= sffn_attn_few_rows(d); }
 
-// Over how many workgroups the keys of one sequence (few rows) or of one row tile are spread: enough for `want`
-// workgroups in all, at most one per FEW_LEAST (MANY_LEAST) units of the keys that the longest sequence can see.
+// Over how many workgroups the keys of one sequence (few rows) or of one row tile are spread, at most one per FEW_LEAST
+// (MANY_LEAST) units of the keys that the longest sequence can see.
 int shares(int T, int S, int Hkv, int G, int d, int max_q, int max_kv, int window, int sinks) {
   const bool few = few_rows(G, d, max_q);
   int64_t see = std::max(1, std::min(max_kv, MAX_POS));
@@ -85,8 +85,17 @@ int shares(int T, int S, int Hkv, int G, int d, int max_q, int max_kv, int windo
   const int unit = few ? 1 << sffn::FEW_USH : 1 << sffn::many_ush(d), least = few ? sffn::FEW_LEAST : sffn::MANY_LEAST;
   const int64_t most = std::max<int64_t>(1, (see + (int64_t)unit * least - 1) / ((int64_t)unit * least));
   const int64_t blocks = (few ? (int64_t)S : (int64_t)T * G / sffn::MANY_ROWS + std::min(S, T)) * Hkv;
-    const int64_t want = few ? 2048 : 512;
-  return (int)std::min<int64_t>({(want + blocks - 1) / std::max<int64_t>(1, blocks), most, sffn::MAX_SHARES});
+  const int64_t places = 512;                      // workgroups that run at once: two a compute unit
+  int64_t ns;
+  if (!few) ns = (places + blocks - 1) / blocks;
+  // As many shares as fill one round: partial results cost a join, and with many rows weigh as much as the keys (48
+  // sequences of 4 drafts on 128 heads of 64 over a window of 4096, bf16: one share 86 us, six 121; two sequences of
+  // 131072 on 8 K/V heads, e4m3: 32 shares 105 us, 64 109).
+  else if (max_q * G > 16 || 2 * blocks <= places) ns = places / blocks;
+  // Few rows and most places taken already: shares of half a round's work even out sequences of different lengths (32
+  // sequences to 6000 tokens on 40 heads, int8: one share 187 us, two 169).
+  else ns = (3 * places + blocks - 1) / blocks;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({ns, most, sffn::MAX_SHARES}));
 }
 size_t po_bytes(int T, int Hq, int d, int ns) { return align256((size_t)T * Hq * ns * d * sizeof(float)); }
 
