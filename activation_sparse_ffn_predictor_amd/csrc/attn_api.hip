@@ -84,14 +84,16 @@ int shares(int T, int S, int Hkv, int G, int d, int max_q, int max_kv, int windo
   }
   const int unit = few ? 1 << sffn::FEW_USH : 1 << sffn::many_ush(d), least = few ? sffn::FEW_LEAST : sffn::MANY_LEAST;
   const int64_t most = std::max<int64_t>(1, (see + (int64_t)unit * least - 1) / ((int64_t)unit * least));
-  const int64_t blocks = (few ? (int64_t)S : (int64_t)T * G / sffn::MANY_ROWS + std::min(S, T)) * Hkv;
+  // workgroups without shares; row tiles: the whole ones, and half a tile more for each further sequence's end
+  const int64_t tiles = ((int64_t)T * G + sffn::MANY_ROWS - 1) / sffn::MANY_ROWS + (std::min(S, T) - 1) / 2;
+  const int64_t blocks = (few ? (int64_t)S : tiles) * Hkv;
   const int64_t places = 512;                      // workgroups that run at once: two a compute unit
   int64_t ns;
-  if (!few) ns = (places + blocks - 1) / blocks;
   // As many shares as fill one round: partial results cost a join, and with many rows weigh as much as the keys (48
   // sequences of 4 drafts on 128 heads of 64 over a window of 4096, bf16: one share 86 us, six 121; two sequences of
-  // 131072 on 8 K/V heads, e4m3: 32 shares 105 us, 64 109).
-  else if (max_q * G > 16 || 2 * blocks <= places) ns = places / blocks;
+  // 131072 on 8 K/V heads, e4m3: 32 shares 105 us, 64 109; 100 tokens on 64 heads over 100000, fp16: nine shares 424 us,
+  // ten 511).
+  if (!few || max_q * G > 16 || 2 * blocks <= places) ns = places / blocks;
   // Few rows and most places taken already: shares of half a round's work even out sequences of different lengths (32
   // sequences to 6000 tokens on 40 heads, int8: one share 187 us, two 169).
   else ns = (3 * places + blocks - 1) / blocks;
