@@ -186,7 +186,7 @@ int sffn_attn(sffn_kv c, sffn_seqs q, int type, const void* qp, int64_t q_stride
   a.ns = ns;
   a.ldq = q_stride;
   a.ldo = out_stride;
-  a.c = fabsf(scale) * 1.4426950408889634f;
+  a.c = std::max(fabsf(scale) * 1.4426950408889634f, 1.2e-38f);   // not 0: masked scores are -infinity times it
   a.neg = scale < 0.f;
   a.po = (float*)ws;
   a.pml = (float2*)((char*)ws + (ns > 1 ? po_bytes(q.T, Hq, c.head_dim, ns) : 0));

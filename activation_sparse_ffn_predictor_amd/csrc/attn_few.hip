@@ -61,7 +61,7 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const Place& pl, cha
 #pragma unroll
     for (int qb = 0; qb < QB; ++qb)
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) big = fmaxf(big, absmax8<true>(qf[qb][ks]));
+      for (int ks = 0; ks < KS; ++ks) big = fmaxf(big, absmax8<true>(finite_only<true>(qf[qb][ks])));
     const float up = to_f16_range(wave_max(big), c);
 #pragma unroll
     for (int qb = 0; qb < QB; ++qb)

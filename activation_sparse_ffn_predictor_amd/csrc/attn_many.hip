@@ -124,7 +124,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
   if constexpr (C8 && BF) {   // bf16 queries into fp16's range, as in the few-row kernel
     float big = 0.f;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) big = fmaxf(big, absmax8<true>(qf[ks]));
+    for (int ks = 0; ks < KS; ++ks) big = fmaxf(big, absmax8<true>(finite_only<true>(qf[ks])));
     big = wave_max(big);
     if (l == 0) big_[w] = big;
     __syncthreads();

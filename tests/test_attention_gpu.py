@@ -536,6 +536,112 @@ def test_graph_replays_and_other_streams(gpu_ready):
     assert torch.equal(got, a.out)
 
 
+@pytest.mark.parametrize("qt,kvt", [("f16", "f16"), ("bf16", "bf16"), ("f16", "i8"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("scale", [0.0, -0.125, 1e-42, 3.0])
+def test_any_finite_scale(gpu_ready, qt, kvt, scale):
+    for ns, ks in (([1, 2], [90, 40]), ([70, 3], [90, 40])):
+        b = Paged(ns, ks, 2, 64, 16, qt, kvt, seed=8)
+        check_attn(b, 4, gpu_ready, scale=scale, q_scale=0.2)
+
+
+@pytest.mark.parametrize("kvt", ["bf16", "i8"])
+def test_queries_with_infinities_touch_only_their_rows(gpu_ready, kvt):
+    for n in (2, 80):
+        b = Paged([n], [150], 1, 64, 16, "bf16", kvt, seed=4)
+        q = (torch.randn((n, 4, 64), generator=b.g) * 1000).bfloat16()
+        clean = q.clone()
+        q[0, 1, 3], q[n - 1, 2, 7] = math.inf, math.nan
+        out, lse = run_attn(b, q, 4, gpu_ready)
+        o, l, to, tl = attention(b, clean, 4, 0.125)
+        ok = torch.ones((n, 4), dtype=torch.bool)
+        ok[0, 1] = ok[n - 1, 2] = False
+        assert_near(out[ok.to(out.device)], o[ok], to[ok])
+        assert_near(lse[ok.to(out.device)], l[ok], tl[ok])
+        assert out[~ok.to(out.device)].isnan().all()
+
+
+def test_shared_pages(gpu_ready):
+    """Sequences whose tables share the pages of a common beginning."""
+    for n in (1, 60):
+        b = Paged([n, n, n], [160, 200, 170], 2, 64, 16, "f16", "f16", seed=n)
+        b.table[1, :4] = b.table[0, :4]
+        b.table[2, :4] = b.table[0, :4]
+        check_attn(b, 8, gpu_ready)
+
+
+def test_many_sequences(gpu_ready):
+    """More sequences than any lookup step takes at once: single tokens, and a few longer ones among them."""
+    dev = gpu_ready
+    for S, long in ((5000, 0), (700, 9)):
+        ns = [1] * S
+        ks = [1 + (7 * i) % 40 for i in range(S)]
+        for i in range(long):
+            ns[71 * i] = ks[71 * i] = 20 + i
+        b = Paged(ns, ks, 1, 16, 16, "f16", "f16", seed=3)
+        q = torch.randn((b.T, 4, 16), generator=b.g).half()
+        kv, cu, kl, tab = b.gpu(dev)
+        back = torch.zeros((2, b.T, 1, 16), dtype=torch.float16, device=dev)
+        _lib.kv_read(kv, cu, kl, tab, back[0], back[1])
+        _lib.kv_write(back[0], back[1], kv, cu, kl, tab)
+        out, lse = run_attn(b, q, 4, dev)
+        assert torch.equal(kv[0].cpu(), b.codes[0])
+        pick = sorted({0, 1, S // 2, S - 2, S - 1, *(71 * i for i in range(long))})
+        for s in pick:
+            one = Paged([ns[s]], [ks[s]], 1, 16, 16, "f16", "f16")
+            one.table, one.n_pages, one.cols, one.val = b.table[s:s + 1], b.n_pages, b.cols, b.val
+            t = int(b.cu[s])
+            o, l, to, tl = attention(one, q[t:t + ns[s]], 4, 0.25)
+            assert_near(out[t:t + ns[s]], o, to, f"sequence {s}")
+            assert torch.equal(back[0, t:t + ns[s]].cpu().double(), one.rows(0, 0, ks[s])[0][:, -ns[s]:].transpose(0, 1))
+
+
+def test_graphs_of_chunks_share_a_workspace(gpu_ready):
+    """Two graphs (a chunk with split keys, single tokens) that use one workspace in turn, with a norm and a read among
+    their nodes, replayed alternately with eager work between: each replay gives the eager bits."""
+    dev, Hq, Hkv, d = gpu_ready, 16, 2, 64
+    b = Paged([40, 1], [2000, 900], Hkv, d, 16, "bf16", "bf16", seed=12)
+    kv, cu, kl, tab = b.gpu(dev)
+    sizes = [_lib.attn_workspace_size(41, 2, Hq, Hkv, d, 40, 2000), _lib.attn_workspace_size(2, 2, Hq, Hkv, d, 1, 2000)]
+    assert min(sizes) > 0
+    ws = torch.empty(max(sizes), dtype=torch.uint8, device=dev)
+    x = torch.randn((41, Hq * d), device=dev)
+    w = torch.ones(Hq * d, device=dev)
+
+    class Job:
+        def __init__(self, T, cu, max_q):
+            self.cu, self.max_q, self.x = cu, max_q, x[:T].clone()
+            self.xn = torch.zeros((T, Hq * d), dtype=torch.bfloat16, device=dev)
+            self.out = torch.zeros((T, Hq, d), dtype=torch.bfloat16, device=dev)
+            self.back = torch.zeros((2, T, Hkv, d), dtype=torch.bfloat16, device=dev)
+
+        def step(self):
+            _lib.add_rmsnorm(self.x, None, w, 1e-5, self.xn)
+            _lib.attn(self.xn.view(-1, Hq, d), kv, self.cu, kl, tab, self.max_q, 2000, self.out, ws)
+            _lib.kv_read(kv, self.cu, kl, tab, self.back[0], self.back[1])
+
+    jobs = [Job(41, cu, 40), Job(2, torch.tensor([0, 1, 2], dtype=torch.int32, device=dev), 1)]
+    graphs = []
+    for j in jobs:
+        j.step()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            j.step()
+        graphs.append(g)
+    for rep in range(3):
+        for j, g in zip(jobs, graphs):
+            j.x.normal_()
+            j.out.fill_(float("nan"))
+            j.back.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            got = [t.clone() for t in (j.xn, j.out, j.back)]
+            j.out.fill_(float("nan"))
+            j.step()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, c) for a, c in zip(got, (j.xn, j.out, j.back))), rep
+
+
 def test_no_tokens(gpu_ready):
     dev = gpu_ready
     b = Paged([0, 0], [5, 0], 1, 64, 16, "f16", "f16")
