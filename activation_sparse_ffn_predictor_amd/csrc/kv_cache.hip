@@ -20,6 +20,14 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v) {
   return v;
 }
 
+// b / TOP, correctly rounded (shown for every mantissa of 11 bits by exact arithmetic; below 2^-60 it does not matter)
+template <int TOP>
+__device__ __forceinline__ float over_top(float b) {
+  constexpr float R = 1.f / TOP;
+  const float q = b * R;
+  return fmaf(fmaf(-q, (float)TOP, b), R, q);
+}
+
 // x / s rounded so that rounding the result to a code rounds the exact quotient: cut towards zero, the last bit set if
 // anything was cut off. inv: 1 / s to within a few steps.
 __device__ __forceinline__ float div_sticky(float x, float s, float inv) {
@@ -142,7 +150,7 @@ __global__ __launch_bounds__(256) void k_kv_write(Kv kv, Seqs sq, const char* __
         const uint32_t big = group_max<LPR>((uint32_t)max(mx.x, mx.y));
         // a row that holds an infinity or NaN has no scale: it is stored as NaN (scale NaN, codes 0)
         const bool fin = big < (BF ? 0x7F80u : 0x7C00u);
-        float sc = lo16<BF>(big) / (KVM == 1 ? 127.f : 448.f);
+        float sc = over_top<KVM == 1 ? 127 : 448>(lo16<BF>(big));
         if (sc < KV_MIN_SCALE) sc = 0.f;
         const bool some = fin && sc > 0.f;
         uint2 c = encode8<KVM == 2>(f, some ? sc : 1.f);
@@ -207,14 +215,15 @@ template <int LPR>
 hipError_t go(bool write, const Kv& kv, int kvm, bool bf, const Seqs& sq, char* k, char* v, long ldk, long ldv,
               hipStream_t st) {
   constexpr int RPB = 256 / LPR;
-  // four tokens a thread where that still leaves 16 workgroups a compute unit
+  // two tokens a thread where that still leaves 32 workgroups a compute unit (54000 tokens of 40 heads read from e4m3:
+  // 155 -> 134 us; 4000 tokens written in 10000 workgroups: 33 us, in 5000 34)
   const long one = (long)((sq.T + RPB - 1) / RPB) * kv.hkv;
-  const bool four = one >= 4 * 16 * 256;
-  const int per = four ? 4 * RPB : RPB;
+  const bool two = one >= 2 * 32 * 256;
+  const int per = two ? 2 * RPB : RPB;
   const dim3 grid((unsigned)((sq.T + per - 1) / per) * kv.hkv);
 #define GO(K, KVM, BF)                                                                                        \
   do {                                                                                                        \
-    if (four) hipLaunchKernelGGL((K<LPR, KVM, BF, 4>), grid, dim3(256), 0, st, kv, sq, k, v, ldk, ldv);       \
+    if (two) hipLaunchKernelGGL((K<LPR, KVM, BF, 2>), grid, dim3(256), 0, st, kv, sq, k, v, ldk, ldv);        \
     else hipLaunchKernelGGL((K<LPR, KVM, BF, 1>), grid, dim3(256), 0, st, kv, sq, k, v, ldk, ldv);            \
   } while (0)
 #define PICK(K)                                    \
