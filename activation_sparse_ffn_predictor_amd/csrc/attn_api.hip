@@ -214,6 +214,8 @@ int sffn_add_rmsnorm(int x_type, const void* x, int64_t x_stride, int res_type, 
   if (s) return s;
   if (is8(y_type) && !y_scale) return fail(SFFN_ERR_NULL, "an 8-bit y needs y_scale");
   if ((w && !al(w, 16)) || (y_scale && !al(y_scale, 4))) return fail(SFFN_ERR_ALIGN, "add_rmsnorm: misaligned pointer");
+  if (res && res == res_out && res_stride != res_out_stride)
+    return fail(SFFN_ERR_ARG, "add_rmsnorm: res_out is res with another stride");
   if (y == x || y == res || y == res_out || x == res_out) return fail(SFFN_ERR_ARG, "add_rmsnorm: y or res_out overlaps an input");
   const hipError_t e = sffn_launch_add_rmsnorm(x, x_type, res, res_type, w, eps, T, D, x_stride, res_stride, y, y_type,
                                                y_scale, res_out, y_stride, res_out_stride, (hipStream_t)stream);

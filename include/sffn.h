@@ -225,7 +225,8 @@ int sffn_profile_begin(int kernel, int max_launches);
 int sffn_profile_end(float* ms, int max);
 
 /* ---------------------------------------------------------------------------------------------------------------
- * The attention half of a layer: residual norm, paged K/V cache, attention of new tokens over it.
+ * The attention half of a layer: residual norm, paged K/V cache, attention of new tokens over it. Errors, streams and
+ * checks as above; the stream belongs to the current device.
  *
  * Element types. 16-bit tensors (queries, new K / V, outputs) are SFFN_F16 or SFFN_BF16. A cache holds the same
  * 16-bit type, or 8-bit codes (SFFN_I8, SFFN_E4M3: OCP e4m3) with one fp32 scale per token and head:
@@ -299,7 +300,8 @@ int sffn_attn(sffn_kv cache, sffn_seqs seqs, int type, const void* q, int64_t q_
               void* stream);
 
 /* Root-mean-square norm with the residual's addition:
- *   h = x + res (fp32; h = x if res is NULL);  res_out = h rounded to res_type (if non-NULL; may be res itself)
+ *   h = x + res (fp32; h = x if res is NULL);  res_out = h rounded to res_type (if non-NULL; may be res itself,
+ *                                                           with its stride)
  *   y = h / sqrt(mean(h^2) + eps) * w          (from the unrounded h)
  * x, res, res_out [T, D] of SFFN_F32 / F16 / BF16 (res and res_out of one type), w [D] fp32 or NULL (1), y [T, D] of
  * any type; 8-bit y is codes with y_scale [T] fp32 as in the cache, per row and without its lower limit, computed in

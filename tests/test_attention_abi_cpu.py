@@ -104,7 +104,7 @@ def norm(**kw):
     (dict(D=60), 2), (dict(D=16392), 2), (dict(eps=-1.0), 6), (dict(eps=math.nan), 6), (dict(eps=math.inf), 6),
     (dict(x=None), 1), (dict(y=None), 1), (dict(ldx=56), 2), (dict(ldr=68), 2), (dict(ldy=60), 2), (dict(yt=3), 1),
     (dict(x=A + 4), 3), (dict(res=A + 4), 3), (dict(y=3 * A + 8), 3), (dict(w=A + 4), 3), (dict(yt=3, ys=A + 2), 3),
-    (dict(y=A), 6), (dict(y=2 * A), 6), (dict(ro=3 * A, ldro=64), 6), (dict(ro=A, ldro=64), 6), (dict(ro=4 * A, ldro=8), 2),
+    (dict(y=A), 6), (dict(y=2 * A), 6), (dict(ro=3 * A, ldro=64), 6), (dict(ro=A, ldro=64), 6), (dict(ro=2 * A, ldro=72), 6), (dict(ro=4 * A, ldro=8), 2),
     (dict(T=0, x=None, y=None), 0)])
 def test_norm_rejects(kw, st):
     assert norm(**kw) == st
