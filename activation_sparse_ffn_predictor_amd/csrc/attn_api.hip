@@ -74,7 +74,8 @@ bool attn_sizes_ok(int Hq, int Hkv, int d, int max_q) {
 bool few_rows(int G, int d, int max_q) { return (int64_t)max_q * G <= sffn_attn_few_rows(d); }
 
 // Over how many workgroups the keys of one sequence (few rows) or of one row tile are spread, at most one per FEW_LEAST
-// (MANY_LEAST) units of the keys that the longest sequence can see.
+// (MANY_LEAST) units of the keys that the longest sequence can see. Shares fill the chip, but their partial results are
+// written, read again and joined by a second kernel.
 int shares(int T, int S, int Hkv, int G, int d, int max_q, int max_kv, int window, int sinks) {
   const bool few = few_rows(G, d, max_q);
   int64_t see = std::max(1, std::min(max_kv, MAX_POS));
@@ -83,21 +84,42 @@ int shares(int T, int S, int Hkv, int G, int d, int max_q, int max_kv, int windo
     see = std::min(see, (int64_t)window + rows + std::min<int64_t>(sinks, see) + 128);
   }
   const int unit = few ? 1 << sffn::FEW_USH : 1 << sffn::many_ush(d), least = few ? sffn::FEW_LEAST : sffn::MANY_LEAST;
-  const int64_t most = std::max<int64_t>(1, (see + (int64_t)unit * least - 1) / ((int64_t)unit * least));
+  const int64_t chunk = (int64_t)unit * least;     // keys of the smallest share
+  const int64_t most = std::min<int64_t>((see + chunk - 1) / chunk, sffn::MAX_SHARES);
   // workgroups without shares; row tiles: the whole ones, and half a tile more for each further sequence's end
   const int64_t tiles = ((int64_t)T * G + sffn::MANY_ROWS - 1) / sffn::MANY_ROWS + (std::min(S, T) - 1) / 2;
   const int64_t blocks = (few ? (int64_t)S : tiles) * Hkv;
   const int64_t places = 512;                      // workgroups that run at once: two a compute unit
-  int64_t ns;
-  // As many shares as fill one round: partial results cost a join, and with many rows weigh as much as the keys (48
-  // sequences of 4 drafts on 128 heads of 64 over a window of 4096, bf16: one share 86 us, six 121; two sequences of
-  // 131072 on 8 K/V heads, e4m3: 32 shares 105 us, 64 109; 100 tokens on 64 heads over 100000, fp16: nine shares 424 us,
-  // ten 511).
-  if (!few || max_q * G > 16 || 2 * blocks <= places) ns = places / blocks;
-  // Few rows and most places taken already: shares of half a round's work even out sequences of different lengths (32
-  // sequences to 6000 tokens on 40 heads, int8: one share 187 us, two 169).
-  else ns = (3 * places + blocks - 1) / blocks;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({ns, most, sffn::MAX_SHARES}));
+  if (few) {
+    // Up to one and a half of the smallest share the join costs more than it saves (16 sequences of 700 on 8 K/V heads,
+    // fp16: one share 12.7 us, two 16.3; one sequence of 513: 9.9 and 12.5, of 1000: 14.2 and 13.1).
+    if (2 * see <= 3 * chunk) return 1;
+    // As many shares as fill one round; with many rows partial results weigh as much as the keys (48 sequences of 4
+    // drafts on 128 heads of 64 over a window of 4096, bf16: one share 86 us, six 121; two sequences of 131072 on 8 K/V
+    // heads, e4m3: 32 shares 105 us, 64 109). Few rows and most places taken already: shares of half a round's work even
+    // out sequences of different lengths (32 sequences to 6000 tokens on 40 heads, int8: one share 187 us, two 169).
+    int64_t ns = max_q * G > 16 || 2 * blocks <= places ? places / blocks : (3 * places + blocks - 1) / blocks;
+    ns = std::min(ns, most);
+    // Past one workgroup a compute unit a share of twice the smallest is enough (60 sequences of 2200 on 8 K/V heads,
+    // fp16: four shares 113 us, two 106; 32 of 1100: two 32, one 25).
+    if (ns * blocks > places / 2)
+      ns = std::max(std::min(ns, places / 2 / blocks), std::min(ns, (see + chunk) / (2 * chunk)));
+    return (int)std::max<int64_t>(1, ns);
+  }
+  // Row tiles: one share, a round of one workgroup a compute unit or a round of two, whichever a sum of measured costs
+  // puts first: a key takes a tile of head size 128 about 20 ns, half as much again where two share a compute unit; a join
+  // starts in 4 us and moves each partial result out and in at 4 TB/s. 64 heads of 128 on 8, fp16: 300 tokens over 300:
+  // one share 14 us, two 23; over 1000 one 29, three 35; over 2500 one 59, three 51; 100 tokens over 4000: four shares
+  // 36 us, nine 41; over 100000: nine 424, ten 511 (more than a round).
+  int64_t best = 1;
+  double cost = 0;
+  for (const int64_t wgs : {(int64_t)0, places / 2, places}) {
+    const int64_t ns = std::max<int64_t>(1, std::min(most, wgs / blocks));
+    double t = (double)see / ns * (d + 64) * 0.104 * (ns * blocks > places / 2 ? 1.5 : 1.0);
+    if (ns > 1) t += 4000.0 + 0.002 * ns * T * Hkv * G * d;
+    if (wgs == 0 || t < cost) best = ns, cost = t;
+  }
+  return (int)best;
 }
 size_t po_bytes(int T, int Hq, int d, int ns) { return align256((size_t)T * Hq * ns * d * sizeof(float)); }
 

@@ -390,6 +390,43 @@ def test_split_hint_changes_only_the_split(gpu_ready):
         assert torch.equal(no_lse[0], run_attn(b, q, 8, gpu_ready)[0])
 
 
+SPREAD = {
+    "single wide": ([1, 1], [2500, 700], 1, 4, 256, 16, 0, 0),
+    "drafts 48": ([3, 2], [3000, 900], 2, 8, 48, 32, 0, 0),
+    "drafts 208, window": ([2, 1], [5000, 4000], 1, 3, 208, 16, 3000, 5),
+    "chunk 80": ([50], [4000], 1, 4, 80, 64, 0, 0),
+    "chunk wide": ([20], [2500], 1, 4, 208, 16, 0, 0),
+    "chunk wide, window": ([33, 7], [3000, 2200], 1, 4, 256, 16, 1500, 9),
+}
+
+
+@pytest.mark.parametrize("qt,kvt", TYPES)
+@pytest.mark.parametrize("name", SPREAD)
+def test_keys_spread_over_workgroups(gpu_ready, name, qt, kvt):
+    """Keys in several parts, then with pages missing from whole parts, then with infinities and NaN where no row
+    looks (16-bit caches: and where one does)."""
+    ns, ks, Hkv, Hq, d, page, window, sinks = SPREAD[name]
+    assert _lib.attn_workspace_size(sum(ns), len(ns), Hq, Hkv, d, max(ns), max(ks), window, sinks) > 0
+    say(f"[spread {name} {qt} {kvt}]")
+    b = Paged(ns, ks, Hkv, d, page, qt, kvt, seed=len(name), pad=1)
+    check_attn(b, Hq, gpu_ready, window=window, sinks=sinks)
+    table = b.table.clone()
+    b.table[0, 600 // page:(ks[0] - 300) // page] = -1
+    check_attn(b, Hq, gpu_ready, window=window, sinks=sinks)
+    b.table = table
+    x = torch.randn((2, b.n_pages, Hkv, page, d), generator=b.g).to(DT[qt])
+    used = torch.zeros((b.n_pages, page), dtype=torch.bool)
+    for s, k in enumerate(ks):
+        for p in range(k):
+            used[int(table[s, p // page]), p % page] = True
+    x.transpose(2, 3)[:, ~used] = math.nan
+    if kvt == qt:
+        for i, p in enumerate([ks[0] - 1, 600, ks[0] - 700]):
+            x[1, int(table[0, p // page]), 0, p % page, 10 * i] = (math.inf, -math.inf, math.nan)[i]
+    b.set_values(x)
+    check_attn(b, Hq, gpu_ready, window=window, sinks=sinks)
+
+
 def test_strided_queries_and_outputs(gpu_ready):
     dev = gpu_ready
     for n in (1, 60):
