@@ -2,7 +2,7 @@
 //
 // Both are bound by memory, each byte moved once; a row of a head is a few lanes' work, so that its maximum needs no LDS
 // and neighbouring tokens of a head fill neighbouring slots. Measured: 4000 tokens of 40 heads of 128 written in 30 us as
-// bf16 (5.3 TB/s) and 32 us as e4m3 (3.9 TB/s; 24.7 us without the encoding, which is what then bounds it); 54000 tokens
+// bf16 (5.3 TB/s) and as e4m3 (4.1 TB/s; 24.7 us without the encoding, which is what then bounds it); 54000 tokens
 // read from e4m3 to bf16, 703 MB in 134 to 143 us (box to box; 5.0 to 5.3 TB/s).
 #include "attn.h"
 
@@ -33,19 +33,6 @@ __device__ __forceinline__ float over_top(float b) {
   return fmaf(fmaf(-q, (float)TOP, b), R, q);
 }
 
-// x / s rounded so that rounding the result to a code rounds the exact quotient: cut towards zero, the last bit set if
-// anything was cut off. inv: 1 / s to within a few steps.
-__device__ __forceinline__ float div_sticky(float x, float s, float inv) {
-  float q = x * inv;
-  q = fmaf(fmaf(-q, s, x), inv, q);                          // within one step of the quotient
-  const float e = fmaf(-q, s, x);                            // exact remainder
-  if (e != 0.f && q != 0.f) {
-    uint32_t b = __float_as_uint(q);
-    if ((e < 0.f) != (q < 0.f)) b -= 1;                      // |q| is too large: the value below
-    q = __uint_as_float(b | 1u);
-  }
-  return q;
-}
 // four codes of x * f, rounded to nearest even
 template <bool E4M3>
 __device__ __forceinline__ uint32_t encode4(const float* x, float f) {
@@ -60,17 +47,36 @@ __device__ __forceinline__ uint32_t encode4(const float* x, float f) {
                                  __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u), 0x05040100u);
   }
 }
-// Codes of x[0 .. 8) / s, rounded to nearest even from the exact quotients. 1 / s lies between two fp32 factors; where
-// both give the same codes, these are the quotients' codes, and almost always they do. Else (in one of the wave's rows)
-// exact remainders decide. Quotients are at most top (1 + 2^-23) by the scale's making: nothing needs a limit.
+// A value that rounds to the same code as the exact quotient x / s. inv: 1 / s to within a few steps. A code or the middle
+// between two of them has at most 5 significant bits (e4m3) or is a multiple of 1/2 (int8): h is the one nearest to the
+// quotient, and the sign of the remainder x - h s (one rounding: exact) tells on which side of it the quotient lies.
 template <bool E4M3>
+__device__ __forceinline__ float beside(float x, float s, float inv) {
+  const float h = E4M3 ? __uint_as_float((__float_as_uint(x * inv) + 0x40000u) & 0xFFF80000u)
+                       : fmaf(x, inv, 6291456.f) - 6291456.f;      // 1.5 * 2^22: steps of 1/2
+  constexpr float T = E4M3 ? 0x1p-15f : 0x1p-8f;   // 2^-15 is one step at 448; what is nearer to 0 than 2^-10 is 0
+  return h + __builtin_amdgcn_fmed3f(fmaf(-h, s, x) * 0x1p100f, -T, T);
+}
+// Codes of x[0 .. 8) / s, rounded to nearest even from the exact quotients. 1 / s lies between two fp32 factors; where
+// both give the same codes, these are the quotients' codes, else (in one of the wave's rows) remainders decide. A value
+// with the largest one's mantissa is a middle or within a step of one, which every second wave of bf16 rows holds: those
+// go to the remainders at once (4000 tokens of 40 heads of 128, bf16 to e4m3: 31.9 -> 30.0 us; 3300 from fp16 to int8:
+// with the factors 21.2 us, without 22.6). Quotients are at most top (1 + 2^-23) by the scale's making: nothing needs a
+// limit.
+template <bool E4M3, bool BF>
 __device__ __forceinline__ uint2 encode8(const float* x, float s) {
-  const float inv = __builtin_amdgcn_rcpf(s), lo = inv * (1.f - 0x1p-20f), hi = inv * (1.f + 0x1p-20f);
-  uint2 c = make_uint2(encode4<E4M3>(x, lo), encode4<E4M3>(x + 4, lo));
-  if (__any(((c.x ^ encode4<E4M3>(x, hi)) | (c.y ^ encode4<E4M3>(x + 4, hi))) != 0)) {
+  const float inv = __builtin_amdgcn_rcpf(s);
+  uint2 c = make_uint2(0, 0);
+  bool same = false;
+  if constexpr (!BF) {
+    const float lo = inv * (1.f - 0x1p-20f), hi = inv * (1.f + 0x1p-20f);
+    c = make_uint2(encode4<E4M3>(x, lo), encode4<E4M3>(x + 4, lo));
+    same = !__any(((c.x ^ encode4<E4M3>(x, hi)) | (c.y ^ encode4<E4M3>(x + 4, hi))) != 0);
+  }
+  if (!same) {
     float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = div_sticky(x[i], s, inv);
+    for (int i = 0; i < 8; ++i) q[i] = beside<E4M3>(x[i], s, inv);
     c = make_uint2(encode4<E4M3>(q, 1.f), encode4<E4M3>(q + 4, 1.f));
   }
   return c;
@@ -158,7 +164,7 @@ __global__ __launch_bounds__(256) void k_kv_write(Kv kv, Seqs sq, const char* __
         float sc = over_top<KVM == 1 ? 127 : 448>(lo16<BF>(big));
         if (sc < KV_MIN_SCALE) sc = 0.f;
         const bool some = fin && sc > 0.f;
-        uint2 c = encode8<KVM == 2>(f, some ? sc : 1.f);
+        uint2 c = encode8<KVM == 2, BF>(f, some ? sc : 1.f);
         if (!some) c = make_uint2(0, 0);
         if (row[p] >= 0 && act) {
           *reinterpret_cast<uint2*>(dst + row[p] * kv.d + lane * 8) = c;

@@ -160,6 +160,39 @@ def test_write_then_read(gpu_ready, qt, kvt, d, Hkv, page, bi):
         assert (out[m, b.N:] == 3.0).all()
 
 
+@pytest.mark.parametrize("qt", ["f16", "bf16"])
+@pytest.mark.parametrize("kvt", ["i8", "e4m3"])
+def test_write_rounds_exact_quotients(gpu_ready, qt, kvt):
+    """Every mantissa under largest values of many, at sizes from a row's largest value to a 2^-12th of it: quotients
+    on the middle of two codes and a few 2^-30ths beside it are among them."""
+    dev = gpu_ready
+    bits = 7 if qt == "bf16" else 10
+    man = 1 + torch.arange(2 ** bits, dtype=torch.float64) / 2 ** bits
+    big = man[::1 if qt == "bf16" else 37]
+    x = man.view(-1, 128).repeat(len(big) * 13, 1)                # [row, 128]
+    per = len(x) // (len(big) * 13)
+    e = torch.arange(13).repeat_interleave(per).repeat(len(big))
+    b = big.repeat_interleave(13 * per)
+    x = x * torch.pow(torch.tensor(2.0, dtype=torch.float64), -e.double())[:, None]
+    x = torch.where(x > b[:, None], x / 2, x)
+    x[:, ::2] *= -1
+    x[:, 5] = b
+    for size in ([1.0] if qt == "f16" else [1.0, 2.0 ** 126, 2.0 ** -50]):
+        v = (x * size).to(DT[qt]).view(-1, 1, 128)
+        assert torch.equal(v.double().view(-1, 128), x * size)
+        T, page = len(v), 64
+        n = -(-T // page)
+        kv = tuple(torch.zeros((n, 1, page, 128), device=dev).to(DT[kvt]) for _ in range(2))
+        kv += tuple(torch.zeros((n, 1, page), device=dev) for _ in range(2))
+        cu, kl, tab = (torch.tensor(t, dtype=torch.int32, device=dev) for t in ([0, T], [T], [list(range(n))]))
+        _lib.kv_write(v.to(dev), v.to(dev), kv, cu, kl, tab)
+        torch.cuda.synchronize()
+        c, sc = quant_rows(v.double().view(-1, 128), kvt)
+        for m in range(2):
+            assert torch.equal(f64(kv[m]).view(-1, 128)[:T], c), f"part {m} size {size}"
+            assert torch.equal(kv[2 + m].cpu().view(-1)[:T], sc)
+
+
 @pytest.mark.parametrize("kvt", ["f16", "i8", "e4m3"])
 def test_write_nothing_to_bad_places(gpu_ready, kvt):
     """Pages outside the cache, positions outside the table row and before the first token: nothing is written there
