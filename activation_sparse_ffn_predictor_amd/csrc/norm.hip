@@ -74,6 +74,26 @@ __device__ __forceinline__ uint32_t code4(const double* v) {
   }
 }
 
+// sum of a row's squares in 64 bits, the same in every thread (part: LDS of a double a wave)
+template <int WPR, int CH>
+__device__ __forceinline__ double square_sum(const float (&h)[CH][8], double* part, int wv, int lane) {
+  double q = 0.0;
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) q = fma((double)h[c][k], (double)h[c][k], q);
+#pragma unroll
+  for (int o = 32; o; o >>= 1) q += shfl_xor_d(q, o);
+  if (WPR > 1) {
+    if (lane == 0) part[wv] = q;
+    __syncthreads();
+    q = part[0];
+#pragma unroll
+    for (int k = 1; k < WPR; ++k) q += part[k];
+  }
+  return q;
+}
+
 // WPR waves a row, CH chunks of 8 elements per lane: D <= 512 * WPR * CH. One chunk a lane wherever 1024 threads hold a
 // row (4099 rows of 8192 to int8: 97 us on 4 waves, 93 on 8, 81 on 16). The row stays in registers
 // between its sum and its output, so every byte is read and written once. YQ: 0 = 16 / 32 bits out, 1 = int8,
@@ -143,29 +163,27 @@ __global__ __launch_bounds__(WPR > 4 ? WPR * 64 : 256) void k_add_rmsnorm(const 
 #pragma unroll
       for (int k = 1; k < WPR; ++k) q += r[k];
     }
-    const float rs = 1.0f / sqrtf(q / (float)D + (float)eps);
+    const float mean = q / (float)D + (float)eps;
+    if (mean >= 1e-30f && mean < INFINITY) {
+      const float rs = 1.0f / sqrtf(mean);
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[c][k] = h[c][k] * rs * g[c][k];
+    } else {                                // squares outside fp32's range (or a zero row without eps): again in 64 bits
+      const double rs = 1.0 / sqrt(square_sum<WPR, CH>(h, red[1], wv, lane) / (double)D + eps);
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[c][k] = (float)((double)h[c][k] * rs * (double)g[c][k]);
+    }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int i = (c * WPR * 64 + t) * 8;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) h[c][k] = h[c][k] * rs * g[c][k];
       if (i < D) store8(y, yt, row * ldy + i, h[c]);
     }
   } else {
-    double q = 0.0;
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) q = fma((double)h[c][k], (double)h[c][k], q);
-#pragma unroll
-    for (int o = 32; o; o >>= 1) q += shfl_xor_d(q, o);
-    if (WPR > 1) {
-      if (lane == 0) red[0][wv] = q;
-      __syncthreads();
-      q = red[0][0];
-#pragma unroll
-      for (int k = 1; k < WPR; ++k) q += red[0][k];
-    }
+    const double q = square_sum<WPR, CH>(h, red[0], wv, lane);
     const double rs = 1.0 / sqrt(q / (double)D + eps);
     double big = 0.0;                       // largest |h w| (times rs below); NaN is looked for apart
     bool bad = false;
@@ -209,6 +227,19 @@ hipError_t sffn_launch_add_rmsnorm(const void* x, int xt, const void* res, int r
                                    int D, long ldx, long ldr, void* y, int yt, float* ys, void* res_out, long ldy,
                                    long ldro, hipStream_t st) {
   const int yq = yt == T_I8 ? 1 : yt == T_E4M3 ? 2 : 0;
+  // a launch holds fewer than 2^32 threads, 4 million rows of 1024: more rows go in several
+  constexpr int MOST = 1 << 21;
+  if (T > MOST) {
+    auto size = [](int t) { return t == T_F32 ? 4 : t == T_I8 || t == T_E4M3 ? 1 : 2; };
+    hipError_t e = hipSuccess;
+    for (int r = 0; r < T && e == hipSuccess; r += MOST) {
+      const long o = r;
+      e = sffn_launch_add_rmsnorm((const char*)x + o * ldx * size(xt), xt, res ? (const char*)res + o * ldr * size(rt) : nullptr, rt,
+                                  w, eps, T - r < MOST ? T - r : MOST, D, ldx, ldr, (char*)y + o * ldy * size(yt), yt,
+                                  ys ? ys + o : nullptr, res_out ? (char*)res_out + o * ldro * size(rt) : nullptr, ldy, ldro, st);
+    }
+    return e;
+  }
 #define GO(WPR, CH, YQ)                                                                                           \
   hipLaunchKernelGGL((k_add_rmsnorm<WPR, CH, YQ>), dim3(WPR == 1 ? (T + 3) / 4 : T), dim3(WPR > 4 ? WPR * 64 : 256), 0, st, x, xt, \
                      res, rt, \

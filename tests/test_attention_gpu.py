@@ -103,6 +103,43 @@ def test_norm_edges(gpu_ready, yt):
             assert (outs[0][0][row] == 0).all() and math.isnan(outs[0][1][row].item())
 
 
+@pytest.mark.parametrize("xt", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 640, 4096, 8192, 16384])
+def test_norm_of_any_finite_size(gpu_ready, D, xt):
+    """Rows whose squares leave fp32's range at either end, beside ordinary ones."""
+    dev = gpu_ready
+    size = torch.tensor([1.0, 1e25, 3e36, 1e18, 1e-12, 1e-18, 1e-25, 1e-36], dtype=torch.float64)
+    x = (torch.randn((8, D), generator=torch.Generator().manual_seed(D), dtype=torch.float64) * size[:, None]).to(DT[xt])
+    w = 1 + 0.3 * torch.randn(D, generator=torch.Generator().manual_seed(1))
+    for eps in (0.0, 1e-6, 1e-40):
+        _, y = norm_ref(x, None, w, eps)
+        for yt in ("f32", "bf16"):
+            yo = torch.zeros((8, D), device=dev).to(DT[yt])
+            _lib.add_rmsnorm(x.to(dev), None, w.to(dev), eps, yo)
+            torch.cuda.synchronize()
+            # as above; values below the smallest normal one may be flushed
+            tol = (D / 2 + 8) * 2.0 ** -24 * y.abs() + half_step(yt) * y.abs() * 1.01
+            assert_near(yo.float(), y, tol + torch.finfo(DT[yt]).tiny, f"y {xt} {yt} {eps}")
+
+
+def test_norm_of_more_rows_than_a_launch_holds(gpu_ready):
+    T, D = (1 << 22) + 5, 4104
+    if torch.cuda.mem_get_info(gpu_ready)[0] < T * D * 4:
+        pytest.skip("needs 70 GB")
+    x = torch.empty((T, D), device=gpu_ready, dtype=torch.float16).fill_(0.25)
+    y, ys = torch.empty((T, D), device=gpu_ready, dtype=torch.int8), torch.zeros(T, device=gpu_ready)
+    rows = [0, 1, (1 << 21) - 1, 1 << 21, (1 << 22) - 1, 1 << 22, T - 1]
+    for r in rows:
+        x[r, ::2] = -0.5 * (1 + r % 7)
+    _lib.add_rmsnorm(x, None, None, 1e-5, y, y_scale=ys)
+    torch.cuda.synchronize()
+    for r in rows + [7, T - 2]:
+        c, s = quant_rows(norm_ref(x[r:r + 1].cpu(), None, None, 1e-5)[1], "i8", floor=0.0)
+        assert torch.equal(f64(y[r:r + 1]), c) and ys[r].item() == s.item(), r
+    del x, y
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------------------------------------ write and read
 CACHES = [("f16", "f16", 128, 8, 16), ("bf16", "bf16", 64, 1, 64), ("f16", "i8", 128, 3, 16), ("bf16", "i8", 16, 2, 32),
           ("f16", "e4m3", 80, 5, 128), ("bf16", "e4m3", 256, 2, 16), ("f16", "f16", 24, 2, 16), ("bf16", "i8", 112, 40, 32),
