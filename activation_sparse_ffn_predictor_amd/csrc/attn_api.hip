@@ -63,6 +63,14 @@ int check_rows(const char* what, const void* p, int64_t stride, int64_t width) {
   return SFFN_OK;
 }
 
+// kv_write, kv_read: fewer than 2^32 threads, a thread taking 8 elements of two tokens
+int check_move(const sffn_kv& c, const sffn_seqs& q) {
+  const int lanes = c.head_dim <= 32 ? 4 : c.head_dim <= 64 ? 8 : c.head_dim <= 128 ? 16 : 32, tokens = 2 * 256 / lanes;
+  if ((int64_t)((q.T + tokens - 1) / tokens) * c.n_kv_heads >= ((int64_t)1 << 24))
+    return fail(SFFN_ERR_SHAPE, "T=%d, n_kv_heads=%d, head_dim=%d: too many elements", q.T, c.n_kv_heads, c.head_dim);
+  return SFFN_OK;
+}
+
 sffn::Kv kv_of(const sffn_kv& c) {
   return {(char*)c.k, (char*)c.v, c.k_scale, c.v_scale, c.n_pages, __builtin_ctz(c.page), c.n_kv_heads, c.head_dim};
 }
@@ -90,6 +98,7 @@ int shares(int T, int S, int Hkv, int G, int d, int max_q, int max_kv, int windo
   const int64_t tiles = ((int64_t)T * G + sffn::MANY_ROWS - 1) / sffn::MANY_ROWS + (std::min(S, T) - 1) / 2;
   const int64_t blocks = (few ? (int64_t)S : tiles) * Hkv;
   const int64_t places = 512;                      // workgroups that run at once: two a compute unit
+  if ((int64_t)T * Hkv * G >= ((int64_t)1 << 24)) return 1;          // one launch joins: fewer than 2^32 threads
   if (few) {
     // Up to one and a half of the smallest share the join costs more than it saves (16 sequences of 700 on 8 K/V heads,
     // fp16: one share 12.7 us, two 16.3; one sequence of 513: 9.9 and 12.5, of 1000: 14.2 and 13.1).
@@ -135,7 +144,7 @@ int sffn_kv_write(sffn_kv c, sffn_seqs q, int type, const void* k, int64_t k_str
   if (!s && q.T) s = check_rows("k", k, k_stride, (int64_t)c.n_kv_heads * c.head_dim);
   if (!s && q.T) s = check_rows("v", v, v_stride, (int64_t)c.n_kv_heads * c.head_dim);
   if (s || q.T == 0) return s;
-  if ((int64_t)((q.T + 7) / 8) * c.n_kv_heads >= ((int64_t)1 << 31)) return fail(SFFN_ERR_SHAPE, "T * n_kv_heads too large");
+  if ((s = check_move(c, q))) return s;
   const hipError_t e = sffn_launch_kv_write(kv_of(c), c.type, seqs_of(q), k, v, type, k_stride, v_stride, (hipStream_t)stream);
   return e == hipSuccess ? SFFN_OK : sffn_err_hip(e, "kv_write launch");
 }
@@ -147,7 +156,7 @@ int sffn_kv_read(sffn_kv c, sffn_seqs q, int type, void* k, int64_t k_stride, vo
   if (!s && q.T) s = check_rows("k", k, k_stride, (int64_t)c.n_kv_heads * c.head_dim);
   if (!s && q.T) s = check_rows("v", v, v_stride, (int64_t)c.n_kv_heads * c.head_dim);
   if (s || q.T == 0) return s;
-  if ((int64_t)((q.T + 7) / 8) * c.n_kv_heads >= ((int64_t)1 << 31)) return fail(SFFN_ERR_SHAPE, "T * n_kv_heads too large");
+  if ((s = check_move(c, q))) return s;
   const hipError_t e = sffn_launch_kv_read(kv_of(c), c.type, seqs_of(q), k, v, type, k_stride, v_stride, (hipStream_t)stream);
   return e == hipSuccess ? SFFN_OK : sffn_err_hip(e, "kv_read launch");
 }
@@ -192,8 +201,9 @@ int sffn_attn(sffn_kv c, sffn_seqs q, int type, const void* qp, int64_t q_stride
     if (ws_bytes < need) return fail(SFFN_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, need);
   }
   const bool few = few_rows(G, c.head_dim, max_q);
-  if (!few && ((int64_t)q.T * G / sffn::MANY_ROWS + std::min(q.S, q.T)) * c.n_kv_heads >= ((int64_t)1 << 31))
-    return fail(SFFN_ERR_SHAPE, "T * Hq too large");
+  // fewer than 2^32 threads a launch
+  if (!few && ((int64_t)q.T * G / sffn::MANY_ROWS + std::min(q.S, q.T)) * c.n_kv_heads >= ((int64_t)1 << 24))
+    return fail(SFFN_ERR_SHAPE, "T=%d, S=%d, Hq=%d: too many row tiles", q.T, q.S, Hq);
   sffn::AttnArgs a;
   a.q = (const char*)qp;
   a.out = (char*)out;

@@ -264,13 +264,14 @@ typedef struct {
 
 /* New tokens' K and V into the cache. k, v: [T, n_kv_heads, head_dim] of a 16-bit `type` (the cache's own if that has
  * 16 bits), tokens k_stride and v_stride elements apart (multiples of 8, at least n_kv_heads * head_dim, so columns
- * of a fused Q/K/V product serve as they are). Two tokens of one call that share a slot (sequences whose tables
+ * of a fused Q/K/V product serve as they are). T * n_kv_heads * head_dim, the last rounded up to 32, 64, 128 or 256,
+ * < 2^36. Two tokens of one call that share a slot (sequences whose tables
  * share the page that is written) leave it undefined. One kernel. */
 int sffn_kv_write(sffn_kv cache, sffn_seqs seqs, int type, const void* k, int64_t k_stride, const void* v,
                   int64_t v_stride, void* stream);
 
 /* The other way: the rows named by seqs (cu[s + 1] - cu[s] = kv_len[s] takes whole sequences) as contiguous K and V,
- * code * scale rounded once to `type`; a 16-bit cache is copied. Rows whose position holds no token stay as they
+ * code * scale rounded once to `type`; a 16-bit cache is copied. Limits as above. Rows whose position holds no token stay as they
  * were. One kernel. */
 int sffn_kv_read(sffn_kv cache, sffn_seqs seqs, int type, void* k, int64_t k_stride, void* v, int64_t v_stride,
                  void* stream);
@@ -290,7 +291,7 @@ int sffn_kv_read(sffn_kv cache, sffn_seqs seqs, int type, void* k, int64_t k_str
  * (SFFN_ATTN_FEW), more run the tile kernel (SFFN_ATTN_MANY); where keys are spread a second kernel joins the parts
  * in a fixed order, so the same call gives the same bits. The workspace needs sffn_attn_workspace_size bytes of
  * the same sizes (0: none needed, ws may be NULL); it holds nothing between calls, and calls that overlap in time
- * need separate ones. Hq * T < 2^31. */
+ * need separate ones. Hq * T < 2^31; for the tile kernel Hq * T / 128 + n_kv_heads * min(S, T) < 2^24. */
 enum { SFFN_ATTN_FEW = 0, SFFN_ATTN_MANY = 1 };
 int sffn_attn_path(int Hq, int n_kv_heads, int head_dim, int max_q);   /* -1 for bad sizes */
 size_t sffn_attn_workspace_size(int T, int S, int Hq, int n_kv_heads, int head_dim, int max_q, int max_kv, int window,
@@ -306,7 +307,7 @@ int sffn_attn(sffn_kv cache, sffn_seqs seqs, int type, const void* q, int64_t q_
  * x, res, res_out [T, D] of SFFN_F32 / F16 / BF16 (res and res_out of one type), w [D] fp32 or NULL (1), y [T, D] of
  * any type; 8-bit y is codes with y_scale [T] fp32 as in the cache, per row and without its lower limit, computed in
  * 64 bits from h on. Row strides in elements, multiples of 8, at least D. D as elsewhere:
- * 8 <= D <= 16384, D % 8 == 0. eps >= 0. y overlaps no input. 0 <= T <= 2^24. One kernel. */
+ * 8 <= D <= 16384, D % 8 == 0. eps >= 0. y overlaps no input. 0 <= T <= 2^24. One kernel for each 2^21 rows. */
 int sffn_add_rmsnorm(int x_type, const void* x, int64_t x_stride, int res_type, const void* res, int64_t res_stride,
                      const float* w, double eps, int T, int D, int y_type, void* y, int64_t y_stride, float* y_scale,
                      void* res_out, int64_t res_out_stride, void* stream);

@@ -92,6 +92,19 @@ def test_attn_sizes():
     assert ws(0, 1, 8, 8, 64, 1, 10) == 0 and ws(1, 1, 8, 3, 64, 1, 10) == 0 and ws(1, 1, 8, 8, 64, 1, 10, -1) == 0
 
 
+def test_launch_limits():
+    """More threads than one launch holds: refused, or (partial results of that many rows) not asked for."""
+    wide = dict(n_kv_heads=64, head_dim=256)
+    for fn in ("sffn_kv_write", "sffn_kv_read"):
+        assert move(fn, c=kv(**wide), s=sq(T=1 << 24), k_stride=64 * 256, v_stride=64 * 256) == 2
+        assert "too many" in _lib.lib().sffn_last_error().decode()
+    assert attn(c=kv(n_kv_heads=126, head_dim=16), s=sq(T=1 << 24, S=65535), Hq=126, max_q=1 << 20, q_stride=126 * 16,
+                out_stride=126 * 16) == 2
+    assert "too many" in _lib.lib().sffn_last_error().decode()
+    assert _lib.attn_workspace_size(1 << 17, 1, 64, 8, 128, 1, 131072) > 0
+    assert _lib.attn_workspace_size(1 << 18, 1, 64, 8, 128, 1, 131072) == 0
+
+
 def norm(**kw):
     a = dict(xt=0, x=A, ldx=64, rt=0, res=2 * A, ldr=64, w=A, eps=1e-5, T=3, D=64, yt=1, y=3 * A, ldy=64, ys=None, ro=None,
              ldro=0, stream=None)
