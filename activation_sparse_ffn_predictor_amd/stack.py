@@ -147,6 +147,9 @@ class SparseFFNStack:
         T = x.shape[0]
         if self.attn is None or not 0 <= s < self.max_batch or not 1 <= T <= self.max_batch:
             raise ValueError(f"prompt: sequence {s}, {T} tokens (at most {self.max_batch}; the stack needs attention)")
+        if x.dim() != 2 or x.shape[1] != self.wl.D or x.dtype != torch.float32 or x.device != self.out.device:
+            raise ValueError(f"prompt: x is fp32 [T, {self.wl.D}] on {self.out.device}")
+        x = x.contiguous()
         self._room(s, T)
         cu = self.cu_prompt.setdefault(T, torch.tensor([0, T], dtype=torch.int32, device=self.device))
         self.kv_len[s:s + 1] += T

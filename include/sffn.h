@@ -284,7 +284,8 @@ int sffn_kv_read(sffn_kv cache, sffn_seqs seqs, int type, void* k, int64_t k_str
  * q [T, Hq, head_dim] of a 16-bit `type` (the cache's own if that has 16 bits), out likewise, tokens q_stride and
  * out_stride elements apart (multiples of 8). lse [T, Hq] fp32 or NULL: the natural logarithm of the softmax's sum
  * (-infinity for a token that sees nothing). Scores, sums and accumulators are fp32; the weights enter the second
- * product as 16-bit values, and 8-bit codes enter both products exactly.
+ * product as 16-bit values, and 8-bit codes enter both products exactly. Over an 8-bit cache bf16 queries enter the
+ * first one in steps of at most 2^-39 of the largest finite element among the rows of a workgroup.
  * max_q: at least the largest number of new tokens of one sequence (tokens past it are not computed and their rows
  * stay as they were). max_kv: about the largest kv_len; it decides only over how many workgroups a sequence's keys
  * are spread. Up to 32 rows max_q * Hq / n_kv_heads (64 for head_dim <= 64, 16 for head_dim > 128) run the few-row kernel

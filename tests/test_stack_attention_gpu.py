@@ -139,3 +139,17 @@ def test_no_room_is_refused(gpu_ready):
     plain = SparseFFNStack(sg.workload("toy_relu"), gpu_ready)
     with pytest.raises(ValueError):
         plain.prompt(0, x[:1])
+
+
+def test_prompt_checks_its_input_first(gpu_ready):
+    """A refused prompt leaves the sequence as it was; rows need not be dense."""
+    st = toy(gpu_ready, "f16", max_batch=4, max_len=16, layers=1)
+    wide = torch.randn((4, 1032), device=gpu_ready, generator=torch.Generator(gpu_ready).manual_seed(2))
+    for x in (wide, wide[:, :504], wide[:, :512].half(), wide[:, :512].cpu(), wide[0, :512][None, None]):
+        with pytest.raises(ValueError):
+            st.prompt(0, x)
+    assert st.lens == [0, 0, 0, 0] and (st.kv_len == 0).all()
+    st.prompt(0, wide[:, 3:515])
+    a = st.out.clone()
+    st.prompt(1, wide[:, 3:515].contiguous())
+    assert torch.equal(a, st.out) and st.lens == [4, 4, 0, 0]
