@@ -350,6 +350,27 @@ def test_attention(gpu_ready, name, qt, kvt):
 
 
 @pytest.mark.parametrize("qt,kvt", TYPES)
+@pytest.mark.parametrize("d", [16, 64, 80, 96, 112, 128, 144, 192, 208, 256])
+def test_chunks_of_every_padding(gpu_ready, d, qt, kvt):
+    """Head sizes at both ends of each padded one; columns past a head hold NaN or another head's values."""
+    say(f"[chunk d={d} {qt} {kvt}]")
+    b = Paged([70, 3], [150, 90], 2, d, 16, qt, kvt, seed=d, pad=1, v_scale=0.5)
+    check_attn(b, 6, gpu_ready, window=100, sinks=3)
+    q = (torch.randn((b.T, 6, d), generator=b.g)).to(DT[qt])
+    wide = torch.full((b.T, 6 * d + 64), math.nan).to(DT[qt]).to(gpu_ready)
+    wide[:, :6 * d] = q.flatten(1).to(gpu_ready)
+    kv, cu, kl, tab = b.gpu(gpu_ready)
+    out = torch.full((b.T, 6 * d + 64), 3.0).to(DT[qt]).to(gpu_ready)
+    need = _lib.attn_workspace_size(b.T, b.S, 6, 2, d, 70, 150)
+    ws = torch.full((need + 256,), 255, dtype=torch.uint8, device=gpu_ready)
+    _lib.attn(wide[:, :6 * d].unflatten(1, (6, d)), kv, cu, kl, tab, 70, 150, out[:, :6 * d].unflatten(1, (6, d)), ws)
+    torch.cuda.synchronize()
+    o, l, to, tl = attention(b, q, 6, d ** -0.5)
+    assert_near(out[:b.N, :6 * d].unflatten(1, (6, d)), o[:b.N], to[:b.N], "out")
+    assert (out[:, 6 * d:] == 3.0).all() and (out[b.N:] == 3.0).all()
+
+
+@pytest.mark.parametrize("qt,kvt", TYPES)
 def test_attention_sizes_of_values(gpu_ready, qt, kvt):
     """Values and queries far from 1: small ones keep their relative precision, one row is far larger than its
     neighbours, another holds only zeros."""
