@@ -422,8 +422,10 @@ hipError_t sffn_launch_attn_few(const AttnArgs& a, int qt, int kvt, hipStream_t 
   const int kvm = kvt == T_I8 ? 1 : kvt == T_E4M3 ? 2 : 0;
   const int rows = a.max_q * a.G;
   // eight waves a workgroup where there is at most one workgroup a compute unit (500 keys, 64 heads on 8: 12.2 us with four
-  // waves, two shares and a join, 9.6 with eight and no join); four otherwise, two workgroups a compute unit
-  const bool wide = (long)grid.x * grid.y * grid.z <= 256;
+  // waves, two shares and a join, 9.6 with eight and no join); four otherwise, two workgroups a compute unit. Four for
+  // 16-bit rows of head sizes over 128 too: eight leave a wave too few registers there (30 sequences of 700, size 256, fp16:
+  // 50 us with eight, 39.5 with four; int8, 16 of 1000: 21 and 23)
+  const bool wide = (a.kv.d <= 128 || kvm) && (long)grid.x * grid.y * grid.z <= 256;
 #define GO(BF, KVM, DP, QB, NW) hipLaunchKernelGGL((k_attn_few<BF, KVM, DP, QB, NW>), grid, dim3(NW * 64), 0, st, a)
 #define TYPES(DP, QB, NW)                                                                                          \
   if (bf) {                                                                                                        \
@@ -434,7 +436,10 @@ hipError_t sffn_launch_attn_few(const AttnArgs& a, int qt, int kvt, hipStream_t 
 #define WAVES(DP, QB) if (wide) { TYPES(DP, QB, 8) } else { TYPES(DP, QB, 4) }
   if (a.kv.d <= 64) { if (rows > 32) { WAVES(64, 4) } else if (rows > 16) { WAVES(64, 2) } else { WAVES(64, 1) } }
   else if (a.kv.d <= 128) { if (rows > 16) { WAVES(128, 2) } else { WAVES(128, 1) } }
-  else { WAVES(256, 1) }
+  else if (wide) {
+    if (bf) { if (kvm == 1) GO(true, 1, 256, 1, 8); else GO(true, 2, 256, 1, 8); }
+    else { if (kvm == 1) GO(false, 1, 256, 1, 8); else GO(false, 2, 256, 1, 8); }
+  } else { TYPES(256, 1, 4) }
 #undef WAVES
 #undef TYPES
 #undef GO
