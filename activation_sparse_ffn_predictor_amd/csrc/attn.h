@@ -99,8 +99,11 @@ struct AttnArgs {
   float2* pml;              // their maxima (log2 domain) and sums [T * hq][ns]
 };
 
-// few-row kernel: units of 32 keys; a share has at least FEW_LEAST of them and a multiple of FEW_STEP
-constexpr int FEW_USH = 5, FEW_LEAST = 16, FEW_STEP = 4;
+// few-row kernel: units of 32 keys; a share has at least few_least of them and a multiple of FEW_STEP. (Head sizes over
+// 128, whose rows take twice the time: one sequence of 1000 keys, 64 heads on 8 of 256, fp16: 22.1 us in two shares, 15.6
+// in four; of 300: 14.5 in one or two.)
+constexpr int FEW_USH = 5, FEW_STEP = 4;
+__host__ __device__ constexpr int few_least(int d) { return d <= 128 ? 16 : 8; }
 // tile kernel: units of 64 keys (32 for head sizes over 128: the accumulators leave no registers for more), 128 rows
 __host__ __device__ constexpr int many_ush(int d) { return d <= 128 ? 6 : 5; }
 constexpr int MANY_LEAST = 4, MANY_ROWS = 128;

@@ -81,7 +81,7 @@ bool attn_sizes_ok(int Hq, int Hkv, int d, int max_q) {
 }
 bool few_rows(int G, int d, int max_q) { return (int64_t)max_q * G <= sffn_attn_few_rows(d); }
 
-// Over how many workgroups the keys of one sequence (few rows) or of one row tile are spread, at most one per FEW_LEAST
+// Over how many workgroups the keys of one sequence (few rows) or of one row tile are spread, at most one per few_least
 // (MANY_LEAST) units of the keys that the longest sequence can see. Shares fill the chip, but their partial results are
 // written, read again and joined by a second kernel.
 int shares(int T, int S, int Hkv, int G, int d, int max_q, int max_kv, int window, int sinks) {
@@ -91,7 +91,7 @@ int shares(int T, int S, int Hkv, int G, int d, int max_q, int max_kv, int windo
     const int64_t rows = few ? max_q : sffn::MANY_ROWS / G + 2;      // tokens of one tile
     see = std::min(see, (int64_t)window + rows + std::min<int64_t>(sinks, see) + 128);
   }
-  const int unit = few ? 1 << sffn::FEW_USH : 1 << sffn::many_ush(d), least = few ? sffn::FEW_LEAST : sffn::MANY_LEAST;
+  const int unit = few ? 1 << sffn::FEW_USH : 1 << sffn::many_ush(d), least = few ? sffn::few_least(d) : sffn::MANY_LEAST;
   const int64_t chunk = (int64_t)unit * least;     // keys of the smallest share
   const int64_t most = std::min<int64_t>((see + chunk - 1) / chunk, sffn::MAX_SHARES);
   // workgroups without shares; row tiles: the whole ones, and half a tile more for each further sequence's end
@@ -109,10 +109,10 @@ int shares(int T, int S, int Hkv, int G, int d, int max_q, int max_kv, int windo
     // out sequences of different lengths (32 sequences to 6000 tokens on 40 heads, int8: one share 187 us, two 169).
     int64_t ns = max_q * G > 16 || 2 * blocks <= places ? places / blocks : (3 * places + blocks - 1) / blocks;
     ns = std::min(ns, most);
-    // Past one workgroup a compute unit a share of twice the smallest is enough (60 sequences of 2200 on 8 K/V heads,
-    // fp16: four shares 113 us, two 106; 32 of 1100: two 32, one 25).
+    // Past one workgroup a compute unit shares of 1024 keys are enough (60 sequences of 2200 on 8 K/V heads, fp16: four
+    // shares 113 us, two 106; 32 of 1100: two 32, one 25; size 256, 64 of 1000: two 116, one 103).
     if (ns * blocks > places / 2)
-      ns = std::max(std::min(ns, places / 2 / blocks), std::min(ns, (see + chunk) / (2 * chunk)));
+      ns = std::max(std::min(ns, places / 2 / blocks), std::min(ns, (see + 512) / 1024));
     return (int)std::max<int64_t>(1, ns);
   }
   // Row tiles: one share, a round of one workgroup a compute unit or a round of two, whichever a sum of measured costs

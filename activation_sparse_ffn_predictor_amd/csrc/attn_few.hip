@@ -11,8 +11,8 @@
 // of 131072, 64 heads on 8 of 128, e4m3, 554 MB in 104 us with the join (5.3 TB/s; a large read reaches 5.9); fp16, 1.07 GB
 // in 187 us (5.7 TB/s); 32 ragged sequences to 6000 tokens, 40 heads, int8, 892 MB in 169 to 176 us; 48 sequences of up to 4
 // drafts, 128 heads on 8 of 64, bf16, window 4096, 385 MB in 80 us (4.8 TB/s). One sequence of 500 tokens, 2 MB: 9.6 us,
-// of which 5 are a call on 32 tokens: the rest is one compute unit's loads of a head's 256 KB. From 769 keys on the keys
-// are spread and joined (13 us up to 4000; in one workgroup 700 take 11.7, 1000 take 14.2).
+// of which 5 are a call on 32 tokens: the rest is one compute unit's loads of a head's 256 KB. From 769 keys on (385
+// for sizes over 128) the keys are spread and joined (13 us up to 4000; in one workgroup 700 take 11.7, 1000 take 14.2).
 #include "attn.h"
 
 using namespace sffn;
@@ -400,7 +400,7 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void k_attn_few(AttnArg
   pl.p0 = pl.sq.len - pl.sq.n;                     // positions of the first and last new token
   pl.p1 = pl.p0 + pl.n - 1;
   pl.un = key_units(pl.p0, pl.p1, pl.sq.len, a.window, a.sinks, FEW_USH);
-  const int per = share_units(pl.un.tot, a.ns, FEW_LEAST, FEW_STEP);
+  const int per = share_units(pl.un.tot, a.ns, few_least(DP), FEW_STEP);
   pl.used = max(1, (pl.un.tot + per - 1) / per);
   if (pl.split >= pl.used) return;
   pl.u0 = pl.split * per;

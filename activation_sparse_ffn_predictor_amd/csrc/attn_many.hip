@@ -530,7 +530,7 @@ __global__ __launch_bounds__(NT) void k_attn_join(AttnArgs a, int few) {
     hi = p0 + (min(n * a.G, r0 + MANY_ROWS) - 1) / a.G;
   }
   const Units un = key_units(lo, hi, sq.len, a.window, a.sinks, few ? FEW_USH : many_ush(d));
-  const int per = share_units(un.tot, a.ns, few ? FEW_LEAST : MANY_LEAST, few ? FEW_STEP : 1);
+  const int per = share_units(un.tot, a.ns, few ? few_least(d) : MANY_LEAST, few ? FEW_STEP : 1);
   const int used = (un.tot + per - 1) / per;       // at most MAX_SHARES
   if (used <= 1) return;                           // the row's only block has written it
   const float2 ml = l < used ? a.pml[row * a.ns + l] : make_float2(-INFINITY, 0.f);
