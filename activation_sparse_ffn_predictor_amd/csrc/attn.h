@@ -25,10 +25,21 @@ struct Seqs {
   const int* table;
   int S, T, cols, ldt;
 };
+// The position of row t of a sequence whose rows end at `end` and whose length is `len`: len - n + (t - first). It comes from
+// the caller's numbers as they are, whatever the table row or the call's rows hold (only accesses are bounded by those), so
+// the attention and the write agree on it. Lengths count up to MOST_LEN, which puts every one of the up to 2^24 new tokens of
+// a longer sequence behind the largest table row; positions far below 0 are all the same.
+constexpr int MOST_LEN = (1 << 30) + (1 << 24);
+__host__ __device__ __forceinline__ int token_pos(int len, int end, int t) {
+  const int64_t p = (int64_t)min(len, MOST_LEN) - end + t;
+  return (int)(p < -(1 << 25) ? -(1 << 25) : p > 0x7FFFFFFF ? 0x7FFFFFFF : p);
+}
+
 // One sequence, clamped so that nothing read from device memory can lead an access out of the caller's tensors:
-// its first row of the token tensors, its new tokens, its cached tokens (at most what its table row can hold).
+// its first row of the token tensors, its new tokens, its cached tokens (at most what its table row can hold); and the first
+// row's position, which is not clamped by those.
 struct Seq {
-  int q0, n, len;
+  int q0, n, len, p0;
 };
 __host__ __device__ __forceinline__ Seq load_seq(const Seqs& q, int s, int psh) {
   Seq r;
@@ -36,6 +47,7 @@ __host__ __device__ __forceinline__ Seq load_seq(const Seqs& q, int s, int psh) 
   r.q0 = min(max(a, 0), q.T);
   r.n = min(max(b, r.q0), q.T) - r.q0;
   r.len = min(max(l, 0), q.cols << psh);
+  r.p0 = token_pos(l, b, r.q0);
   return r;
 }
 
@@ -71,7 +83,7 @@ __host__ __device__ __forceinline__ Units key_units(int p_lo, int p_hi, int len,
   const int end = min(len, p_hi + 1);          // keys at or after it are visible to no row
   Units u{0, 0, 0};
   if (end <= 0) return u;
-  const int lo = window > 0 ? max(0, p_lo - window + 1) : 0;
+  const int lo = window > 0 ? min(max(0, p_lo - window + 1), end) : 0;   // past the end: tokens past the table row
   u.w0 = lo >> ush;
   u.sink = min((min(sinks, lo) + (1 << ush) - 1) >> ush, u.w0);
   u.tot = u.sink + ((end + (1 << ush) - 1) >> ush) - u.w0;

@@ -213,7 +213,7 @@ int sffn_attn(sffn_kv c, sffn_seqs q, int type, const void* qp, int64_t q_stride
   a.hq = Hq;
   a.G = G;
   a.max_q = max_q;
-  a.window = std::min(window, MAX_POS);
+  a.window = std::min(window, sffn::MOST_LEN);                    // every position is below it
   a.sinks = std::min(sinks, MAX_POS);
   a.ns = ns;
   a.ldq = q_stride;

@@ -397,7 +397,7 @@ __global__ __launch_bounds__(NW * 64, DP <= 128 ? 2 : 1) void k_attn_few(AttnArg
   pl.n = min(pl.sq.n, a.max_q);
   pl.rows = pl.n * a.G;
   if (pl.rows == 0) return;
-  pl.p0 = pl.sq.len - pl.sq.n;                     // positions of the first and last new token
+  pl.p0 = pl.sq.p0;                                // positions of the first and last new token
   pl.p1 = pl.p0 + pl.n - 1;
   pl.un = key_units(pl.p0, pl.p1, pl.sq.len, a.window, a.sinks, FEW_USH);
   const int per = share_units(pl.un.tot, a.ns, few_least(DP), FEW_STEP);

@@ -105,7 +105,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
   tile = ntiles - 1 - tile;                        // the longest first
   const Seq sq = load_seq(a.sq, s, a.kv.psh);
   const int n = min(sq.n, a.max_q), r0 = tile * MANY_ROWS, rows = min(MANY_ROWS, n * G - r0);
-  const int p0 = sq.len - sq.n;
+  const int p0 = sq.p0;
   const int b_lo = p0 + r0 / G, b_hi = p0 + (r0 + rows - 1) / G;
   const Units un = key_units(b_lo, b_hi, sq.len, a.window, a.sinks, USH);
   const int per = share_units(un.tot, a.ns, MANY_LEAST, 1), used = max(1, (un.tot + per - 1) / per);
@@ -518,7 +518,7 @@ __global__ __launch_bounds__(NT) void k_attn_join(AttnArgs a, int few) {
   const int s = __builtin_amdgcn_readfirstlane(find_seq<64>(a.sq.cu, a.sq.S, t));
   if (s >= a.sq.S) return;
   const Seq sq = load_seq(a.sq, s, a.kv.psh);
-  const int n = min(sq.n, a.max_q), i = t - sq.q0, p0 = sq.len - sq.n;
+  const int n = min(sq.n, a.max_q), i = t - sq.q0, p0 = sq.p0;
   if (i < 0 || i >= n) return;
   int lo, hi;                                      // positions of the row's tile
   if (few) {

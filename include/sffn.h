@@ -253,8 +253,9 @@ typedef struct {
  * table[s * table_stride + p / page]; a table row holds max_pages entries. Rows at and behind cu[S] belong to no
  * sequence: they are neither read nor written. The arrays are read on the device, so they are not checked on the
  * host; whatever they hold, no access leaves the given tensors: a position outside the table row or a page id
- * outside 0 .. n_pages - 1 holds no token (not written, not read, not seen). Tokens before a sequence's first
- * (kv_len[s] < n) see nothing. 1 <= S <= 65535, 0 <= T <= 2^24 (T = 0: nothing is done), max_pages * page <= 2^30. */
+ * outside 0 .. n_pages - 1 holds no token (not written, not read, not seen). New tokens keep their positions there: of a
+ * sequence that has run past its table row the last ones are not held, and see what the row holds. kv_len counts up to
+ * 2^30 + 2^24. Tokens before a sequence's first (kv_len[s] < n) see nothing. 1 <= S <= 65535, 0 <= T <= 2^24 (T = 0: nothing is done), max_pages * page <= 2^30. */
 typedef struct {
   const int32_t* cu;
   const int32_t* kv_len;
