@@ -108,7 +108,7 @@ struct AttnArgs {
   float c;                  // |softmax scale| * log2(e)
   int neg;                  // the scale is negative: the queries' signs are turned as they are loaded
   float* po;                // partial outputs [T * hq][ns][d], used when ns > 1
-  float2* pml;              // their maxima (log2 domain) and sums [T * hq][ns]
+  float2* pml;              // their references (log2 domain) and sums [T * hq][ns]
 };
 
 // few-row kernel: units of 32 keys; a share has at least few_least of them and a multiple of FEW_STEP. (Head sizes over
@@ -228,7 +228,7 @@ __device__ __forceinline__ uint2 codes4(uint32_t u) {
 
 // What the softmax takes from a key's scales. With 8-bit V rows the weights p_j s_j that multiply the codes must not
 // leave fp16's range whatever the scales are, so the running maximum is taken over x_j + log2 s_j (x: scores in
-// log2 units): P_j = 2^(x_j + log2 s_j - m) <= 1 multiplies the codes, and the softmax's own sum is that of P_j / s_j.
+// log2 units): P_j = 2^(x_j + log2 s_j - m) multiplies the codes, and the softmax's own sum is that of P_j / s_j.
 // A row with scale 0 has codes 0, so any scale serves; one with scale NaN counts in the sum as if it had scale 0, and
 // its weight in the second product is NaN for the rows that see it.
 struct VScale {
@@ -238,7 +238,20 @@ __device__ __forceinline__ VScale v_scale(float s) {
   const float t = s >= KV_MIN_SCALE ? s : KV_MIN_SCALE;
   return {__builtin_amdgcn_logf(t), __builtin_amdgcn_rcpf(t)};
 }
-// Factor of what was accumulated under the maximum m when the maximum becomes `to` (finite): never 0 where something
+// What weights refer to. P_j = 2^(x_j - m) enters the second product in 16 bits. The reference m follows a row's maximum (lazily:
+// it moves only when the maximum has grown by 2^8, so that most tiles leave the sums alone) and lies WEIGHT_UP powers of two
+// under it: the largest P_j is 2^WEIGHT_UP .. 2^(WEIGHT_UP + 8). fp16 holds normal numbers from 2^-14 to 2^16, so with 7 weights
+// down to 2^-21 of the largest keep its 11 bits and those below are off by at most 2^-25, 2^-32 of the largest; with 0 a flat tail
+// of weights under 2^-17 of a dominant key lost its bits, under 2^-25 itself, though its sum may be the output (4000 keys at
+// 2^-24.5: 41% off). bf16 has fp32's exponents and needs none (and headroom for values near its largest).
+template <bool CB>
+constexpr float WEIGHT_UP = CB ? 0.f : 7.f;
+template <bool CB>
+__device__ __forceinline__ bool outgrown(float top, float m) { return top > m + (WEIGHT_UP<CB> + 8.f); }
+template <bool CB>
+__device__ __forceinline__ float new_reference(float top, float m) { return fmaxf(m, top - WEIGHT_UP<CB>); }
+
+// Factor of what was accumulated under the reference m when the reference becomes `to` (finite): never 0 where something
 // was, so that an infinity or NaN stays one however small its weight has become.
 __device__ __forceinline__ float fade(float m, float to) {
   return m == -INFINITY ? 0.f : fmaxf(__builtin_amdgcn_exp2f(m - to), 1.1754944e-38f);

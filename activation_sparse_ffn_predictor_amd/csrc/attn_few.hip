@@ -244,9 +244,8 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const Place& pl, cha
         for (int i = 0; i < 4; ++i) top = fmaxf(top, sc[qb][kb][i]);
       top = over32<true>(over16<true>(top));
       if constexpr (!C8) top *= c;
-      // the maximum that weights refer to moves only when a row's has grown by more than 2^8 (see the tile kernel)
-      if (__any(top > m[qb] + 8.f)) {
-        const float mn = fmaxf(m[qb], top), f = fade(m[qb], mn);
+      if (__any(outgrown<CB>(top, m[qb]))) {
+        const float mn = new_reference<CB>(top, m[qb]), f = fade(m[qb], mn);
         ls[qb] *= f;
 #pragma unroll
         for (int db = 0; db < DB; ++db) o[qb][db] *= f;

@@ -319,10 +319,8 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
       for (int i = 0; i < 16; ++i) top = fmaxf(top, sc[kb][i]);
     top = over32<true>(top);
     if constexpr (!C8) top *= c;
-    // The maximum that weights refer to is only moved when a row's has grown by more than 2^8 (a weight of 2^8 is
-    // still far inside fp16, and relative precision does not depend on it): most tiles leave the sums alone.
-    if (__any(top > m + 8.f)) {
-      const float mn = fmaxf(m, top), f = fade(m, mn);
+    if (__any(outgrown<CB>(top, m))) {
+      const float mn = new_reference<CB>(top, m), f = fade(m, mn);
       ls *= f;
 #pragma unroll
       for (int db = 0; db < DB; ++db) o[db] *= f;

@@ -285,7 +285,8 @@ int sffn_kv_read(sffn_kv cache, sffn_seqs seqs, int type, void* k, int64_t k_str
  * q [T, Hq, head_dim] of a 16-bit `type` (the cache's own if that has 16 bits), out likewise, tokens q_stride and
  * out_stride elements apart (multiples of 8). lse [T, Hq] fp32 or NULL: the natural logarithm of the softmax's sum
  * (-infinity for a token that sees nothing). Scores, sums and accumulators are fp32; the weights enter the second
- * product as 16-bit values, and 8-bit codes enter both products exactly. Over an 8-bit cache bf16 queries enter the
+ * product as 16-bit values of the cache's type (fp16 over 8-bit caches; those under 2^-21 of a token's largest, times the
+ * scales there, are off by up to 2^-32 of it), and 8-bit codes enter both products exactly. Over an 8-bit cache bf16 queries enter the
  * first one in steps of at most 2^-39 of the largest finite element among the rows of a workgroup.
  * max_q: at least the largest number of new tokens of one sequence (tokens past it are not computed and their rows
  * stay as they were). max_kv: about the largest kv_len; it decides only over how many workgroups a sequence's keys
