@@ -28,11 +28,11 @@ struct Seqs {
 // The position of row t of a sequence whose rows end at `end` and whose length is `len`: len - n + (t - first). It comes from
 // the caller's numbers as they are, whatever the table row or the call's rows hold (only accesses are bounded by those), so
 // the attention and the write agree on it. Lengths count up to MOST_LEN, which puts every one of the up to 2^24 new tokens of
-// a longer sequence behind the largest table row; positions far below 0 are all the same.
+// a longer sequence behind the largest table row. 0 <= t < end. In 32 bits (64 cost a large write 3%): the two limits keep the
+// difference from wrapping, and change only positions that are below 0 with them and without.
 constexpr int MOST_LEN = (1 << 30) + (1 << 24);
 __host__ __device__ __forceinline__ int token_pos(int len, int end, int t) {
-  const int64_t p = (int64_t)min(len, MOST_LEN) - end + t;
-  return (int)(p < -(1 << 25) ? -(1 << 25) : p > 0x7FFFFFFF ? 0x7FFFFFFF : p);
+  return min(max(len, -(1 << 24)), MOST_LEN) - min(end - t, 0x7F000000);
 }
 
 // One sequence, clamped so that nothing read from device memory can lead an access out of the caller's tensors:
@@ -47,7 +47,7 @@ __host__ __device__ __forceinline__ Seq load_seq(const Seqs& q, int s, int psh) 
   r.q0 = min(max(a, 0), q.T);
   r.n = min(max(b, r.q0), q.T) - r.q0;
   r.len = min(max(l, 0), q.cols << psh);
-  r.p0 = token_pos(l, b, r.q0);
+  r.p0 = token_pos(l, max(b, r.q0), r.q0);
   return r;
 }
 

@@ -96,7 +96,7 @@ __device__ __forceinline__ bool find_slot(const Kv& kv, const Seqs& sq, int s, i
 // one sequence, so it is searched for once.
 template <int LPR, int PASS>
 __device__ __forceinline__ void find_rows(const Kv& kv, const Seqs& sq, int h, int t0, int step, long (&row)[PASS]) {
-  int s = 0, a = 0, end = -1, len = 0;             // sequence, its tokens a .. end - 1, its length
+  int s = 0, a = 0, end = -1, shift = 0;           // sequence, its tokens a .. end - 1, their positions less their rows
 #pragma unroll
   for (int p = 0; p < PASS; ++p) {
     const int t = t0 + p * step;
@@ -107,9 +107,9 @@ __device__ __forceinline__ void find_rows(const Kv& kv, const Seqs& sq, int h, i
       if (s >= sq.S) continue;                     // behind the last sequence
       a = sq.cu[s];
       end = sq.cu[s + 1];
-      len = sq.len[s];
+      shift = token_pos(sq.len[s], max(end, 0), 0);
     }
-    const int pos = token_pos(len, end, t);
+    const int pos = shift + t;
     if (t < a || t >= end || pos < 0 || (pos >> kv.psh) >= sq.cols) continue;
     const int pid = sq.table[(long)s * sq.ldt + (pos >> kv.psh)];
     if ((unsigned)pid >= (unsigned)kv.n_pages) continue;
