@@ -192,6 +192,17 @@ __device__ __forceinline__ uint4 finite_only(const uint4& t) {
   }
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
+// e4m3's two NaN codes, 0x7F and 0xFF (no write stores them): a bit pattern with a byte's top bit where four codes hold one;
+// and the codes with those replaced by 0
+__device__ __forceinline__ uint32_t nan_codes(uint32_t u) { return ((u & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t finite_codes(uint32_t u) {
+  const uint32_t n = nan_codes(u);
+  return u & ~(n | (n - (n >> 7)));
+}
+__device__ __forceinline__ uint32_t nan_codes4(const uint4& t) { return nan_codes(t.x) | nan_codes(t.y) | nan_codes(t.z) | nan_codes(t.w); }
+__device__ __forceinline__ uint4 finite_codes4(const uint4& t) {
+  return make_uint4(finite_codes(t.x), finite_codes(t.y), finite_codes(t.z), finite_codes(t.w));
+}
 // bf16 queries for fp16 products: all times one power of two that takes the largest, `big`, to 2^14 .. 2^15 (exact
 // but for elements below 2^-29 of it, which lose bits under 2^-40 of it); c takes the factor back.
 __device__ __forceinline__ float to_f16_range(float big, float& c) {

@@ -175,8 +175,24 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const Place& pl, cha
           for (int qb = 0; qb < QB; ++qb) sc[qb][kb] = mfma16<CB>(kr[kb][i], q_frag(qb, i), sc[qb][kb]);
         }
       }
-    // V through the wave's own LDS tile (the LDS pipe keeps a wave's accesses in order). Infinities and NaN in a unit
-    // that some row sees only in part are left out here and added where they are seen after the last unit.
+    // V through the wave's own LDS tile (the LDS pipe keeps a wave's accesses in order). Infinities and NaN (NaN codes) in a
+    // unit that some row sees only in part are left out here and added where they are seen after the last unit.
+    if constexpr (KVM == 2) {
+      if (!full) {
+        uint32_t n = 0;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int i = 0; i < VL; ++i) n |= nan_codes4(vr[kb][i]);
+        if (__any(n != 0)) {
+          left_out = true;
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int i = 0; i < VL; ++i) vr[kb][i] = finite_codes4(vr[kb][i]);
+        }
+      }
+    }
     int lv = l;                                    // as in load: worked out anew
     asm volatile("" : "+v"(lv));
 #pragma unroll
@@ -298,7 +314,7 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const Place& pl, cha
     asm volatile("" ::: "memory");
   }
 
-  if (!C8 && __any(left_out)) {
+  if (KVM != 1 && __any(left_out)) {
     // once more through the keys of the units that some row sees only in part
 #pragma unroll 1
     for (u = pl.u0 + w; u < u1; u += NW) {
@@ -320,8 +336,15 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const Place& pl, cha
           for (int db = 0; db < DB; ++db) {
             const int d0 = db * 16 + g4 * 4;
             if (d0 >= d) continue;
-            const uint2 v = *reinterpret_cast<const uint2*>(row + d0 * 2);
-            const float f[4] = {lo16<CB>(v.x), hi16<CB>(v.x), lo16<CB>(v.y), hi16<CB>(v.y)};
+            float f[4];
+            if constexpr (C8) {
+              const uint32_t v = nan_codes(*reinterpret_cast<const uint32_t*>(row + d0));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) f[i] = v >> (8 * i + 7) & 1 ? __uint_as_float(0x7FC00000u) : 0.f;
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(row + d0 * 2);
+              f[0] = lo16<CB>(v.x), f[1] = hi16<CB>(v.x), f[2] = lo16<CB>(v.y), f[3] = hi16<CB>(v.y);
+            }
 #pragma unroll
             for (int qb = 0; qb < QB; ++qb) {
               const bool see = j <= pos[qb] && (a.window <= 0 || j > pos[qb] - a.window || j < a.sinks);

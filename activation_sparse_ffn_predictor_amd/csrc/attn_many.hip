@@ -98,6 +98,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
   constexpr int USH = many_ush(DP), TK = 1 << USH, KB = TK / 32, NG = TK / 16;   // keys of a tile, by 32 and by 16
   __shared__ Tile<DP, C8> tile0, tile1;
   __shared__ float big_[NW];
+  __shared__ int nan_code;                         // e4m3: a tile that some row may see only in part held a NaN code of V
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, h = l >> 5, ql = l & 31;
   const int hk = blockIdx.x % a.kv.hkv, d = a.kv.d, G = a.G, split = blockIdx.y;
   int s, tile, ntiles;
@@ -140,7 +141,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) qf[ks] = bf16_to_f16(qf[ks], up);
   }
-  if (threadIdx.x == 0) { tile0.odd = -1; tile1.odd = -1; }
+  if (threadIdx.x == 0) { tile0.odd = -1; tile1.odd = -1; nan_code = 0; }
   __syncthreads();
 
   const int* trow = a.sq.table + (long)s * a.sq.ldt;
@@ -185,8 +186,24 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
     }
     if (!C8 && l == 0) tl.have[grp] = have;
   };
+  // whether every row of the block sees every key that exists of the TK keys from t0 on
+  auto by_all = [&](int t0) {
+    return t0 + TK - 1 <= b_lo && (a.window <= 0 || t0 > b_hi - a.window || t0 + TK <= a.sinks);
+  };
   // 8-bit: the fetched codes into the tile
   auto store = [&](Tile<DP, C8>& tl, int u) {
+    if constexpr (KVM == 2) {
+      if (do_v && !by_all(un.key0(u, USH))) {      // NaN codes are left out and added after the last tile, see look()
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < LD; ++i) bad |= nan_codes4(vr[i]);
+        if (__any(bad != 0)) {
+          nan_code = 1;
+#pragma unroll
+          for (int i = 0; i < LD; ++i) vr[i] = finite_codes4(vr[i]);
+        }
+      }
+    }
     if constexpr (C8) {
       int lx = l;                                  // places worked out anew per tile: registers are short
       asm volatile("" : "+v"(lx));
@@ -396,10 +413,8 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
     }
   };
   // Infinities and NaN in a 16-bit tile that some row may see only in part: set to 0 in LDS, and added after the last
-  // tile where they are seen.
-  auto inside = [&](int t0, int have) {
-    return t0 + TK - 1 <= b_lo && (a.window <= 0 || t0 > b_hi - a.window || t0 + TK <= a.sinks) && have == TK;
-  };
+  // tile where they are seen. (NaN codes of e4m3: in store().)
+  auto inside = [&](int t0, int have) { return by_all(t0) && have == TK; };
   auto look = [&](Tile<DP, C8>& tl, int u, int t0) {
     if (C8 || inside(t0, tl.have[0] + tl.have[1] + (NG > 2 ? tl.have[2] + tl.have[3] : 0))) return;   // the same in every wave
 #pragma unroll
@@ -437,8 +452,12 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
     if (u + 1 < u1) step(tile1, tile0, u + 1);
   }
 
+  if constexpr (KVM == 2) {
+    __syncthreads();
+    left_out = nan_code;
+  }
   if (!wave_on) return;
-  if (!C8 && left_out) {
+  if (KVM != 1 && left_out) {
     // once more through the keys of those tiles
 #pragma unroll 1
     for (int u = u0; u < u1; ++u) {
@@ -450,7 +469,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
         have[k] = (unsigned)pid[k] < (unsigned)a.kv.n_pages ? min(16, max(0, sq.len - (t0 + k * 16))) : 0;
         nv += have[k];
       }
-      if (inside(t0, nv)) continue;
+      if (C8 ? by_all(t0) : inside(t0, nv)) continue;
 #pragma unroll
       for (int k = 0; k < NG; ++k)
 #pragma unroll 1
@@ -464,8 +483,15 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
             for (int e = 0; e < 4; ++e) {
               const int d0 = db * 32 + e * 8 + h * 4;
               if (d0 >= d) continue;
-              const uint2 v = *reinterpret_cast<const uint2*>(row + d0 * 2);
-              const float f[4] = {lo16<CB>(v.x), hi16<CB>(v.x), lo16<CB>(v.y), hi16<CB>(v.y)};
+              float f[4];
+              if constexpr (C8) {
+                const uint32_t v = nan_codes(*reinterpret_cast<const uint32_t*>(row + d0));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = v >> (8 * i + 7) & 1 ? __uint_as_float(0x7FC00000u) : 0.f;
+              } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(row + d0 * 2);
+                f[0] = lo16<CB>(v.x), f[1] = hi16<CB>(v.x), f[2] = lo16<CB>(v.y), f[3] = hi16<CB>(v.y);
+              }
 #pragma unroll
               for (int i = 0; i < 4; ++i) o[db][e * 4 + i] += see && !(fabsf(f[i]) < INFINITY) ? f[i] : 0.f;
             }

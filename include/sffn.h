@@ -281,7 +281,8 @@ int sffn_kv_read(sffn_kv cache, sffn_seqs seqs, int type, void* k, int64_t k_str
  *   out[t, h, :] = sum_j softmax_j(scale * q[t, h, :] . K[j, h', :]) V[j, h', :],   h' = h / (Hq / n_kv_heads)
  * over the positions j that token t at position p sees: j <= p, j < kv_len, and if window > 0 also j > p - window or
  * j < sinks (a sliding window beside which the first `sinks` tokens stay visible). A token that sees nothing gets
- * zeros. What lies in places a token does not see, infinities and NaN included, has no effect on it.
+ * zeros. What lies in places a token does not see, infinities and NaN (of an 8-bit cache: NaN scales, and e4m3's NaN codes,
+ * which no write stores) included, has no effect on it.
  * q [T, Hq, head_dim] of a 16-bit `type` (the cache's own if that has 16 bits), out likewise, tokens q_stride and
  * out_stride elements apart (multiples of 8). lse [T, Hq] fp32 or NULL: the natural logarithm of the softmax's sum
  * (-infinity for a token that sees nothing). Scores, sums and accumulators are fp32; the weights enter the second
