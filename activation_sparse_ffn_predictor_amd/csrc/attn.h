@@ -268,6 +268,13 @@ __device__ __forceinline__ float fade(float m, float to) {
   return m == -INFINITY ? 0.f : fmaxf(__builtin_amdgcn_exp2f(m - to), 1.1754944e-38f);
 }
 
+// An accumulator that an infinity under a weight of 0 (what 16 bits hold of a small one) has made NaN is set to LOST, a small
+// number that stays as it is when 0 is added and is gone with the first infinity or NaN that its row sees; what is still LOST
+// after them all was NaN for another reason and is put back.
+constexpr float LOST = 1.17549449e-38f;            // one step over the smallest normal number
+__device__ __forceinline__ float lose_nan(float o) { return o == o ? o : LOST; }
+__device__ __forceinline__ float find_lost(float o) { return o == LOST ? __uint_as_float(0x7FC00000u) : o; }
+
 // natural logarithm of L * 2^M (-infinity for a row without visible keys)
 __device__ __forceinline__ float log_sum(float M, float L) {
   return L == 0.f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) * 0.6931471805599453f;

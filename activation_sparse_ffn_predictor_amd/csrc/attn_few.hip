@@ -386,6 +386,33 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, const Place& pl, cha
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] = fmaf(src[j], f, acc[j]);
     }
+    if constexpr (!C8) {
+      const float all = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+      if (all != all && L == L) {                  // perhaps a lost infinity: once more through what the row sees
+        const int pr = p0 + i;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = lose_nan(acc[j]);
+#pragma unroll 1
+        for (int t = pl.u0; t < u1; ++t) {
+          const int t0 = un.key0(t, FEW_USH);
+#pragma unroll 1
+          for (int j = t0; j < min(t0 + 32, min(sq.len, pr + 1)); ++j) {
+            const int pid = trow[min(j >> a.kv.psh, a.sq.cols - 1)];
+            if ((unsigned)pid >= (unsigned)a.kv.n_pages || !(a.window <= 0 || j > pr - a.window || j < a.sinks)) continue;
+            const uint4 v = *reinterpret_cast<const uint4*>(
+                a.kv.v + ((((long)pid * a.kv.hkv + hk) << a.kv.psh) + (j & ((1 << a.kv.psh) - 1))) * dB + d0 * 2);
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float f = k & 1 ? hi16<CB>(x[k >> 1]) : lo16<CB>(x[k >> 1]);
+              acc[k] += fabsf(f) < INFINITY ? 0.f : f;
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = find_lost(acc[j]);
+      }
+    }
     const long row = (long)(sq.q0 + i) * a.hq + hk * G + g;
     if (used == 1) {
       const float iv = L == 0.f ? 0.f : 1.f / L;   // no key was visible: 0

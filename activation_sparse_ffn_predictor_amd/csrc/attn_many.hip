@@ -457,8 +457,23 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
     left_out = nan_code;
   }
   if (!wave_on) return;
-  if (KVM != 1 && left_out) {
-    // once more through the keys of those tiles
+  ls = over32<false>(ls);
+  bool again = false;                              // NaN though the row's sum is none: it may be an infinity's (see LOST)
+  if constexpr (!C8) {
+#pragma unroll
+    for (int db = 0; db < DB; ++db)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) again |= ls == ls && o[db][i] != o[db][i];
+    again = __any(again);
+    if (again) {
+#pragma unroll
+      for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[db][i] = lose_nan(o[db][i]);
+    }
+  }
+  if (KVM != 1 && (again || left_out)) {
+    // once more through the keys of those tiles (of all, for lost infinities)
 #pragma unroll 1
     for (int u = u0; u < u1; ++u) {
       const int t0 = un.key0(u, USH);
@@ -469,7 +484,7 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
         have[k] = (unsigned)pid[k] < (unsigned)a.kv.n_pages ? min(16, max(0, sq.len - (t0 + k * 16))) : 0;
         nv += have[k];
       }
-      if (C8 ? by_all(t0) : inside(t0, nv)) continue;
+      if (!again && (C8 ? by_all(t0) : inside(t0, nv))) continue;
 #pragma unroll
       for (int k = 0; k < NG; ++k)
 #pragma unroll 1
@@ -497,8 +512,13 @@ __global__ __launch_bounds__(NT, DP <= 128 ? 2 : 1) void k_attn_many(AttnArgs a)
             }
         }
     }
+    if (again) {
+#pragma unroll
+      for (int db = 0; db < DB; ++db)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[db][i] = find_lost(o[db][i]);
+    }
   }
-  ls = over32<false>(ls);
   if (!mine) return;
   const long row = (long)(sq.q0 + ri) * a.hq + hk * G + rg;
   if (used == 1) {

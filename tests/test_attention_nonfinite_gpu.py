@@ -1,5 +1,5 @@
-"""Infinities and NaN in the cache: in places that a row does not see they change nothing, where it sees them it shows them.
-8-bit caches may hold e4m3's NaN codes (0x7F, 0xFF), which no write stores."""
+"""Infinities and NaN in the cache: in places that a row does not see they change nothing, where it sees them it shows them,
+however small their weight. 8-bit caches may hold e4m3's NaN codes (0x7F, 0xFF), which no write stores."""
 import math
 
 import pytest
@@ -66,3 +66,37 @@ def test_nan_key_codes(gpu_ready, d):
         o, l, to, tl = definition(b, q, 4, d ** -0.5, window)
         assert_near(out.cpu()[~bad], o[~bad], to[~bad])
         assert_near(lse.cpu()[~bad], l[~bad], tl[~bad])
+
+
+@pytest.mark.parametrize("qt", ["f16", "bf16"])
+@pytest.mark.parametrize("n,d", [(1, 64), (2, 128), (1, 256), (60, 64), (60, 128), (40, 256)])
+def test_infinities_under_vanishing_weights(gpu_ready, n, d, qt):
+    """An infinity whose weight is far below what 16 bits, or 32, hold: the output is that infinity in a unit of keys that
+    every row sees as in one that some row sees in part; one of each sign, or a NaN: NaN."""
+    for k, gap in ((200, 30.0), (200, 300.0), (3000, 60.0)):
+        b = Paged([n], [k], 1, d, 16, qt, qt, seed=n + d)
+        x = torch.randn((2, b.n_pages, 1, 16, d), generator=b.g)
+        x[0] *= 0.1
+        x[0, ..., 0] = 0
+
+        def put(p, el, v):
+            x[1, int(b.table[0, p // 16]), 0, p % 16, el] = v
+        for s in range(0, k, 32):                    # in every part of the keys
+            x[0, int(b.table[0, s // 16]), 0, s % 16, 0] = 8.0
+        put(33, 1, math.inf)
+        put(34, 2, -math.inf)
+        put(35, 3, math.inf)
+        put(70, 3, -math.inf)
+        put(36, 4, math.nan)
+        put(k - n, 5, math.inf)
+        put(k - 1, 6, -math.inf)
+        put(k // 2 + 3, 9, math.inf)
+        b.set_values(x.to(DT[qt]))
+        q = torch.randn((n, 4, d), generator=b.g)
+        q[..., 0] = gap * d ** 0.5 / 8
+        q = q.to(DT[qt])
+        out, lse = run_attn(b, q, 4, gpu_ready)
+        o, l, to, tl = definition(b, q, 4, d ** -0.5)
+        assert (o[:, :, 1] == math.inf).all() and (o[:, :, 9] == math.inf).all() and o[:, :, 3].isnan().all()
+        assert_near(out, o, to, f"out {k} {gap}")
+        assert_near(lse, l, tl, f"lse {k} {gap}")
