@@ -228,11 +228,12 @@ class SparseFFNStack:
         return g
 
     def replay(self, B: int = 1):
+        graph = self.graphs[B]                                 # (before any length grows)
         if self.attn is not None:
             for s in range(B):
                 self._room(s, 1)
             self.lens[:B] = [n + 1 for n in self.lens[:B]]
-        self.graphs[B].replay()
+        graph.replay()
 
     # ------------------------------------------------------------------ accounting
     def active_weight_bytes_per_row(self) -> int:
