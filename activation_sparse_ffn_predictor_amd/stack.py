@@ -18,6 +18,7 @@ used as they are projected.
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 from typing import Dict, List, Optional
 
@@ -138,6 +139,23 @@ class SparseFFNStack:
             self.layer_call(i, self.xf[:B], False, x)
         _lib.add_rmsnorm(x, self.h[:B], self.w_out, self.attn.eps, self.out[:B], res_out=self.h[:B])
 
+    @contextlib.contextmanager
+    def _grown(self, rows: slice, n: int):
+        """The sequences `rows` longer by n tokens for the calls inside; as they were if one of these is refused."""
+        before = self.lens[rows]
+        self.lens[rows] = [m + n for m in before]
+        self.kv_len[rows] += n
+        try:
+            yield
+        except Exception:
+            self.lens[rows] = before
+            self.kv_len[rows] -= n
+            raise
+
+    def _batch(self, B: int):
+        if not 1 <= B <= self.max_batch:
+            raise ValueError(f"{B} sequences: need 1 to max_batch = {self.max_batch}")
+
     def _room(self, s: int, n: int):
         if self.lens[s] + n > self.attn.max_len:
             raise ValueError(f"sequence {s}: {self.lens[s]} + {n} tokens exceed max_len = {self.attn.max_len}")
@@ -152,9 +170,9 @@ class SparseFFNStack:
         x = x.contiguous()
         self._room(s, T)
         cu = self.cu_prompt.setdefault(T, torch.tensor([0, T], dtype=torch.int32, device=self.device))
-        self.kv_len[s:s + 1] += T
-        self.lens[s] += T
-        self._layers(x, T, cu, self.kv_len[s:s + 1], self.table[s:s + 1], T)
+        one = slice(s, s + 1)
+        with self._grown(one, T):
+            self._layers(x, T, cu, self.kv_len[one], self.table[one], T)
 
     def reset(self):
         """Forget every sequence's tokens."""
@@ -199,11 +217,11 @@ class SparseFFNStack:
         attention: the next token of each of the first B sequences, the last layer's output in self.out[:B] too."""
         x = self.x_in[:B]
         if self.attn is not None:
+            self._batch(B)
             for s in range(B):
                 self._room(s, 1)
-            self.lens[:B] = [n + 1 for n in self.lens[:B]]
-            self.kv_len[:B] += 1
-            self._layers(x, B, self.cu_step[:B + 1], self.kv_len[:B], self.table[:B], 1)
+            with self._grown(slice(0, B), 1):
+                self._layers(x, B, self.cu_step[:B + 1], self.kv_len[:B], self.table[:B], 1)
             return
         for i in range(len(self.layers)):
             y = self.y[i, :B]
@@ -216,14 +234,16 @@ class SparseFFNStack:
         lens = None if self.attn is None else (list(self.lens), self.kv_len.clone())
         self.step(B)
         torch.cuda.synchronize(self.device)
-        if lens is not None:
-            self.lens = list(lens[0])
-        g = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(g):
-            self.step(B)
-        if lens is not None:
-            self.lens = lens[0]
-            self.kv_len.copy_(lens[1])
+        try:
+            if lens is not None:
+                self.lens = list(lens[0])
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                self.step(B)
+        finally:
+            if lens is not None:
+                self.lens = lens[0]
+                self.kv_len.copy_(lens[1])
         self.graphs[B] = g
         return g
 

@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import synthgen as sg
+from activation_sparse_ffn_predictor_amd import SffnError
 from activation_sparse_ffn_predictor_amd.stack import AttnConfig, SparseFFNStack
 
 pytestmark = pytest.mark.gpu
@@ -32,3 +33,42 @@ def test_replay_of_an_uncaptured_batch(gpu_ready):
     st.replay(2)
     assert state(st) == ([4, 1, 0, 0], [4, 1, 0, 0])
     del g
+
+
+@pytest.mark.parametrize("B", [0, -1, 5])
+def test_batches_out_of_range(gpu_ready, B):
+    st = toy(gpu_ready)
+    before = state(st)
+    for call in (st.step, st.capture, st.replay):
+        with pytest.raises((KeyError, ValueError)):
+            call(B)
+        assert state(st) == before
+
+
+def test_a_call_refused_below_leaves_the_sequences(gpu_ready, monkeypatch):
+    """The library turns a layer's call away (here: a cache whose page size it does not take)."""
+    st = toy(gpu_ready)
+    st.prompt(1, torch.randn((2, 512), device=gpu_ready))
+    before = state(st)
+    good = st.layers[0]["kv"]
+    st.layers[0]["kv"] = tuple(t[:, :, :12].contiguous() for t in good)
+    for call in (lambda: st.step(2), lambda: st.prompt(1, torch.randn((3, 512), device=gpu_ready)), lambda: st.capture(3)):
+        with pytest.raises(SffnError):
+            call()
+        assert state(st) == before
+    st.layers[0]["kv"] = good
+    st.step(2)
+    assert state(st) == ([1, 3, 0, 0], [1, 3, 0, 0])
+
+
+def test_prompts_longer_than_the_ffn_takes(gpu_ready):
+    """The sparse FFN takes up to 64 tokens a call, so a prompt of more is refused, and changes nothing."""
+    st = toy(gpu_ready, max_batch=70, max_len=100)
+    st.prompt(2, torch.randn((64, 512), device=gpu_ready))
+    before = state(st)
+    for call in (lambda: st.prompt(2, torch.randn((65, 512), device=gpu_ready)[:, :512]), lambda: st.step(66)):
+        with pytest.raises((ValueError, SffnError)):
+            call()
+        assert state(st) == before
+    st.prompt(2, torch.randn((30, 512), device=gpu_ready))
+    assert st.lens[2] == 94
