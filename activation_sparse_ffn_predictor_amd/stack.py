@@ -169,10 +169,11 @@ class SparseFFNStack:
             raise ValueError(f"prompt: x is fp32 [T, {self.wl.D}] on {self.out.device}")
         x = x.contiguous()
         self._room(s, T)
-        cu = self.cu_prompt.setdefault(T, torch.tensor([0, T], dtype=torch.int32, device=self.device))
+        if T not in self.cu_prompt:
+            self.cu_prompt[T] = torch.tensor([0, T], dtype=torch.int32, device=self.device)
         one = slice(s, s + 1)
         with self._grown(one, T):
-            self._layers(x, T, cu, self.kv_len[one], self.table[one], T)
+            self._layers(x, T, self.cu_prompt[T], self.kv_len[one], self.table[one], T)
 
     def reset(self):
         """Forget every sequence's tokens."""

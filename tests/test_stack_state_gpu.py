@@ -72,3 +72,21 @@ def test_prompts_longer_than_the_ffn_takes(gpu_ready):
         assert state(st) == before
     st.prompt(2, torch.randn((30, 512), device=gpu_ready))
     assert st.lens[2] == 94
+
+
+def test_prompt_uploads_nothing_it_has(gpu_ready):
+    """A prompt of a length that was entered before builds no new tensor of its boundaries (one is kept for each length)."""
+    st = toy(gpu_ready)
+    st.prompt(0, torch.randn((3, 512), device=gpu_ready))
+    kept = st.cu_prompt[3]
+    real, made = torch.tensor, []
+
+    def spy(*a, **kw):
+        made.append(a)
+        return real(*a, **kw)
+    torch.tensor = spy
+    try:
+        st.prompt(1, torch.randn((3, 512), device=gpu_ready))
+    finally:
+        torch.tensor = real
+    assert not made and st.cu_prompt[3] is kept
