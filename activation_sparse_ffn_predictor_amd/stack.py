@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import contextlib
 import dataclasses
+import math
 from typing import Dict, List, Optional
 
 import numpy as np
@@ -87,7 +88,10 @@ class SparseFFNStack:
     def _attn_setup(self, seed: int):
         """Projections and norm weights (synthetic, normal), caches, page table and buffers of the attention half."""
         c, D, B, dev = self.attn, self.wl.D, self.max_batch, self.device
-        if c.kv_type not in KV_TYPES or c.max_len < 1 or c.n_heads % c.n_kv_heads:
+        step = 8 if c.kv_type == "f16" else 16
+        if (c.kv_type not in KV_TYPES or min(c.max_len, c.n_kv_heads, c.n_heads) < 1 or c.n_heads % c.n_kv_heads
+                or not 16 <= c.head_dim <= 256 or c.head_dim % step or c.page not in (16, 32, 64, 128, 256, 512, 1024)
+                or min(c.window, c.sinks) < 0 or not (c.eps >= 0 and math.isfinite(c.eps))):
             raise ValueError(f"attention: {c}")
         width, cols = (c.n_heads + 2 * c.n_kv_heads) * c.head_dim, -(-c.max_len // c.page)
         kt, cache = KV_TYPES[c.kv_type], (B * cols, c.n_kv_heads, c.page, c.head_dim)

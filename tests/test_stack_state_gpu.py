@@ -90,3 +90,11 @@ def test_prompt_uploads_nothing_it_has(gpu_ready):
     finally:
         torch.tensor = real
     assert not made and st.cu_prompt[3] is kept
+
+
+@pytest.mark.parametrize("kw", [dict(n_kv_heads=0), dict(n_heads=0), dict(head_dim=60), dict(head_dim=0), dict(page=24), dict(page=8),
+                                dict(kv_type="i8", head_dim=72), dict(kv_type="bf16"), dict(max_len=0), dict(window=-1), dict(sinks=-1),
+                                dict(n_heads=7), dict(eps=-1.0)])
+def test_configurations_are_checked_at_the_start(gpu_ready, kw):
+    with pytest.raises(ValueError):
+        toy(gpu_ready, **kw)
