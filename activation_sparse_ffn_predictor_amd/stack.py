@@ -32,6 +32,10 @@ from . import _lib
 from .pack import hot_first_perm, pack_layer
 
 
+KV_TYPES = {"f16": torch.float16, "i8": torch.int8, "e4m3": torch.float8_e4m3fn}
+PAGES = tuple(1 << b for b in range(4, 11))
+
+
 @dataclasses.dataclass(frozen=True)
 class AttnConfig:
     """Attention of a stack's layers: head layout, cache type ("f16", "i8" or "e4m3") and room, window and sinks."""
@@ -45,8 +49,12 @@ class AttnConfig:
     sinks: int = 0
     eps: float = 1e-5
 
-
-KV_TYPES = {"f16": torch.float16, "i8": torch.int8, "e4m3": torch.float8_e4m3fn}
+    def __post_init__(self):
+        if (self.kv_type not in KV_TYPES or min(self.max_len, self.n_kv_heads, self.n_heads) < 1
+                or self.n_heads % self.n_kv_heads or not 16 <= self.head_dim <= 256
+                or self.head_dim % (8 if self.kv_type == "f16" else 16) or self.page not in PAGES
+                or min(self.window, self.sinks) < 0 or not (self.eps >= 0 and math.isfinite(self.eps))):
+            raise ValueError(f"attention: {self}")
 
 
 class SparseFFNStack:
@@ -88,11 +96,6 @@ class SparseFFNStack:
     def _attn_setup(self, seed: int):
         """Projections and norm weights (synthetic, normal), caches, page table and buffers of the attention half."""
         c, D, B, dev = self.attn, self.wl.D, self.max_batch, self.device
-        step = 8 if c.kv_type == "f16" else 16
-        if (c.kv_type not in KV_TYPES or min(c.max_len, c.n_kv_heads, c.n_heads) < 1 or c.n_heads % c.n_kv_heads
-                or not 16 <= c.head_dim <= 256 or c.head_dim % step or c.page not in (16, 32, 64, 128, 256, 512, 1024)
-                or min(c.window, c.sinks) < 0 or not (c.eps >= 0 and math.isfinite(c.eps))):
-            raise ValueError(f"attention: {c}")
         width, cols = (c.n_heads + 2 * c.n_kv_heads) * c.head_dim, -(-c.max_len // c.page)
         kt, cache = KV_TYPES[c.kv_type], (B * cols, c.n_kv_heads, c.page, c.head_dim)
         for l, t in zip(self.layer_ids, self.layers):
