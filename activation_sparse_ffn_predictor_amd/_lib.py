@@ -290,8 +290,7 @@ def attn(q, kv, cu, kv_len, table, max_q: int, max_kv: int, out, ws, scale: Opti
     """sffn_attn: attention of the new tokens q [T, Hq, head size] (fp16 or bf16) over the cache (see kv_write), causal,
     with an optional window and always-visible first tokens. out as q; lse [T, Hq] fp32 or None; ws a uint8 tensor of
     attn_workspace_size bytes (or None if that is 0); scale: 1 / sqrt(head size) unless given."""
-    rc = (_bound or _fast()).attn(q, kv, cu, kv_len, table, max_q, max_kv, out, ws,
-                                  q.shape[-1] ** -0.5 if scale is None else scale, window, sinks, lse,
+    rc = (_bound or _fast()).attn(q, kv, cu, kv_len, table, max_q, max_kv, out, ws, scale, window, sinks, lse,
                                   _handle_of(stream))
     if rc:
         _check(rc, "sffn_attn")

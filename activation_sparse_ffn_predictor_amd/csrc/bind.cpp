@@ -10,6 +10,7 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <stdexcept>
 #include <string>
 
@@ -200,7 +201,7 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (ws) same_device(*c.K, *ws, where);
     const sffn_seqs sq = seqs(a[2], a[3], a[4], T, *c.K, where);
     const int max_q = int_of(a[5]), max_kv = int_of(a[6]), window = int_of(a[10]), sinks = int_of(a[11]);
-    const float scale = (float)number(a[9]);
+    const float scale = (float)(a[9] == Py_None ? std::pow((double)c.c.head_dim, -0.5) : number(a[9]));
     const int hq = as_int(Hq, where);
     return call(*c.K, a[13], where, [&](void* st) {
       return p_attn(c.c, sq, ty, q.data_ptr(), lq, hq, max_q, max_kv, scale, window, sinks, out.data_ptr(), lo,
