@@ -27,8 +27,6 @@ __device__ __forceinline__ int few_swz(int key, bool codes) {
   return RB >= 256 ? (key & 7) << 1 : ((key >> 1) & 3) << 1;
 }
 
-// KVM 0: cache of the query's 16-bit type, 1: int8, 2: e4m3 (both computed in fp16: codes are exact there, and bf16
-// queries are scaled by one power of two into fp16's range). DP: head size padded to 64, 128 or 256. QB: 16-row tiles.
 // The sequence and share of a block.
 struct Place {
   Seq sq;
@@ -36,6 +34,8 @@ struct Place {
   int n, rows, p0, p1, hk, s, split, used, u0, u1;
 };
 
+// KVM 0: cache of the query's 16-bit type, 1: int8, 2: e4m3 (both computed in fp16: codes are exact there, and bf16
+// queries are scaled by one power of two into fp16's range). DP: head size padded to 64, 128 or 256. QB: 16-row tiles.
 template <bool BF, int KVM, int DP, int QB, int NW>
 __device__ __forceinline__ void few_rows(const AttnArgs& a, const Place& pl, char* lds, float (*mlw)[2], uint4* qlds) {
   constexpr int NT = NW * 64;

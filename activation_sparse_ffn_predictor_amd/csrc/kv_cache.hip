@@ -82,16 +82,6 @@ __device__ __forceinline__ uint2 encode8(const float* x, float s) {
   return c;
 }
 
-// The slot of token t in the cache (row index of head 0's slot 0 of its page is pid * hkv << psh), or false.
-__device__ __forceinline__ bool find_slot(const Kv& kv, const Seqs& sq, int s, int t, int& pid, int& slot) {
-  if (s >= sq.S) return false;
-  const int a = sq.cu[s], n = sq.cu[s + 1] - a, pos = sq.len[s] - n + (t - a);
-  if (t < a || pos < 0 || (pos >> kv.psh) >= sq.cols) return false;
-  pid = sq.table[(long)s * sq.ldt + (pos >> kv.psh)];
-  slot = pos & ((1 << kv.psh) - 1);
-  return (unsigned)pid < (unsigned)kv.n_pages;
-}
-
 // The rows (cache row index of head 0's copy, or -1) of the PASS tokens t0, t0 + step, ...: neighbours mostly belong to
 // one sequence, so it is searched for once.
 template <int LPR, int PASS>
