@@ -203,8 +203,9 @@ __device__ __forceinline__ uint32_t nan_codes4(const uint4& t) { return nan_code
 __device__ __forceinline__ uint4 finite_codes4(const uint4& t) {
   return make_uint4(finite_codes(t.x), finite_codes(t.y), finite_codes(t.z), finite_codes(t.w));
 }
-// bf16 queries for fp16 products: all times one power of two that takes the largest, `big`, to 2^14 .. 2^15 (exact
-// but for elements below 2^-29 of it, which lose bits under 2^-40 of it); c takes the factor back.
+// bf16 queries for fp16 products: all times one power of two that takes the largest, `big`, to 2^14 .. 2^15 (exact but for
+// elements below 2^-31 of it, rounded to fp16's smallest step: 2^-38 of it or less; the factor ends at 2^126, so under 2^-112 the
+// largest comes out smaller and the step is 2^-150 of the elements as they were); c takes the factor back.
 __device__ __forceinline__ float to_f16_range(float big, float& c) {
   const int e = big > 0.f && big < 3.4e38f ? 14 - ((int)((__float_as_uint(big) >> 23) & 255) - 127) : 0;
   const int e1 = min(max(e, -126), 126);

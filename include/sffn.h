@@ -233,7 +233,8 @@ int sffn_profile_end(float* ms, int max);
  *   scale = fp32(max|x| / top), top = 127 or 448;  code = x / scale rounded to nearest, ties to even (of the exact
  *   quotient);  value = code * scale.
  * Rows whose scale would be below 2^-60 are stored as zeros with scale 0; a row that holds an infinity or NaN is
- * stored with scale NaN and codes 0. */
+ * stored with scale NaN and codes 0. sffn_kv_read takes any scale; sffn_attn takes V scales that are NaN, 0 (with codes 0) or
+ * finite and at least 2^-60, as they are stored. */
 typedef enum { SFFN_F32 = 0, SFFN_F16 = 1, SFFN_BF16 = 2, SFFN_I8 = 3, SFFN_E4M3 = 4 } sffn_type;
 
 /* One layer's cache (device pointers, contiguous): k, v [n_pages, n_kv_heads, page, head_dim], and for 8-bit types
@@ -251,7 +252,7 @@ typedef struct {
  * in all; cu [S + 1] ascends from 0) are the newest tokens of sequence s, whose cache holds kv_len[s] tokens with
  * them: the i-th of n stands at position kv_len[s] - n + i. Position p lies in slot p % page of page
  * table[s * table_stride + p / page]; a table row holds max_pages entries. Rows at and behind cu[S] belong to no
- * sequence: they are neither read nor written. The arrays are read on the device, so they are not checked on the
+ * sequence: they are not written, and what they hold has no effect. The arrays are read on the device, so they are not checked on the
  * host; whatever they hold, no access leaves the given tensors: a position outside the table row or a page id
  * outside 0 .. n_pages - 1 holds no token (not written, not read, not seen). New tokens keep their positions there: of a
  * sequence that has run past its table row the last ones are not held, and see what the row holds. kv_len counts up to
@@ -287,8 +288,10 @@ int sffn_kv_read(sffn_kv cache, sffn_seqs seqs, int type, void* k, int64_t k_str
  * out_stride elements apart (multiples of 8). lse [T, Hq] fp32 or NULL: the natural logarithm of the softmax's sum
  * (-infinity for a token that sees nothing). Scores, sums and accumulators are fp32; the weights enter the second
  * product as 16-bit values of the cache's type (fp16 over 8-bit caches; those under 2^-21 of a token's largest, times the
- * scales there, are off by up to 2^-32 of it), and 8-bit codes enter both products exactly. Over an 8-bit cache bf16 queries enter the
- * first one in steps of at most 2^-39 of the largest finite element among the rows of a workgroup.
+ * scales there, are off by up to 2^-32 of it), and 8-bit codes enter both products exactly. Over an 8-bit cache the V scales
+ * that one token sees lie within 2^80 of each other (beyond it the sum loses the part of those with small ones), and bf16
+ * queries enter the first product rounded to steps of 2^-38 of the largest finite element among the rows of a workgroup (of
+ * 2^-150 where that one is below 2^-112).
  * max_q: at least the largest number of new tokens of one sequence (tokens past it are not computed and their rows
  * stay as they were). max_kv: about the largest kv_len; it decides only over how many workgroups a sequence's keys
  * are spread. Up to 32 rows max_q * Hq / n_kv_heads (64 for head_dim <= 64, 16 for head_dim > 128) run the few-row kernel

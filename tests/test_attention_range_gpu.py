@@ -79,3 +79,26 @@ def test_maxima_that_grow(gpu_ready, n, qt, kvt):
         o, l, to, tl = definition(b, q.to(DT[qt]), 4, 1.0)
         assert_near(out, o, to, f"out, step {step}")
         assert_near(lse, l, tl, f"lse, step {step}")
+
+
+@pytest.mark.parametrize("qt", ["f16", "bf16"])
+@pytest.mark.parametrize("kvt", ["i8", "e4m3"])
+def test_value_scales_far_apart(gpu_ready, qt, kvt):
+    """V rows of sizes 2^-40 to 2^40 side by side (cache contents given as codes and scales): the large ones are the output,
+    and the small ones count in the sum."""
+    for n in (2, 60):
+        b = Paged([n], [300], 2, 64, 16, "f16", kvt, seed=n)
+        b.qt = qt
+        size = torch.tensor([2.0 ** -40, 1.0, 2.0 ** 40, 2.0 ** -20])[torch.arange(16) % 4]
+        b.scales = b.scales.clone()
+        b.scales[1] *= size
+        b.val[1] *= size.double()[:, None]
+        if qt == "f16":                              # outputs within fp16's range
+            b.scales[1] *= 2.0 ** -42
+            b.scales[1] = b.scales[1].clamp(min=2.0 ** -60)
+            b.val[1] = b.codes[1].double() * b.scales[1].double()[..., None]
+        q = (torch.randn((n, 4, 64), generator=b.g) * 2).to(DT[qt])
+        out, lse = run_attn(b, q, 4, gpu_ready)
+        o, l, to, tl = definition(b, q, 4, 0.125)
+        assert_near(out, o, to, "out")
+        assert_near(lse, l, tl, "lse")
