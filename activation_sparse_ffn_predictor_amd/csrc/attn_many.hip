@@ -4,11 +4,11 @@
 // 32 rows, its 16 scores per 32 keys are that row's, and they are the second product's operand as they are. Four
 // waves (128 rows of one K/V head, the query heads of a token next to each other) share tiles of 64 keys in LDS.
 //
-// Bound by the matrix cores and the power they draw: 4096 tokens of 64 heads on 8 of 128 over 8192, 825 GFLOP, take 855 to
-// 960 us in fp16 (box to box; 859 to 964 TFLOP/s where a large fp16 product reaches 1221) and 810 to 850 in bf16, with the
-// matrix cores busy 48% of the time at a mean clock of about 1.8 GHz and no LDS conflicts. Wave priorities around the
+// Bound by the matrix cores and the power they draw: 4096 tokens of 64 heads on 8 of 128 over 8192, 825 GFLOP, take 850 to
+// 960 us in fp16 (box to box; 859 to 970 TFLOP/s where a large fp16 product reaches 1221 to 1289) and 807 to 850 in bf16 (970
+// to 1022, where one of bf16 reaches 1376 to 1389), with the matrix cores busy 48% of the time at a mean clock of about 1.8 GHz and no LDS conflicts. Wave priorities around the
 // products, reading operands further ahead, and computing the next tile's scores under this one's softmax changed that by
-// -2 to +2%. int8: 1.1 to 1.2 ms, with the codes widened once a workgroup on their way into LDS. What was worth it: tiles
+// -2 to +2%. int8 and e4m3: 1.0 to 1.2 ms, with the codes widened once a workgroup on their way into LDS. What was worth it: tiles
 // straight to LDS, a maximum that seldom moves, no second copy of the product loops (2557 -> 870 us).
 #include "attn.h"
 

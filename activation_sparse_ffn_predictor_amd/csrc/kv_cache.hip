@@ -1,8 +1,8 @@
 // Paged K/V cache: new tokens written (as they are or quantised to 8 bits), and a range of tokens read back.
 //
 // Both are bound by memory, each byte moved once; a row of a head is a few lanes' work, so that its maximum needs no LDS
-// and neighbouring tokens of a head fill neighbouring slots. Measured: 4000 tokens of 40 heads of 128 written in 30 us as
-// bf16 (5.3 TB/s) and as e4m3 (4.1 TB/s; 24.7 us without the encoding, which is what then bounds it); 54000 tokens
+// and neighbouring tokens of a head fill neighbouring slots. Measured: 4000 tokens of 40 heads of 128 written in 32.5 us as
+// bf16 (5.0 TB/s) and in 28 to 31 as e4m3 (4.0 to 4.4 TB/s; 24.7 us without the encoding, which is what then bounds it); 54000 tokens
 // read from e4m3 to bf16, 703 MB in 134 to 143 us (box to box; 5.0 to 5.3 TB/s).
 #include "attn.h"
 
@@ -217,7 +217,7 @@ hipError_t go(bool write, const Kv& kv, int kvm, bool bf, const Seqs& sq, char* 
               hipStream_t st) {
   constexpr int RPB = 256 / LPR;
   // two tokens a thread where that still leaves 32 workgroups a compute unit (54000 tokens of 40 heads read from e4m3:
-  // 155 -> 134 us; 4000 tokens written in 10000 workgroups: 33 us, in 5000 34)
+  // 155 -> 134 us; 4000 tokens written to e4m3 in 10000 workgroups: 28.1 us, in 5000 28.6, 6400 in 16000 47.3, in 8000 50.3)
   const long one = (long)((sq.T + RPB - 1) / RPB) * kv.hkv;
   const bool two = one >= 2 * 32 * 256;
   const int per = two ? 2 * RPB : RPB;
