@@ -266,8 +266,12 @@ def _own(s):
         return dict(q=s["q_out"], k=s["k_out"])
     kv = (s["K"], s["V"], s["Ks"], s["Vs"])
     if s["op"] == "mass":
+        if "ws" not in s:
+            need = _lib.attn_mass_workspace_size(s["S"], s["q"].shape[1], s["K"].shape[1], s["d"], s["max_q"], s["max_kv"],
+                                                 s["mass"].shape[2])
+            s["ws"] = torch.empty(need, dtype=torch.uint8, device="cuda")
         _lib.attn_mass(s["q"], kv, s["cu"], s["kv_len"], s["table"], s["max_q"], s["max_kv"], s["lse"], s["mass"], s["pos"],
-                       seq_len=s["seq_len"], mass_out=s["mass_out"], scale=s["scale"], window=s["window"], sinks=s["sinks"])
+                       s["ws"], seq_len=s["seq_len"], mass_out=s["mass_out"], scale=s["scale"], window=s["window"], sinks=s["sinks"])
         return dict(mass=s["mass_out"], pos=s["pos"])
     if "ws" not in s:
         need = _lib.kv_evict_workspace_size(s["S"], s["K"].shape[1], s["mass"].shape[2], s["keep"])
