@@ -20,7 +20,9 @@ EXPORTS = ("sffn_status_string", "sffn_last_error", "sffn_workspace_size", "sffn
            "sffn_predict_hot", "sffn_forward", "sffn_forward_q4", "sffn_profile_begin", "sffn_profile_end",
            "sffn_forward_path", "sffn_decode", "sffn_decode_path", "sffn_decode_noalloc",
            "sffn_noalloc_scratch_bytes", "sffn_kv_write", "sffn_kv_read", "sffn_attn", "sffn_attn_path",
-           "sffn_attn_workspace_size", "sffn_add_rmsnorm")
+           "sffn_attn_workspace_size", "sffn_add_rmsnorm", "sffn_quant128", "sffn_mm_e4m3", "sffn_mm_workspace_size",
+           "sffn_qk_norm_rope", "sffn_attn_mass", "sffn_attn_mass_workspace_size", "sffn_kv_evict",
+           "sffn_kv_evict_workspace_size")
 K_PRED_H, K_PRED_Z, K_ROWS, K_COLS = 0, 1, 2, 3
 
 
@@ -89,6 +91,19 @@ def lib() -> ctypes.CDLL:
         h.sffn_attn.restype = i32
         h.sffn_add_rmsnorm.argtypes = [i32, vp, i64, i32, vp, i64, vp, f64, i32, i32, i32, vp, i64, vp, vp, i64, vp]
         h.sffn_add_rmsnorm.restype = i32
+        h.sffn_quant128.argtypes, h.sffn_quant128.restype = [i32, vp, i64, i32, i32, i32, vp, i64, vp, vp], i32
+        h.sffn_mm_workspace_size.argtypes, h.sffn_mm_workspace_size.restype = [i32] * 3, sz
+        h.sffn_mm_e4m3.argtypes = [vp, i64, vp, vp, i64, vp, i32, i32, i32, i32, vp, i64, vp, sz, vp]
+        h.sffn_mm_e4m3.restype = i32
+        h.sffn_qk_norm_rope.argtypes = [i32, vp, vp, i32, i32, vp, i64, i32, vp, i64, i32, i32, i32, vp, vp, f64, vp, i32, i32, vp,
+                                        i64, vp, i64, vp]
+        h.sffn_qk_norm_rope.restype = i32
+        h.sffn_attn_mass_workspace_size.argtypes, h.sffn_attn_mass_workspace_size.restype = [i32] * 7, sz
+        h.sffn_attn_mass.argtypes = [_KV, _Seqs, vp, i32, vp, i64, i32, i32, i32, f32, i32, i32, vp, vp, vp, vp, i32, vp, sz, vp]
+        h.sffn_attn_mass.restype = i32
+        h.sffn_kv_evict_workspace_size.argtypes, h.sffn_kv_evict_workspace_size.restype = [i32] * 4, sz
+        h.sffn_kv_evict.argtypes = [_KV, vp, vp, vp, i32, i32, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+        h.sffn_kv_evict.restype = i32
         _handle = h
     return _handle
 
@@ -245,7 +260,8 @@ def _fast():
         from . import _bind
         h = lib()
         _bind.bind(*(ctypes.cast(getattr(h, n), ctypes.c_void_p).value
-                     for n in ("sffn_kv_write", "sffn_kv_read", "sffn_attn", "sffn_add_rmsnorm")))
+                     for n in ("sffn_kv_write", "sffn_kv_read", "sffn_attn", "sffn_add_rmsnorm", "sffn_quant128",
+                               "sffn_mm_e4m3", "sffn_qk_norm_rope", "sffn_attn_mass", "sffn_kv_evict")))
         _bound = _bind
     return _bound
 
@@ -303,3 +319,67 @@ def add_rmsnorm(x, res, w, eps: float, y, res_out=None, y_scale=None, stream=Non
     rc = (_bound or _fast()).add_rmsnorm(x, res, w, eps, y, res_out, y_scale, _handle_of(stream))
     if rc:
         _check(rc, "sffn_add_rmsnorm")
+
+
+# ------------------------------------------------------------- 8-bit products, head norms with rotation, eviction
+def quant128(x, y, scale, rows: int = 1, stream=None):
+    """sffn_quant128: x [T, D] fp32, fp16 or bf16 as codes y [T, D] float8_e4m3fn with one scale for each block of `rows` (1:
+    activations, 128: weights) x 128 columns, scale [ceil(T / rows), ceil(D / 128)] fp32."""
+    rc = (_bound or _fast()).quant128(x, y, scale, rows, _handle_of(stream))
+    if rc:
+        _check(rc, "sffn_quant128")
+
+
+def mm_workspace_size(T: int, N: int, K: int) -> int:
+    """Bytes of workspace that mm_e4m3 needs for these sizes (0: none)."""
+    return int(lib().sffn_mm_workspace_size(T, N, K))
+
+
+def mm_e4m3(a, a_scale, b, b_scale, out, ws=None, stream=None):
+    """sffn_mm_e4m3: out [T, N] = a [T, K] b [N, K]^T for float8_e4m3fn codes with scales of blocks of 128 columns of a row
+    (a_scale [T, ceil(K / 128)]) and of 128 x 128 (b_scale [ceil(N / 128), ceil(K / 128)]); out fp32, fp16 or bf16; ws a uint8
+    tensor of mm_workspace_size bytes (or None if that is 0)."""
+    rc = (_bound or _fast()).mm_e4m3(a, a_scale, b, b_scale, out, ws, _handle_of(stream))
+    if rc:
+        _check(rc, "sffn_mm_e4m3")
+
+
+def qk_norm_rope(q, k, w_q, w_k, eps: Optional[float], cu, seq_len, freq, q_out, k_out, interleaved: bool = False, stream=None):
+    """sffn_qk_norm_rope: norms of every head of q [T, Hq, head size] and k [T, K/V heads, head size] (eps None: no norm; w_q,
+    w_k [head size] fp32 or None: 1), then the rotation of the first 2 * len(freq) elements (freq None: none) by positions
+    seq_len[s] - n + i, in halves or in neighbouring pairs. k and k_out may be None; q_out may be q, k_out k."""
+    rc = (_bound or _fast()).qk_norm_rope(q, k, w_q, w_k, eps, cu, seq_len, freq, q_out, k_out, interleaved, _handle_of(stream))
+    if rc:
+        _check(rc, "sffn_qk_norm_rope")
+
+
+def attn_mass_workspace_size(S: int, Hq: int, n_kv_heads: int, head_dim: int, max_q: int, max_kv: int, W: int) -> int:
+    """Bytes of workspace that attn_mass needs for these sizes (0: none)."""
+    return int(lib().sffn_attn_mass_workspace_size(S, Hq, n_kv_heads, head_dim, max_q, max_kv, W))
+
+
+def attn_mass(q, kv, cu, kv_len, table, max_q: int, max_kv: int, lse, mass, pos, ws=None, seq_len=None, mass_out=None,
+              scale: Optional[float] = None, window: int = 0, sinks: int = 0, stream=None):
+    """sffn_attn_mass: the attention weight that every cached token got in the attn call with these arguments (lse as it wrote
+    it), added to mass [S, K/V heads, slots] fp32 (mass_out None: in place); new tokens begin at 0 and enter their positions in
+    pos (int32, same sizes), counted by seq_len [S] (None: kv_len)."""
+    rc = (_bound or _fast()).attn_mass(q, kv, cu, kv_len, table, max_q, max_kv, lse, mass, pos, ws, seq_len, mass_out, scale,
+                                       window, sinks, _handle_of(stream))
+    if rc:
+        _check(rc, "sffn_attn_mass")
+
+
+def kv_evict_workspace_size(S: int, n_kv_heads: int, W: int, keep: int) -> int:
+    """Bytes of workspace that kv_evict needs for these sizes."""
+    return int(lib().sffn_kv_evict_workspace_size(S, n_kv_heads, W, keep))
+
+
+def kv_evict(kv, kv_len, table, mass, pos, keep: int, src, ws, seq_len=None, sinks: int = 0, recent: int = 0, kv_len_out=None,
+             mass_out=None, pos_out=None, stream=None):
+    """sffn_kv_evict: cuts every sequence with more than `keep` cached tokens down to them: those at positions below `sinks` or
+    among the last `recent` (of seq_len tokens; None: kv_len), then those with the largest mass. src [S, K/V heads, keep] int32
+    tells which slot each came from. kv_len_out, mass_out, pos_out None: in place."""
+    rc = (_bound or _fast()).kv_evict(kv, kv_len, table, mass, pos, keep, src, ws, seq_len, sinks, recent, kv_len_out, mass_out,
+                                      pos_out, _handle_of(stream))
+    if rc:
+        _check(rc, "sffn_kv_evict")

@@ -318,3 +318,8 @@ int sffn_attn_few_rows(int d);
 hipError_t sffn_launch_attn_few(const sffn::AttnArgs& a, int qt, int kvt, hipStream_t st);
 hipError_t sffn_launch_attn_many(const sffn::AttnArgs& a, int qt, int kvt, hipStream_t st);
 hipError_t sffn_launch_attn_join(const sffn::AttnArgs& a, int qt, bool few, hipStream_t st);
+hipError_t sffn_launch_quant128(const void* x, int xt, long ldx, int T, int D, int rows, void* y, long ldy, float* scale,
+                                hipStream_t st);
+hipError_t sffn_launch_rope(int type, const int* cu, const int* len, int S, int T, const void* q, long ldq, int hq,
+                            const void* k, long ldk, int hk, int d, int norm, const float* wq, const float* wk, double eps,
+                            const float* freq, int rot, int inter, void* qo, long ldqo, void* ko, long ldko, hipStream_t st);

@@ -1,4 +1,5 @@
-// C ABI of the residual norm, the paged K/V cache and the attention: argument checks and dispatch (host only).
+// C ABI of the residual norm, the paged K/V cache, the attention, the block-scaled products, the head norms with rotation and
+// the eviction: argument checks and dispatch (host only).
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -7,6 +8,9 @@
 
 #include "../../include/sffn.h"
 #include "attn.h"
+#include "evict.h"
+#include "mass.h"
+#include "mm.h"
 
 namespace {
 
@@ -130,6 +134,37 @@ int shares(int T, int S, int Hkv, int G, int d, int max_q, int max_kv, int windo
   }
   return (int)best;
 }
+int check_workspace(const void* ws, size_t have, size_t need) {
+  if (!need) return SFFN_OK;
+  if (!ws) return fail(SFFN_ERR_NULL, "workspace is NULL");
+  if (!al(ws, 256)) return fail(SFFN_ERR_ALIGN, "workspace not 256-byte aligned");
+  if (have < need) return fail(SFFN_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", have, need);
+  return SFFN_OK;
+}
+bool mm_sizes_ok(int N, int K) { return N >= 8 && N <= (1 << 22) && N % 8 == 0 && K >= 16 && K <= 65536 && K % 16 == 0; }
+// mass and pos [S, n_kv_heads, W]
+int check_track(int S, int Hkv, int W) {
+  if (W < 1 || (int64_t)S * Hkv >= (1 << 22) || (long double)S * Hkv * W >= 2147483648.0L) return fail(SFFN_ERR_SHAPE, "S=%d, n_kv_heads=%d, W=%d", S, Hkv, W);
+  return SFFN_OK;
+}
+// Workgroups of an attn_mass call along the keys, and the shares of its rows
+struct MassPlan {
+  int tiles, rs, wp;
+};
+MassPlan mass_plan(int S, int Hkv, int G, int d, int max_q, int max_kv, int W) {
+  const int64_t keys = std::max(1, std::min(max_kv, W)), rows = (int64_t)max_q * G, seqs = (int64_t)S * Hkv;
+  MassPlan p{1, 1, 0};
+  if (sffn::mass_few(rows, d)) {
+    p.tiles = (int)std::max<int64_t>(1, std::min((keys + 127) / 128, (2048 + seqs - 1) / seqs));
+    return p;
+  }
+  const int tile = sffn::mass_tile(d);
+  p.tiles = (int)std::min<int64_t>((keys + tile - 1) / tile, std::max<int64_t>(1, (1 << 20) / seqs));
+  const int64_t blocks = seqs * p.tiles;
+  if (blocks < 1024) p.rs = (int)std::max<int64_t>(1, std::min({(1024 + blocks - 1) / blocks, (rows + 511) / 512, (int64_t)16}));
+  p.wp = p.tiles * tile;
+  return p;
+}
 size_t po_bytes(int T, int Hq, int d, int ns) { return align256((size_t)T * Hq * ns * d * sizeof(float)); }
 
 }  // namespace
@@ -252,6 +287,174 @@ int sffn_add_rmsnorm(int x_type, const void* x, int64_t x_stride, int res_type, 
   const hipError_t e = sffn_launch_add_rmsnorm(x, x_type, res, res_type, w, eps, T, D, x_stride, res_stride, y, y_type,
                                                y_scale, res_out, y_stride, res_out_stride, (hipStream_t)stream);
   return e == hipSuccess ? SFFN_OK : sffn_err_hip(e, "add_rmsnorm launch");
+}
+
+int sffn_quant128(int x_type, const void* x, int64_t x_stride, int T, int D, int rows, void* y, int64_t y_stride, float* scale,
+                  void* stream) {
+  sffn_err_clear();
+  if (x_type != SFFN_F32 && !is16(x_type)) return fail(SFFN_ERR_ARG, "quant128: type %d", x_type);
+  if (rows != 1 && rows != 128) return fail(SFFN_ERR_ARG, "quant128: rows=%d: need 1 or 128", rows);
+  if (T < 0 || T > MAX_T) return fail(SFFN_ERR_SHAPE, "T=%d outside [0, %d]", T, MAX_T);
+  if (D < 8 || D > 65536 || D % 8) return fail(SFFN_ERR_SHAPE, "D=%d: need 8 <= D <= 65536, D %% 8 == 0", D);
+  if (T == 0) return SFFN_OK;
+  int s = check_rows("x", x, x_stride, D);
+  if (!s) s = check_rows("y", y, y_stride, D);
+  if (s) return s;
+  if (!scale) return fail(SFFN_ERR_NULL, "scale is required");
+  if (!al(scale, 4)) return fail(SFFN_ERR_ALIGN, "scale misaligned");
+  if (x == y || x == scale || y == (void*)scale) return fail(SFFN_ERR_ARG, "quant128: an output overlaps another tensor");
+  const hipError_t e = sffn_launch_quant128(x, x_type, x_stride, T, D, rows, y, y_stride, scale, (hipStream_t)stream);
+  return e == hipSuccess ? SFFN_OK : sffn_err_hip(e, "quant128 launch");
+}
+
+size_t sffn_mm_workspace_size(int T, int N, int K) {
+  if (T < 1 || T > MAX_T || !mm_sizes_ok(N, K)) return 0;
+  return align256(sffn_mm_workspace(T, N, K));
+}
+
+int sffn_mm_e4m3(const void* a, int64_t a_stride, const float* a_scale, const void* b, int64_t b_stride, const float* b_scale,
+                 int T, int N, int K, int out_type, void* out, int64_t out_stride, void* ws, size_t ws_bytes, void* stream) {
+  sffn_err_clear();
+  if (out_type != SFFN_F32 && !is16(out_type)) return fail(SFFN_ERR_ARG, "mm_e4m3: type %d", out_type);
+  if (T < 0 || T > MAX_T) return fail(SFFN_ERR_SHAPE, "T=%d outside [0, %d]", T, MAX_T);
+  if (!mm_sizes_ok(N, K))
+    return fail(SFFN_ERR_SHAPE, "N=%d, K=%d: need N %% 8 == 0, 8 <= N <= 2^22, K %% 16 == 0, 16 <= K <= 65536", N, K);
+  if ((int64_t)((T + 127) / 128) * ((N + 127) / 128) >= ((int64_t)1 << 24)) return fail(SFFN_ERR_SHAPE, "T=%d, N=%d: too many tiles", T, N);
+  if (T == 0) return SFFN_OK;
+  int s = check_rows("a", a, a_stride, K);
+  if (!s) s = check_rows("b", b, b_stride, K);
+  if (!s) s = check_rows("out", out, out_stride, N);
+  if (s) return s;
+  if (a_stride % 16 || b_stride % 16 || a_stride > (1 << 22) || b_stride > (1 << 22))
+    return fail(SFFN_ERR_SHAPE, "mm_e4m3: strides %lld, %lld: need multiples of 16, at most 2^22", (long long)a_stride, (long long)b_stride);
+  if (!a_scale || !b_scale) return fail(SFFN_ERR_NULL, "a_scale and b_scale are required");
+  if (!al(a_scale, 4) || !al(b_scale, 4)) return fail(SFFN_ERR_ALIGN, "a_scale or b_scale misaligned");
+  if (out == a || out == b || out == a_scale || out == b_scale) return fail(SFFN_ERR_ARG, "mm_e4m3: out overlaps an input");
+  const size_t need = sffn_mm_workspace_size(T, N, K);
+  if ((s = check_workspace(ws, ws_bytes, need))) return s;
+  const sffn::MmArgs g{(const char*)a, (const char*)b, a_scale, b_scale, out, (char*)ws, (long)a_stride, (long)b_stride, (long)out_stride, T, N, K};
+  const hipError_t e = sffn_launch_mm(g, out_type, (hipStream_t)stream);
+  return e == hipSuccess ? SFFN_OK : sffn_err_hip(e, "mm_e4m3 launch");
+}
+
+int sffn_qk_norm_rope(int type, const int32_t* cu, const int32_t* seq_len, int S, int T, const void* q, int64_t q_stride, int Hq,
+                      const void* k, int64_t k_stride, int n_kv_heads, int head_dim, int norm, const float* w_q, const float* w_k,
+                      double eps, const float* freq, int rot, int interleaved, void* q_out, int64_t q_out_stride, void* k_out,
+                      int64_t k_out_stride, void* stream) {
+  sffn_err_clear();
+  if (!is16(type)) return fail(SFFN_ERR_ARG, "type %d is not a 16-bit type", type);
+  if (!cu || !seq_len) return fail(SFFN_ERR_NULL, "cu and seq_len are required");
+  if (S < 1 || S > MAX_S) return fail(SFFN_ERR_SHAPE, "S=%d outside [1, %d]", S, MAX_S);
+  if (T < 0 || T > MAX_T) return fail(SFFN_ERR_SHAPE, "T=%d outside [0, %d]", T, MAX_T);
+  if (head_dim < 8 || head_dim > 256 || head_dim % 8)
+    return fail(SFFN_ERR_SHAPE, "head_dim=%d: need 8 <= head_dim <= 256, head_dim %% 8 == 0", head_dim);
+  if (rot < 0 || rot > head_dim || rot % 8) return fail(SFFN_ERR_SHAPE, "rot=%d: need 0 <= rot <= head_dim=%d, rot %% 8 == 0", rot, head_dim);
+  if (Hq < 1 || Hq > 65535 || (k && (n_kv_heads < 1 || n_kv_heads > 65535)))
+    return fail(SFFN_ERR_SHAPE, "Hq=%d, n_kv_heads=%d outside [1, 65535]", Hq, n_kv_heads);
+  if (norm && (!(eps >= 0.0) || !isfinite(eps))) return fail(SFFN_ERR_ARG, "eps=%g: need a finite eps >= 0", eps);
+  if (rot && !freq) return fail(SFFN_ERR_NULL, "freq is required");
+  if (!al(cu, 4) || !al(seq_len, 4) || !al(freq, 4) || !al(w_q, 4) || !al(w_k, 4)) return fail(SFFN_ERR_ALIGN, "qk_norm_rope: misaligned pointer");
+  if (T == 0) return SFFN_OK;
+  int s = check_rows("q", q, q_stride, (int64_t)Hq * head_dim);
+  if (!s) s = check_rows("q_out", q_out, q_out_stride, (int64_t)Hq * head_dim);
+  if (!s && k) s = check_rows("k", k, k_stride, (int64_t)n_kv_heads * head_dim);
+  if (!s && k) s = check_rows("k_out", k_out, k_out_stride, (int64_t)n_kv_heads * head_dim);
+  if (s) return s;
+  if ((q == q_out && q_stride != q_out_stride) || (k && k == k_out && k_stride != k_out_stride))
+    return fail(SFFN_ERR_ARG, "qk_norm_rope: an output is its input with another stride");
+  if (k && (q_out == k || k_out == q || k_out == q_out)) return fail(SFFN_ERR_ARG, "qk_norm_rope: an output overlaps another tensor");
+  const hipError_t e = sffn_launch_rope(type, cu, seq_len, S, T, q, q_stride, Hq, k, k_stride, n_kv_heads, head_dim, norm, w_q, w_k,
+                                        eps, freq, rot, interleaved, q_out, q_out_stride, k_out, k_out_stride, (hipStream_t)stream);
+  return e == hipSuccess ? SFFN_OK : sffn_err_hip(e, "qk_norm_rope launch");
+}
+
+size_t sffn_attn_mass_workspace_size(int S, int Hq, int n_kv_heads, int head_dim, int max_q, int max_kv, int W) {
+  if (!attn_sizes_ok(Hq, n_kv_heads, head_dim, max_q) || S < 1 || S > MAX_S || W < 1) return 0;
+  const MassPlan p = mass_plan(S, n_kv_heads, Hq / n_kv_heads, head_dim, max_q, max_kv, W);
+  return p.rs > 1 ? align256((size_t)S * n_kv_heads * p.rs * p.wp * sizeof(float)) : 0;
+}
+
+int sffn_attn_mass(sffn_kv c, sffn_seqs q, const int32_t* seq_len, int type, const void* qp, int64_t q_stride, int Hq, int max_q,
+                   int max_kv, float scale, int window, int sinks, const float* lse, const float* mass, float* mass_out,
+                   int32_t* pos, int W, void* ws, size_t ws_bytes, void* stream) {
+  sffn_err_clear();
+  int s = check_cache(c, type);
+  if (!s) s = check_seqs(q, c.page);
+  if (s) return s;
+  if (!seq_len || !mass || !mass_out || !pos) return fail(SFFN_ERR_NULL, "seq_len, mass, mass_out and pos are required");
+  if (Hq < c.n_kv_heads || Hq % c.n_kv_heads) return fail(SFFN_ERR_SHAPE, "Hq=%d is not a multiple of n_kv_heads=%d", Hq, c.n_kv_heads);
+  if ((int64_t)q.T * Hq >= ((int64_t)1 << 31)) return fail(SFFN_ERR_SHAPE, "T=%d, Hq=%d: T * Hq reaches 2^31", q.T, Hq);
+  if (max_q < 1) return fail(SFFN_ERR_SHAPE, "max_q=%d < 1", max_q);
+  if ((s = check_track(q.S, c.n_kv_heads, W))) return s;
+  if (!isfinite(scale)) return fail(SFFN_ERR_ARG, "scale is not finite");
+  if (window < 0 || sinks < 0) return fail(SFFN_ERR_ARG, "window=%d, sinks=%d: need both >= 0", window, sinks);
+  if (!al(seq_len, 4) || !al(lse, 4) || !al(mass, 4) || !al(mass_out, 4) || !al(pos, 4))
+    return fail(SFFN_ERR_ALIGN, "attn_mass: misaligned pointer");
+  if ((const void*)pos == mass || (void*)pos == mass_out) return fail(SFFN_ERR_ARG, "attn_mass: pos overlaps mass");
+  if (q.T == 0) return SFFN_OK;
+  if ((s = check_rows("q", qp, q_stride, (int64_t)Hq * c.head_dim))) return s;
+  if (!lse) return fail(SFFN_ERR_NULL, "lse is required");
+  const size_t need = sffn_attn_mass_workspace_size(q.S, Hq, c.n_kv_heads, c.head_dim, max_q, max_kv, W);
+  if ((s = check_workspace(ws, ws_bytes, need))) return s;
+  const MassPlan p = mass_plan(q.S, c.n_kv_heads, Hq / c.n_kv_heads, c.head_dim, max_q, max_kv, W);
+  sffn::MassArgs a;
+  a.q = (const char*)qp;
+  a.lse = lse;
+  a.mass = mass;
+  a.out = mass_out;
+  a.pos = pos;
+  a.plen = seq_len;
+  a.kv = kv_of(c);
+  a.sq = seqs_of(q);
+  a.hq = Hq;
+  a.G = Hq / c.n_kv_heads;
+  a.max_q = max_q;
+  a.window = std::min(window, sffn::MOST_LEN);
+  a.sinks = std::min(sinks, MAX_POS);
+  a.W = W;
+  a.ldq = q_stride;
+  a.c = scale * 1.4426950408889634f;
+  a.rs = p.rs;
+  a.wp = p.wp;
+  a.part = (float*)ws;
+  const hipError_t e = sffn_launch_mass(a, type, c.type, p.tiles, (hipStream_t)stream);
+  return e == hipSuccess ? SFFN_OK : sffn_err_hip(e, "attn_mass launch");
+}
+
+size_t sffn_kv_evict_workspace_size(int S, int n_kv_heads, int W, int keep) {
+  if (S < 1 || S > MAX_S || n_kv_heads < 1 || n_kv_heads > 65535 || keep < 1 || keep > W) return 0;
+  return align256((size_t)S * n_kv_heads * keep * sizeof(int));
+}
+
+int sffn_kv_evict(sffn_kv c, const int32_t* kv_len, const int32_t* seq_len, const int32_t* table, int S, int max_pages,
+                  int table_stride, const float* mass, const int32_t* pos, int W, int keep, int sinks, int recent, int32_t* src,
+                  float* mass_out, int32_t* pos_out, int32_t* kv_len_out, void* ws, size_t ws_bytes, void* stream) {
+  sffn_err_clear();
+  int s = check_cache(c, is16(c.type) ? c.type : SFFN_F16);
+  // (the table's checks ask for a cu array too, which an eviction has none of)
+  if (!s) s = check_seqs({kv_len, kv_len, table, S, 0, max_pages, table_stride}, c.page);
+  if (s) return s;
+  if (!seq_len || !mass || !pos || !src || !mass_out || !pos_out || !kv_len_out)
+    return fail(SFFN_ERR_NULL, "seq_len, mass, pos, src, mass_out, pos_out and kv_len_out are required");
+  if ((s = check_track(S, c.n_kv_heads, W))) return s;
+  if (keep < 1 || keep > W) return fail(SFFN_ERR_SHAPE, "keep=%d outside [1, W=%d]", keep, W);
+  if (sinks < 0 || recent < 0 || (int64_t)sinks + recent > keep)
+    return fail(SFFN_ERR_ARG, "sinks=%d, recent=%d: need both >= 0, their sum at most keep=%d", sinks, recent, keep);
+  if (!al(seq_len, 4) || !al(mass, 4) || !al(pos, 4) || !al(src, 4) || !al(mass_out, 4) || !al(pos_out, 4) || !al(kv_len_out, 4))
+    return fail(SFFN_ERR_ALIGN, "kv_evict: misaligned pointer");
+  const void* all[] = {mass, pos, src, mass_out, pos_out, kv_len, seq_len, kv_len_out, table};
+  for (int i = 0; i < 9; ++i)
+    for (int j = 0; j < i; ++j)
+      if (all[i] == all[j] && !(j == 0 && i == 3) && !(j == 1 && i == 4) && !(j == 5 && (i == 6 || i == 7)))
+        return fail(SFFN_ERR_ARG, "kv_evict: an output overlaps another tensor");
+  if ((s = check_workspace(ws, ws_bytes, sffn_kv_evict_workspace_size(S, c.n_kv_heads, W, keep)))) return s;
+  // fewer than 2^32 threads a launch, 8 slots a workgroup at least
+  if ((int64_t)((keep + 7) / 8) * S * c.n_kv_heads >= ((int64_t)1 << 24))
+    return fail(SFFN_ERR_SHAPE, "S=%d, n_kv_heads=%d, keep=%d: too many slots", S, c.n_kv_heads, keep);
+  const sffn::EvictArgs a{kv_of(c), kv_len, seq_len, table, mass, pos, mass_out, pos_out, kv_len_out, src, (int*)ws, S, max_pages,
+                          table_stride, W, keep, sinks, recent};
+  const hipError_t e = sffn_launch_evict(a, c.type, (hipStream_t)stream);
+  return e == hipSuccess ? SFFN_OK : sffn_err_hip(e, "kv_evict launch");
 }
 
 }  // extern "C"

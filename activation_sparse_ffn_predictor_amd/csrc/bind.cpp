@@ -1,4 +1,4 @@
-// CPython binding of the residual norm, the paged cache and the attention: reads sizes, strides and pointers out of
+// CPython binding of the residual norm, the paged cache, the attention and what joins them: reads sizes, strides and pointers out of
 // the tensors, checks what the C entry points cannot see (types, shapes, layouts, devices) and calls them. In C++ because
 // the same checks in Python take longer than the smallest of these calls run on the GPU. The entry points' addresses are
 // given at start-up, so this module serves whichever build of the library is loaded.
@@ -10,7 +10,9 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <stdexcept>
 #include <string>
 
@@ -22,6 +24,11 @@ decltype(&sffn_kv_write) p_write = nullptr;
 decltype(&sffn_kv_read) p_read = nullptr;
 decltype(&sffn_attn) p_attn = nullptr;
 decltype(&sffn_add_rmsnorm) p_norm = nullptr;
+decltype(&sffn_quant128) p_quant = nullptr;
+decltype(&sffn_mm_e4m3) p_mm = nullptr;
+decltype(&sffn_qk_norm_rope) p_rope = nullptr;
+decltype(&sffn_attn_mass) p_mass = nullptr;
+decltype(&sffn_kv_evict) p_evict = nullptr;
 
 struct Bad : std::runtime_error {
   using std::runtime_error::runtime_error;
@@ -241,11 +248,186 @@ PyObject* add_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// the entry points' addresses: (kv_write, kv_read, attn, add_rmsnorm)
+// contiguous `ty` of the given sizes
+template <class T>
+T* array(const at::Tensor& t, at::ScalarType ty, std::initializer_list<int64_t> sizes, const at::Tensor& ref, const char* where, const char* what) {
+  if (t.scalar_type() != ty || t.dim() != (int64_t)sizes.size() || !std::equal(sizes.begin(), sizes.end(), t.sizes().begin()) || !t.is_contiguous())
+    bad(where, what);
+  same_device(ref, t, where);
+  return (T*)t.data_ptr();
+}
+int64_t blocks(int64_t n) { return (n + 127) / 128; }
+
+// (x, y, scale, rows, stream)
+PyObject* quant128(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 5, [&] {
+    const char* where = "sffn_quant128";
+    const at::Tensor &x = tensor(a[0], where, "x"), &y = tensor(a[1], where, "y"), &sc = tensor(a[2], where, "scale");
+    if (x.dim() != 2) bad(where, "x is [rows, D]");
+    const int64_t T = x.size(0), D = x.size(1);
+    const int xt = type(x, F32 | F16 | BF16, where, "x"), rows = int_of(a[3]);
+    type(y, E4M3, where, "y");
+    if (rows != 1 && rows != 128) bad(where, "rows is 1 or 128");
+    const int64_t lx = mat(x, T, D, where, "x"), ly = mat(y, T, D, where, "y");
+    same_device(x, y, where);
+    float* s = array<float>(sc, at::kFloat, {(T + rows - 1) / rows, blocks(D)}, x, where,
+                            "scale is contiguous fp32, one for each block of rows x 128");
+    const int t32 = as_int(T, where), d32 = as_int(D, where);
+    return call(x, a[4], where, [&](void* st) { return p_quant(xt, x.data_ptr(), lx, t32, d32, rows, y.data_ptr(), ly, s, st); });
+  });
+}
+
+// (a, a_scale, b, b_scale, out, ws, stream)
+PyObject* mm_e4m3(PyObject*, PyObject* const* o, Py_ssize_t n) {
+  return guarded(n, 7, [&] {
+    const char* where = "sffn_mm_e4m3";
+    const at::Tensor &a = tensor(o[0], where, "a"), &sa = tensor(o[1], where, "a_scale"), &b = tensor(o[2], where, "b"),
+                     &sb = tensor(o[3], where, "b_scale"), &out = tensor(o[4], where, "out");
+    const at::Tensor* ws = maybe(o[5], where, "ws");
+    if (a.dim() != 2 || b.dim() != 2) bad(where, "a is [tokens, K], b is [N, K]");
+    const int64_t T = a.size(0), K = a.size(1), N = b.size(0);
+    type(a, E4M3, where, "a");
+    type(b, E4M3, where, "b");
+    const int ot = type(out, F32 | F16 | BF16, where, "out");
+    const int64_t la = mat(a, T, K, where, "a"), lb = mat(b, N, K, where, "b"), lo = mat(out, T, N, where, "out");
+    const float* fa = array<float>(sa, at::kFloat, {T, blocks(K)}, a, where, "a_scale is contiguous fp32 [tokens, blocks of K]");
+    const float* fb = array<float>(sb, at::kFloat, {blocks(N), blocks(K)}, a, where, "b_scale is contiguous fp32 [blocks of N, blocks of K]");
+    same_device(a, b, where);
+    same_device(a, out, where);
+    if (ws && !ws->is_contiguous()) bad(where, "the workspace must be contiguous");
+    if (ws) same_device(a, *ws, where);
+    const int t32 = as_int(T, where), n32 = as_int(N, where), k32 = as_int(K, where);
+    return call(a, o[6], where, [&](void* st) {
+      return p_mm(a.data_ptr(), la, fa, b.data_ptr(), lb, fb, t32, n32, k32, ot, out.data_ptr(), lo, ws ? ws->data_ptr() : nullptr,
+                  ws ? ws->nbytes() : 0, st);
+    });
+  });
+}
+
+// (q, k, w_q, w_k, eps, cu, seq_len, freq, q_out, k_out, interleaved, stream)
+PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 12, [&] {
+    const char* where = "sffn_qk_norm_rope";
+    const at::Tensor &q = tensor(a[0], where, "q"), &qo = tensor(a[8], where, "q_out"), &cu = tensor(a[5], where, "cu"),
+                     &len = tensor(a[6], where, "seq_len");
+    const at::Tensor *k = maybe(a[1], where, "k"), *ko = maybe(a[9], where, "k_out"), *wq = maybe(a[2], where, "w_q"),
+                     *wk = maybe(a[3], where, "w_k"), *freq = maybe(a[7], where, "freq");
+    const int ty = type(q, F16 | BF16, where, "q");
+    if (q.dim() != 3 || qo.scalar_type() != q.scalar_type() || qo.sizes() != q.sizes())
+      bad(where, "q and q_out are [tokens, heads, head size] of one type");
+    const int64_t T = q.size(0), Hq = q.size(1), d = q.size(2);
+    if (!k != !ko) bad(where, "k and k_out go together");
+    if (k && (k->dim() != 3 || k->size(0) != T || k->size(2) != d || k->scalar_type() != q.scalar_type() ||
+              ko->scalar_type() != q.scalar_type() || ko->sizes() != k->sizes()))
+      bad(where, "k and k_out are [tokens, K/V heads, head size] of q's type");
+    const int64_t Hk = k ? k->size(1) : 0;
+    const int64_t lq = rows(q, Hq, d, where, "q"), lqo = rows(qo, Hq, d, where, "q_out"), lk = k ? rows(*k, Hk, d, where, "k") : 0,
+                  lko = k ? rows(*ko, Hk, d, where, "k_out") : 0;
+    if (cu.dim() != 1 || len.dim() != 1 || cu.scalar_type() != at::kInt || len.scalar_type() != at::kInt || !cu.is_contiguous() ||
+        !len.is_contiguous() || cu.size(0) != len.size(0) + 1)
+      bad(where, "cu [S + 1] and seq_len [S] are contiguous int32");
+    for (const at::Tensor* w : {wq, wk})
+      if (w) array<float>(*w, at::kFloat, {d}, q, where, "w_q and w_k are contiguous fp32 [head size]");
+    if (freq && (freq->scalar_type() != at::kFloat || freq->dim() != 1 || !freq->is_contiguous())) bad(where, "freq is contiguous fp32 [rot / 2]");
+    for (const at::Tensor* t : {&qo, &cu, &len, k, ko, freq})
+      if (t) same_device(q, *t, where);
+    const bool norm = a[4] != Py_None;
+    if (!norm && (wq || wk)) bad(where, "w_q and w_k belong to a norm, which eps = None leaves out");
+    const double eps = norm ? number(a[4]) : 0.0;
+    const int inter = PyObject_IsTrue(a[10]), S = as_int(len.size(0), where), t32 = as_int(T, where), hq = as_int(Hq, where),
+              hk = as_int(Hk, where), d32 = as_int(d, where), rot = as_int(freq ? 2 * freq->size(0) : 0, where);
+    return call(q, a[11], where, [&](void* st) {
+      return p_rope(ty, (const int32_t*)cu.data_ptr(), (const int32_t*)len.data_ptr(), S, t32, q.data_ptr(), lq, hq,
+                    k ? k->data_ptr() : nullptr, lk, hk, d32, norm, wq ? (const float*)wq->data_ptr() : nullptr,
+                    wk ? (const float*)wk->data_ptr() : nullptr, eps, freq ? (const float*)freq->data_ptr() : nullptr, rot, inter,
+                    qo.data_ptr(), lqo, k ? ko->data_ptr() : nullptr, lko, st);
+    });
+  });
+}
+
+// [S, heads, W] of mass and pos, and the lengths of the sequences
+struct Track {
+  int64_t W;
+  const float* mass;
+  float* mass_out;
+};
+Track track(const at::Tensor& mass, const at::Tensor* mass_out, int64_t S, int64_t H, const at::Tensor& ref, const char* where) {
+  const int64_t W = mass.dim() == 3 ? mass.size(2) : 0;
+  const char* what = "mass is contiguous fp32 [S, K/V heads, slots]";
+  float* m = array<float>(mass, at::kFloat, {S, H, W}, ref, where, what);
+  return {W, m, mass_out ? array<float>(*mass_out, at::kFloat, {S, H, W}, ref, where, what) : m};
+}
+int32_t* lengths(PyObject* o, int32_t* other, int64_t S, const at::Tensor& ref, const char* where) {
+  return o == Py_None ? other : array<int32_t>(tensor(o, where, "lengths"), at::kInt, {S}, ref, where, "lengths are contiguous int32 [S]");
+}
+
+// (q, kv, cu, kv_len, table, max_q, max_kv, lse, mass, pos, ws, seq_len, mass_out, scale, window, sinks, stream)
+PyObject* attn_mass(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 17, [&] {
+    const char* where = "sffn_attn_mass";
+    const Cache c = cache(a[1], where);
+    const at::Tensor &q = tensor(a[0], where, "q"), &lse = tensor(a[7], where, "lse"), &mass = tensor(a[8], where, "mass"),
+                     &pos = tensor(a[9], where, "pos");
+    const at::Tensor *ws = maybe(a[10], where, "ws"), *mo = maybe(a[12], where, "mass_out");
+    const int ty = type(q, F16 | BF16, where, "q");
+    if (q.dim() != 3) bad(where, "q is [tokens, heads, head size]");
+    const int64_t T = q.size(0), Hq = q.size(1), H = c.c.n_kv_heads;
+    const int64_t lq = rows(q, Hq, c.c.head_dim, where, "q");
+    same_device(*c.K, q, where);
+    const float* l = array<float>(lse, at::kFloat, {T, Hq}, q, where, "lse is contiguous fp32 [tokens, heads]");
+    if (ws && !ws->is_contiguous()) bad(where, "the workspace must be contiguous");
+    if (ws) same_device(q, *ws, where);
+    const sffn_seqs sq = seqs(a[2], a[3], a[4], T, q, where);
+    const Track t = track(mass, mo, sq.S, H, q, where);
+    int32_t* p = array<int32_t>(pos, at::kInt, {sq.S, H, t.W}, q, where, "pos is contiguous int32 [S, K/V heads, slots]");
+    const int32_t* plen = lengths(a[11], (int32_t*)sq.kv_len, sq.S, q, where);
+    const int max_q = int_of(a[5]), max_kv = int_of(a[6]), window = int_of(a[14]), sinks = int_of(a[15]);
+    const float scale = (float)(a[13] == Py_None ? std::pow((double)c.c.head_dim, -0.5) : number(a[13]));
+    const int hq = as_int(Hq, where), W = as_int(t.W, where);
+    return call(q, a[16], where, [&](void* st) {
+      return p_mass(c.c, sq, plen, ty, q.data_ptr(), lq, hq, max_q, max_kv, scale, window, sinks, l, t.mass, t.mass_out, p, W,
+                    ws ? ws->data_ptr() : nullptr, ws ? ws->nbytes() : 0, st);
+    });
+  });
+}
+
+// (kv, kv_len, table, mass, pos, keep, src, ws, seq_len, sinks, recent, kv_len_out, mass_out, pos_out, stream)
+PyObject* kv_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 15, [&] {
+    const char* where = "sffn_kv_evict";
+    const Cache c = cache(a[0], where);
+    const at::Tensor &len = tensor(a[1], where, "kv_len"), &tab = tensor(a[2], where, "table"), &mass = tensor(a[3], where, "mass"),
+                     &pos = tensor(a[4], where, "pos"), &src = tensor(a[6], where, "src");
+    const at::Tensor *ws = maybe(a[7], where, "ws"), *mo = maybe(a[12], where, "mass_out"), *po = maybe(a[13], where, "pos_out");
+    const int64_t S = len.dim() == 1 ? len.size(0) : 0, H = c.c.n_kv_heads;
+    int32_t* l = lengths(a[1], nullptr, S, *c.K, where);
+    const int64_t cols = tab.dim() == 2 ? tab.size(1) : 0;
+    if (tab.scalar_type() != at::kInt || tab.dim() != 2 || tab.size(0) != S || (cols > 1 && tab.stride(1) != 1))
+      bad(where, "table is int32 [S, max_pages] with dense rows");
+    same_device(*c.K, tab, where);
+    const Track t = track(mass, mo, S, H, *c.K, where);
+    const char* what = "pos is contiguous int32 [S, K/V heads, slots]";
+    int32_t* p = array<int32_t>(pos, at::kInt, {S, H, t.W}, *c.K, where, what);
+    int32_t* pout = po ? array<int32_t>(*po, at::kInt, {S, H, t.W}, *c.K, where, what) : p;
+    const int keep = int_of(a[5]), sinks = int_of(a[9]), recent = int_of(a[10]);
+    int32_t* from = array<int32_t>(src, at::kInt, {S, H, keep}, *c.K, where, "src is contiguous int32 [S, K/V heads, keep]");
+    const int32_t* plen = lengths(a[8], l, S, *c.K, where);
+    int32_t* lout = lengths(a[11], l, S, *c.K, where);
+    if (ws && !ws->is_contiguous()) bad(where, "the workspace must be contiguous");
+    if (ws) same_device(*c.K, *ws, where);
+    const int s32 = as_int(S, where), c32 = as_int(cols, where), ldt = as_int(S > 1 ? tab.stride(0) : cols, where), W = as_int(t.W, where);
+    return call(*c.K, a[14], where, [&](void* st) {
+      return p_evict(c.c, l, plen, (const int32_t*)tab.data_ptr(), s32, c32, ldt, t.mass, p, W, keep, sinks, recent, from, t.mass_out,
+                     pout, lout, ws ? ws->data_ptr() : nullptr, ws ? ws->nbytes() : 0, st);
+    });
+  });
+}
+
+// the entry points' addresses: (kv_write, kv_read, attn, add_rmsnorm, quant128, mm_e4m3, qk_norm_rope, attn_mass, kv_evict)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 4, [&]() -> PyObject* {
-    void* p[4];
-    for (int i = 0; i < 4; ++i) {
+  return guarded(n, 9, [&]() -> PyObject* {
+    void* p[9];
+    for (int i = 0; i < 9; ++i) {
       p[i] = PyLong_AsVoidPtr(a[i]);
       if (!p[i]) throw Bad("bind: no address");
     }
@@ -253,13 +435,19 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p_read = (decltype(p_read))p[1];
     p_attn = (decltype(p_attn))p[2];
     p_norm = (decltype(p_norm))p[3];
+    p_quant = (decltype(p_quant))p[4];
+    p_mm = (decltype(p_mm))p[5];
+    p_rope = (decltype(p_rope))p[6];
+    p_mass = (decltype(p_mass))p[7];
+    p_evict = (decltype(p_evict))p[8];
     Py_RETURN_NONE;
   });
 }
 
 #define M(name, fn) {name, (PyCFunction)(void (*)(void))(fn), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {M("bind", bind), M("kv_write", move<true>), M("kv_read", move<false>), M("attn", attn),
-                         M("add_rmsnorm", add_rmsnorm), {nullptr, nullptr, 0, nullptr}};
+                         M("add_rmsnorm", add_rmsnorm), M("quant128", quant128), M("mm_e4m3", mm_e4m3), M("qk_norm_rope", qk_norm_rope),
+                         M("attn_mass", attn_mass), M("kv_evict", kv_evict), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,31 @@
+// Arguments and sizes of the attention-mass kernels (mass.hip), which the host side decides on.
+#pragma once
+#include "attn.h"
+
+namespace sffn {
+
+// mass, out, pos [S, hkv, W]; rows of one K/V head: r = i * G + g for new token i and query head hk * G + g.
+struct MassArgs {
+  const char* q;
+  const float* lse;         // [T, hq]
+  const float* mass;
+  float* out;               // may be mass
+  int* pos;
+  const int* plen;          // tokens of the sequences [S]
+  Kv kv;
+  Seqs sq;
+  int hq, G, max_q, window, sinks, W;
+  long ldq;
+  float c;                  // softmax scale * log2(e)
+  int rs, wp;               // shares of the rows (tile kernel); keys whose sums are shared out
+  float* part;              // [S, hkv, rs, wp], used when rs > 1
+};
+
+// the few-row kernel keeps the queries in registers
+__host__ __device__ constexpr bool mass_few(long rows, int d) { return rows <= (d <= 128 ? 64 : 32); }
+// keys of a workgroup of the tile kernel
+__host__ __device__ constexpr int mass_tile(int d) { return d <= 128 ? 256 : 128; }
+
+}  // namespace sffn
+
+hipError_t sffn_launch_mass(const sffn::MassArgs& a, int qt, int kvt, int tiles, hipStream_t st);

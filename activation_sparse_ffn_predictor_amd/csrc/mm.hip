@@ -1,0 +1,227 @@
+// out = A B^T for e4m3 matrices with one fp32 scale for each 128 columns of a row of A and each 128 x 128 block of B:
+//   out[t, n] = sum over blocks kb of sa[t, kb] sb[n / 128, kb] * (sum over k in kb of A[t, k] B[n, k])
+// Rows of B are the matrix instructions' rows, tokens their columns: a lane's results belong to one token, so its factor is one
+// register, and sb is the same for the whole tile. Blocks are scaled and added in fp32.
+//
+// A block's own sum: the 8-bit instruction (16x16x128, a block at once) brings each 8 products to the largest one's exponent and
+// drops what lies 2^-13 under it; the fp16 instruction on widened codes (exact) adds in fp32, at half the rate. Few tokens wait
+// for memory, so they take the fp16 one, as do fp32 results; 16-bit results of many tokens take the 8-bit one: dropped bits are
+// 1.4e-4 of a sum of independent terms, fp16's own rounding 2.1e-4, bf16's 1.7e-3.
+#include "mm.h"
+
+using namespace sffn;
+
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+// A lane's 32 codes of a block (two 16-byte chunks), as they are or as fp16 operands of four products
+template <bool EXACT>
+struct Codes {
+  uint4 v[EXACT ? 4 : 2];
+  __device__ __forceinline__ void set(const uint4& a, const uint4& b) {
+    if constexpr (EXACT) {
+      const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint2 p = codes4<true>(u[2 * i]), q = codes4<true>(u[2 * i + 1]);
+        v[i] = make_uint4(p.x, p.y, q.x, q.y);
+      }
+    } else {
+      v[0] = a;
+      v[1] = b;
+    }
+  }
+};
+// the block's sums for 16 rows and 16 tokens
+__device__ __forceinline__ f32x4 block_sum(const Codes<false>& a, const Codes<false>& b) {
+  const i32x8 x = {(int)a.v[0].x, (int)a.v[0].y, (int)a.v[0].z, (int)a.v[0].w, (int)a.v[1].x, (int)a.v[1].y, (int)a.v[1].z, (int)a.v[1].w};
+  const i32x8 y = {(int)b.v[0].x, (int)b.v[0].y, (int)b.v[0].z, (int)b.v[0].w, (int)b.v[1].x, (int)b.v[1].y, (int)b.v[1].z, (int)b.v[1].w};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 block_sum(const Codes<true>& a, const Codes<true>& b) {
+  f32x4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p = mfma16<false>(a.v[i], b.v[i], p);
+  return p;
+}
+template <int OT>
+__device__ __forceinline__ void store4(void* p, long i, f32x4 v) {
+  if constexpr (OT == T_F32) *reinterpret_cast<f32x4*>((float*)p + i) = v;
+  else *reinterpret_cast<uint2*>((char*)p + 2 * i) = make_uint2(pack2<OT == T_BF16>(v[0], v[1]), pack2<OT == T_BF16>(v[2], v[3]));
+}
+// rows r0 .. r0 + n - 1 of a matrix of codes; what lies past the last row's end reads as zeros
+__device__ __forceinline__ Buf rows_of(const char* p, long ld, long r0, long rows, int n, int K) {
+  const long have = rows - r0 < n ? rows - r0 : n;
+  return Buf(p + r0 * ld, have > 0 ? (uint32_t)((have - 1) * ld + K) : 0u);
+}
+
+// ------------------------------------------------------------------------------------------------ few tokens
+// 16 rows of B a workgroup, whose 8 waves take blocks of k in turn and are added up in LDS. Bound by B's bytes.
+constexpr int FEW_W = 8;
+template <int OT, int TB>
+__global__ __launch_bounds__(FEW_W * 64) void k_mm_few(MmArgs a) {
+  __shared__ f32x4 part[FEW_W][TB][64];
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, g4 = l >> 4, ql = l & 15;
+  const int n0 = blockIdx.x * 16, KB = (a.K + 127) >> 7;
+  const Buf bb = rows_of(a.b, a.ldb, n0, a.N, 16, a.K), ba = rows_of(a.a, a.lda, 0, a.T, TB * 16, a.K);
+  const float* sb = a.sb + (long)(n0 >> 7) * KB;
+  f32x4 acc[TB];
+#pragma unroll
+  for (int t = 0; t < TB; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  constexpr int U = 4;                             // blocks in flight
+  for (int k0 = w; k0 < KB; k0 += FEW_W * U) {
+    uint4 x[U][2], y[U][TB][2];
+    float f[U][TB];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = k0 + u * FEW_W;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = kb * 128 + (c * 4 + g4) * 16;
+        const bool in = col < a.K;
+        x[u][c] = bb.ld16(boff(in, ql * (uint32_t)a.ldb + col));
+#pragma unroll
+        for (int t = 0; t < TB; ++t) y[u][t][c] = ba.ld16(boff(in, (t * 16 + ql) * (uint32_t)a.lda + col));
+      }
+#pragma unroll
+      for (int t = 0; t < TB; ++t) f[u][t] = kb < KB && t * 16 + ql < a.T ? a.sa[(long)(t * 16 + ql) * KB + kb] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = k0 + u * FEW_W;
+      if (kb >= KB) break;
+      const float s = sb[kb];
+      Codes<true> c;
+      c.set(x[u][0], x[u][1]);
+#pragma unroll
+      for (int t = 0; t < TB; ++t) {
+        Codes<true> z;
+        z.set(y[u][t][0], y[u][t][1]);
+        const f32x4 p = block_sum(c, z);
+        const float g = f[u][t] * s;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(p[i], g, acc[t][i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TB; ++t) part[w][t][l] = acc[t];
+  __syncthreads();
+  if (threadIdx.x < TB * 64) {
+    const int t = threadIdx.x >> 6, tok = t * 16 + ql, n = n0 + 4 * g4;
+    f32x4 v = part[0][t][l];
+#pragma unroll
+    for (int i = 1; i < FEW_W; ++i) v += part[i][t][l];
+    if (tok < a.T && n < a.N) store4<OT>(a.out, tok * a.ldo + n, v);
+  }
+}
+
+// ------------------------------------------------------------------------------------------------ many tokens
+// BN rows of B x BT tokens a workgroup of 2 x 2 waves; both operands' next block of k is on its way to LDS (direct loads)
+// while this one is multiplied. A row's 16-byte chunk c lies in slot c ^ ((row >> 1) & 7): the 16 rows that a fragment's
+// read touches at one chunk spread over all banks.
+template <int OT, int BN, int BT>
+__global__ __launch_bounds__(256) void k_mm_tile(MmArgs a) {
+  constexpr int MI = BN / 32, NI = BT / 32;        // 16-blocks of a wave
+  __shared__ __align__(16) char lb[2][BN * 128], la[2][BT * 128];
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, g4 = l >> 4, ql = l & 15;
+  const int wn = (w & 1) * (BN / 2), wt = (w >> 1) * (BT / 2);
+  const int tn = (a.N + BN - 1) / BN, n0 = blockIdx.x % tn * BN, t0 = blockIdx.x / tn * BT, KB = (a.K + 127) >> 7;
+  const Buf bb = rows_of(a.b, a.ldb, n0, a.N, BN, a.K), ba = rows_of(a.a, a.lda, t0, a.T, BT, a.K);
+  const int slot = l & 7, rr = l >> 3;
+  auto load = [&](int kb, int buf) {
+#pragma unroll
+    for (int i = 0; i < BN / 32; ++i) {
+      const int row = (i * 4 + w) * 8 + rr, col = kb * 128 + ((slot ^ ((row >> 1) & 7)) << 4);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(bb.r, (__attribute__((address_space(3))) void*)(lb[buf] + (i * 4 + w) * 1024), 16,
+                                               (int)boff(col < a.K, row * (uint32_t)a.ldb + col), 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < BT / 32; ++i) {
+      const int row = (i * 4 + w) * 8 + rr, col = kb * 128 + ((slot ^ ((row >> 1) & 7)) << 4);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ba.r, (__attribute__((address_space(3))) void*)(la[buf] + (i * 4 + w) * 1024), 16,
+                                               (int)boff(col < a.K, row * (uint32_t)a.lda + col), 0, 0, 0);
+    }
+  };
+  auto arrive = [&] {                              // every wave's direct loads are there
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    __syncthreads();
+  };
+  const float* sa[NI];
+  bool have[NI];
+#pragma unroll
+  for (int j = 0; j < NI; ++j) {
+    const int t = t0 + wt + j * 16 + ql;
+    have[j] = t < a.T;
+    sa[j] = a.sa + (long)(have[j] ? t : 0) * KB;
+  }
+  const float* sb = a.sb + (long)((n0 + wn) >> 7) * KB;   // (a wave's rows lie in one block of 128)
+  if (n0 + wn >= a.N) sb = a.sb;
+  f32x4 acc[MI][NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  load(0, 0);
+  arrive();
+  for (int kb = 0; kb < KB; ++kb) {
+    const int buf = kb & 1;
+    if (kb + 1 < KB) load(kb + 1, buf ^ 1);
+    const float s = sb[kb];
+    float g[NI];
+#pragma unroll
+    for (int j = 0; j < NI; ++j) g[j] = have[j] ? sa[j][kb] * s : 0.f;
+    auto frag = [&](const char* tile, int row) {     // chunks g4 and 4 + g4 of a row
+      Codes<OT == T_F32> c;
+      const int z = (row >> 1) & 7;
+      c.set(*reinterpret_cast<const uint4*>(tile + row * 128 + ((g4 ^ z) << 4)),
+            *reinterpret_cast<const uint4*>(tile + row * 128 + (((4 + g4) ^ z) << 4)));
+      return c;
+    };
+    Codes<OT == T_F32> y[NI];
+#pragma unroll
+    for (int j = 0; j < NI; ++j) y[j] = frag(la[buf], wt + j * 16 + ql);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const Codes<OT == T_F32> x = frag(lb[buf], wn + i * 16 + ql);
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        const f32x4 p = block_sum(x, y[j]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], g[j], acc[i][j][e]);
+      }
+    }
+    arrive();
+  }
+#pragma unroll
+  for (int j = 0; j < NI; ++j) {
+    const int t = t0 + wt + j * 16 + ql;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int n = n0 + wn + i * 16 + 4 * g4;
+      if (t < a.T && n < a.N) store4<OT>(a.out, t * a.ldo + n, acc[i][j]);
+    }
+  }
+}
+
+template <int OT>
+hipError_t go(const MmArgs& a, hipStream_t st) {
+  const dim3 few((a.N + 15) / 16);
+  if (a.T <= 16) hipLaunchKernelGGL((k_mm_few<OT, 1>), few, dim3(FEW_W * 64), 0, st, a);
+  else if (a.T <= 32) hipLaunchKernelGGL((k_mm_few<OT, 2>), few, dim3(FEW_W * 64), 0, st, a);
+  else if (a.T <= 64) hipLaunchKernelGGL((k_mm_few<OT, 4>), few, dim3(FEW_W * 64), 0, st, a);
+  else {
+    const unsigned tiles = (unsigned)((a.N + 127) / 128) * ((a.T + 127) / 128);
+    hipLaunchKernelGGL((k_mm_tile<OT, 128, 128>), dim3(tiles), dim3(256), 0, st, a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t sffn_mm_workspace(int T, int N, int K) { (void)T, (void)N, (void)K; return 0; }
+
+hipError_t sffn_launch_mm(const MmArgs& a, int ot, hipStream_t st) {
+  return ot == T_F32 ? go<T_F32>(a, st) : ot == T_F16 ? go<T_F16>(a, st) : go<T_BF16>(a, st);
+}

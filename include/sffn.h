@@ -319,6 +319,83 @@ int sffn_add_rmsnorm(int x_type, const void* x, int64_t x_stride, int res_type, 
                      const float* w, double eps, int T, int D, int y_type, void* y, int64_t y_stride, float* y_scale,
                      void* res_out, int64_t res_out_stride, void* stream);
 
+/* ---------------------------------------------------------------------------------------------------------------
+ * What joins the attention half: 8-bit products for its projections, norms and rotation of queries and keys, and a cache that
+ * keeps the tokens that attention goes to. Errors, streams and checks as above.
+ *
+ * Blocks of 128 columns as e4m3 codes: rows = 1 gives every row of x [T, D] (F32, F16 or BF16) one fp32 scale for each 128 of
+ * its columns (activations), rows = 128 one for each 128 x 128 block (weights); the last blocks may be smaller.
+ *   scale = fp32(max|x| / 448);  code = x / scale rounded to nearest, ties to even (of the exact quotient)
+ * A scale below 2^-60 becomes 0 with codes 0; a block that holds an infinity or NaN gets the scale NaN and codes 0.
+ * y [T, D] codes, scale [ceil(T / rows), ceil(D / 128)]. Row strides in elements, multiples of 8, at least D. 8 <= D <= 65536,
+ * D % 8 == 0; 0 <= T <= 2^24. y overlaps no input. One kernel. */
+int sffn_quant128(int x_type, const void* x, int64_t x_stride, int T, int D, int rows, void* y, int64_t y_stride,
+                  float* scale, void* stream);
+
+/* Product of two such matrices:
+ *   out[t, n] = sum_kb a_scale[t, kb] b_scale[n / 128, kb] * sum_{k in kb} a[t, k] b[n, k]
+ * a [T, K] codes with a_scale [T, ceil(K / 128)], b [N, K] codes with b_scale [ceil(N / 128), ceil(K / 128)] (scales contiguous),
+ * out [T, N] of F32, F16 or BF16, rounded once. The sums over a block are fp32 (codes widened exactly to fp16 products) up to 64
+ * tokens and for fp32 results; 16-bit results of more tokens take the 8-bit matrix instruction, which drops of each 8 products what
+ * lies 2^-13 under the largest one's leading bit. Blocks are scaled and added in fp32, so a block's sum times its scales has to
+ * stay in fp32's range. e4m3's NaN codes and NaN scales make NaN of the results
+ * that they enter. K % 16 == 0, 16 <= K <= 65536; N % 8 == 0, 8 <= N <= 2^22; 0 <= T <= 2^24; strides of a and b multiples of
+ * 16, at least K, at most 2^22; of out a multiple of 8, at least N. out overlaps no input. The workspace needs
+ * sffn_mm_workspace_size bytes of the same sizes (0: none, ws may be NULL), holds nothing between calls, and calls that overlap
+ * in time need separate ones. The same call gives the same bits. ceil(T / 128) * ceil(N / 128) < 2^24. */
+size_t sffn_mm_workspace_size(int T, int N, int K);
+int sffn_mm_e4m3(const void* a, int64_t a_stride, const float* a_scale, const void* b, int64_t b_stride, const float* b_scale,
+                 int T, int N, int K, int out_type, void* out, int64_t out_stride, void* ws, size_t ws_bytes, void* stream);
+
+/* Root-mean-square norm of every head of the queries and keys, then the rotation by their positions, in one pass:
+ *   h = x / sqrt(mean(x^2) + eps) * w           (norm != 0; over a head's elements; w_q, w_k [head_dim] fp32 or NULL (1). Else h = x.)
+ *   y_a = h_a cos f - h_b sin f,  y_b = h_b cos f + h_a sin f,  f = position * freq[i]
+ * for the pairs i < rot / 2 of a head's first rot elements: (a, b) = (i, i + rot / 2), or (2 i, 2 i + 1) if `interleaved`; the
+ * elements behind stay h. freq [rot / 2] fp32 (finite; not read if rot = 0). The i-th of a sequence's n new tokens (cu as in
+ * sffn_seqs) is at position seq_len[s] - n + i: seq_len is kv_len, or what the sequence counts where tokens were evicted. Angles
+ * are reduced in 64 bits, the rest is fp32, rounded once.
+ * q, q_out [T, Hq, head_dim] and k, k_out [T, n_kv_heads, head_dim] of a 16-bit `type` (k and k_out NULL: queries alone); strides as
+ * elsewhere, between tokens, multiples of 8. An output may be its input, with its stride, and overlaps nothing else. Rows at and
+ * behind cu[S] are not written. head_dim % 8 == 0, 8 <= head_dim <= 256; rot % 8 == 0, 0 <= rot <= head_dim; Hq, n_kv_heads <=
+ * 65535; S, T as elsewhere. One kernel (one for each 2^22 tokens). */
+int sffn_qk_norm_rope(int type, const int32_t* cu, const int32_t* seq_len, int S, int T, const void* q, int64_t q_stride, int Hq,
+                      const void* k, int64_t k_stride, int n_kv_heads, int head_dim, int norm, const float* w_q, const float* w_k,
+                      double eps, const float* freq, int rot, int interleaved, void* q_out, int64_t q_out_stride, void* k_out,
+                      int64_t k_out_stride, void* stream);
+
+/* Attention weight of the cached tokens, accumulated: after sffn_attn, with its q, cache, sequences, scale, window and sinks and
+ * the lse that it wrote,
+ *   mass_out[s, h, j] = (j is a new token's slot ? 0 : mass[s, h, j]) + sum over rows that see j of exp(scale * q . K[j, h] - lse)
+ * over the new tokens and the query heads that share K/V head h, for the slots j < min(kv_len[s], what the table row holds, W) of
+ * the sequences that have new tokens; everything else stays as it was. New tokens' slots get pos[s, h, j] = the token's position
+ * in the sequence, as in sffn_qk_norm_rope. mass, mass_out (which may be mass), pos [S, n_kv_heads, W], contiguous. Rows whose lse
+ * is -infinity, and rows past max_q tokens of a sequence, add nothing. What lies in places that a token does not see has no
+ * effect. Sums are fp32 in a fixed order: the same call gives the same bits. bf16 queries over an 8-bit cache enter the product
+ * as in sffn_attn, or as they are. max_kv is a hint as there, of the workspace's size (sffn_attn_mass_workspace_size bytes of the same
+ * sizes; 0: none needed). S * n_kv_heads < 2^22, S * n_kv_heads * W < 2^31. One kernel, or two where a long prompt's rows are shared out. */
+size_t sffn_attn_mass_workspace_size(int S, int Hq, int n_kv_heads, int head_dim, int max_q, int max_kv, int W);
+int sffn_attn_mass(sffn_kv cache, sffn_seqs seqs, const int32_t* seq_len, int type, const void* q, int64_t q_stride, int Hq,
+                   int max_q, int max_kv, float scale, int window, int sinks, const float* lse, const float* mass, float* mass_out,
+                   int32_t* pos, int W, void* ws, size_t ws_bytes, void* stream);
+
+/* Eviction: every sequence that holds more than `keep` tokens (of the first W, in its table row) is cut down to `keep` of them,
+ * for each K/V head its own: those whose position is below `sinks` or at least seq_len[s] - recent, then those with the largest
+ * mass, ties to the lowest slot (a mass that is negative or NaN counts as 0; slots in pages outside the cache go first). Kept
+ * tokens in slots at and behind `keep` move, in order, into the given-up slots below it, in order; the others stay where they are.
+ * src [S, n_kv_heads, keep] int32: the slot that each of the first `keep` slots' tokens stood in (its own where nothing moved).
+ * Moved are K, V, their scales, mass and pos: mass_out and pos_out [S, n_kv_heads, W] get the first min(kv_len, keep) slots (they
+ * may be mass and pos themselves), kv_len_out[s] = keep where tokens were evicted, else kv_len[s] (it may be kv_len, but not
+ * where seq_len is kv_len too: the sequence would forget how long it is). Pages wholly
+ * behind the new length are free. Slots are no longer in the order of positions afterwards: attention sees every slot below a
+ * new token's whatever its position, but a sliding window would count slots. The pages of the sequences must be their own (not
+ * shared between rows of the table). A move into a page outside the cache loses the token. sinks, recent >= 0, sinks + recent <= keep;
+ * 1 <= keep <= W; S, n_kv_heads and W as in sffn_attn_mass. cache: its 16-bit type or 8-bit as elsewhere. Limits of cache and table as in sffn_kv_write.
+ * The workspace needs sffn_kv_evict_workspace_size bytes. Two kernels. */
+size_t sffn_kv_evict_workspace_size(int S, int n_kv_heads, int W, int keep);
+int sffn_kv_evict(sffn_kv cache, const int32_t* kv_len, const int32_t* seq_len, const int32_t* table, int S, int max_pages,
+                  int table_stride, const float* mass, const int32_t* pos, int W, int keep, int sinks, int recent, int32_t* src,
+                  float* mass_out, int32_t* pos_out, int32_t* kv_len_out, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
