@@ -117,61 +117,73 @@ __global__ __launch_bounds__(FEW_W * 64) void k_mm_few(MmArgs a) {
 }
 
 // ------------------------------------------------------------------------------------------------ many tokens
-// BN rows of B x BT tokens a workgroup of 2 x 2 waves; both operands' next block of k is on its way to LDS (direct loads)
+// BN rows of B x BT tokens a workgroup of WN x WT waves; both operands' next block of k is on its way to LDS (direct loads)
 // while this one is multiplied. A row's 16-byte chunk c lies in slot c ^ ((row >> 1) & 7): the 16 rows that a fragment's
-// read touches at one chunk spread over all banks.
-template <int OT, int BN, int BT>
-__global__ __launch_bounds__(256) void k_mm_tile(MmArgs a) {
-  constexpr int MI = BN / 32, NI = BT / 32;        // 16-blocks of a wave
-  __shared__ __align__(16) char lb[2][BN * 128], la[2][BT * 128];
+// read touches at one chunk spread over all banks. Workgroups of one XCD take neighbouring tiles, 4 along the tokens, so that
+// what they load at one time is shared in its L2.
+template <int OT, int BN, int BT, int WN, int WT>
+__global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a) {
+  constexpr int W = WN * WT, MI = BN / WN / 16, NI = BT / WT / 16;        // waves; 16-blocks of a wave
+  // (the two turns' LDS are separate objects: the compiler then sees that loads on their way into one do not concern reads of
+  // the other)
+  __shared__ __align__(16) char b0[BN * 128], b1[BN * 128], a0[BT * 128], a1[BT * 128];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, g4 = l >> 4, ql = l & 15;
-  const int wn = (w & 1) * (BN / 2), wt = (w >> 1) * (BT / 2);
-  const int tn = (a.N + BN - 1) / BN, n0 = blockIdx.x % tn * BN, t0 = blockIdx.x / tn * BT, KB = (a.K + 127) >> 7;
+  const int wn = (w % WN) * (BN / WN), wt = (w / WN) * (BT / WT);
+  static_assert(W % 2 == 0, "a lane's swizzle is the same in every turn of its rows");
+  const int tn = (a.N + BN - 1) / BN, tt = (a.T + BT - 1) / BT, id = xcd_slice(blockIdx.x, gridDim.x);
+  if (id >= tn * tt) return;
+  const int first = id / (4 * tn) * 4, wide = min(4, tt - first), in = id % (4 * tn);
+  const int n0 = in / wide * BN, t0 = (first + in % wide) * BT, KB = (a.K + 127) >> 7;
   const Buf bb = rows_of(a.b, a.ldb, n0, a.N, BN, a.K), ba = rows_of(a.a, a.lda, t0, a.T, BT, a.K);
-  const int slot = l & 7, rr = l >> 3;
-  auto load = [&](int kb, int buf) {
+  // direct loads: a wave's 8 rows at a time, W waves beside each other; a lane's row keeps its swizzle from turn to turn, so one
+  // offset serves all, with the rows and blocks passed as the wave's own. Past the last row, and past K, zeros are read.
+  const int rr = w * 8 + (l >> 3), ch = ((l & 7) ^ ((rr >> 1) & 7)) << 4;
+  const uint32_t vb = rr * (uint32_t)a.ldb + ch, va = rr * (uint32_t)a.lda + ch;
+  const bool tail = (KB - 1) * 128 + ch < a.K;     // does the lane's chunk of the last block exist?
+  auto load = [&](int kb, char* lb, char* la) {
+    const bool in = (kb < KB - 1) | ((kb == KB - 1) & tail);
+    const uint32_t ob = boff(in, vb), oa = boff(in, va);
 #pragma unroll
-    for (int i = 0; i < BN / 32; ++i) {
-      const int row = (i * 4 + w) * 8 + rr, col = kb * 128 + ((slot ^ ((row >> 1) & 7)) << 4);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(bb.r, (__attribute__((address_space(3))) void*)(lb[buf] + (i * 4 + w) * 1024), 16,
-                                               (int)boff(col < a.K, row * (uint32_t)a.ldb + col), 0, 0, 0);
-    }
+    for (int i = 0; i < BN / 8 / W; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(bb.r, (__attribute__((address_space(3))) void*)(lb + (i * W + w) * 1024), 16, (int)ob,
+                                               (int)(i * W * 8 * (uint32_t)a.ldb + kb * 128), 0, 0);
 #pragma unroll
-    for (int i = 0; i < BT / 32; ++i) {
-      const int row = (i * 4 + w) * 8 + rr, col = kb * 128 + ((slot ^ ((row >> 1) & 7)) << 4);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ba.r, (__attribute__((address_space(3))) void*)(la[buf] + (i * 4 + w) * 1024), 16,
-                                               (int)boff(col < a.K, row * (uint32_t)a.lda + col), 0, 0, 0);
-    }
+    for (int i = 0; i < BT / 8 / W; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ba.r, (__attribute__((address_space(3))) void*)(la + (i * W + w) * 1024), 16, (int)oa,
+                                               (int)(i * W * 8 * (uint32_t)a.lda + kb * 128), 0, 0);
   };
   auto arrive = [&] {                              // every wave's direct loads are there
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0x0F70);
     __syncthreads();
   };
-  const float* sa[NI];
-  bool have[NI];
-#pragma unroll
-  for (int j = 0; j < NI; ++j) {
-    const int t = t0 + wt + j * 16 + ql;
-    have[j] = t < a.T;
-    sa[j] = a.sa + (long)(have[j] ? t : 0) * KB;
-  }
-  const float* sb = a.sb + (long)((n0 + wn) >> 7) * KB;   // (a wave's rows lie in one block of 128)
-  if (n0 + wn >= a.N) sb = a.sb;
+  // factors of a lane's tokens (0 behind the last one), and of the wave's rows, which lie in one block of 128
+  const Buf bs(a.sa + (long)t0 * KB, (uint32_t)min(a.T - t0, BT) * KB * 4),
+      bw(a.sb + (long)((n0 + wn) >> 7) * KB, n0 + wn < a.N ? (uint32_t)KB * 4 : 0u);
+  const uint32_t vs = (wt + ql) * (uint32_t)KB * 4;
+  auto factor = [&](int j, int kb) {
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bs.r, (int)vs, (int)((j * 16 * KB + kb) * 4), 0));
+  };
+  auto weight = [&](int kb) { return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bw.r, 0, kb * 4, 0)); };
   f32x4 acc[MI][NI];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  load(0, 0);
-  arrive();
-  for (int kb = 0; kb < KB; ++kb) {
-    const int buf = kb & 1;
-    if (kb + 1 < KB) load(kb + 1, buf ^ 1);
-    const float s = sb[kb];
-    float g[NI];
+  load(0, b0, a0);
+  float g[NI], s = weight(0);
 #pragma unroll
-    for (int j = 0; j < NI; ++j) g[j] = have[j] ? sa[j][kb] * s : 0.f;
+  for (int j = 0; j < NI; ++j) g[j] = factor(j, 0);
+  arrive();
+  // One block: its products' results are scaled and added while the next row's products run, whose operands are read meanwhile.
+  auto block = [&](int kb, const char* lb, const char* la, char* nb, char* na) {
+#pragma unroll
+    for (int j = 0; j < NI; ++j) g[j] *= s;
+    float gn[NI];                                    // (past the last block: another one's, or 0; not used)
+    const float sn = weight(kb + 1);
+#pragma unroll
+    for (int j = 0; j < NI; ++j) gn[j] = factor(j, kb + 1);
+    load(kb + 1, nb, na);
     auto frag = [&](const char* tile, int row) {     // chunks g4 and 4 + g4 of a row
       Codes<OT == T_F32> c;
       const int z = (row >> 1) & 7;
@@ -179,21 +191,39 @@ __global__ __launch_bounds__(256) void k_mm_tile(MmArgs a) {
             *reinterpret_cast<const uint4*>(tile + row * 128 + (((4 + g4) ^ z) << 4)));
       return c;
     };
-    Codes<OT == T_F32> y[NI];
+    Codes<OT == T_F32> y[NI], x = frag(lb, wn + ql);
 #pragma unroll
-    for (int j = 0; j < NI; ++j) y[j] = frag(la[buf], wt + j * 16 + ql);
+    for (int j = 0; j < NI; ++j) y[j] = frag(la, wt + j * 16 + ql);
+    f32x4 p[NI];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const Codes<OT == T_F32> x = frag(lb[buf], wn + i * 16 + ql);
+    for (int i = 0; i <= MI; ++i) {
+      Codes<OT == T_F32> xn;
+      if (i + 1 < MI) xn = frag(lb, wn + (i + 1) * 16 + ql);
 #pragma unroll
       for (int j = 0; j < NI; ++j) {
-        const f32x4 p = block_sum(x, y[j]);
+        f32x4 q;
+        if (i < MI) q = block_sum(x, y[j]);
+        if (i > 0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], g[j], acc[i][j][e]);
+          for (int e = 0; e < 4; ++e) acc[i - 1][j][e] = fmaf(p[j][e], g[j], acc[i - 1][j][e]);
+        }
+        p[j] = q;
+        // (in this order: a product's 8 cycles of issue leave room for four vector instructions, its result is ready four later)
+        if (OT != T_F32) __builtin_amdgcn_sched_barrier(0);
       }
+      x = xn;
     }
     arrive();
+    s = sn;
+#pragma unroll
+    for (int j = 0; j < NI; ++j) g[j] = gn[j];
+  };
+  int kb = 0;
+  for (; kb + 1 < KB; kb += 2) {
+    block(kb, b0, a0, b1, a1);
+    block(kb + 1, b1, a1, b0, a0);
   }
+  if (kb < KB) block(kb, b0, a0, b1, a1);
 #pragma unroll
   for (int j = 0; j < NI; ++j) {
     const int t = t0 + wt + j * 16 + ql;
@@ -212,8 +242,13 @@ hipError_t go(const MmArgs& a, hipStream_t st) {
   else if (a.T <= 32) hipLaunchKernelGGL((k_mm_few<OT, 2>), few, dim3(FEW_W * 64), 0, st, a);
   else if (a.T <= 64) hipLaunchKernelGGL((k_mm_few<OT, 4>), few, dim3(FEW_W * 64), 0, st, a);
   else {
-    const unsigned tiles = (unsigned)((a.N + 127) / 128) * ((a.T + 127) / 128);
-    hipLaunchKernelGGL((k_mm_tile<OT, 128, 128>), dim3(tiles), dim3(256), 0, st, a);
+    auto tiles = [&](int n, int t) { return (unsigned)(((long)(a.N + n - 1) / n * ((a.T + t - 1) / t) + 7) / 8 * 8); };
+    if constexpr (OT != T_F32)
+      if (tiles(256, 256) >= 200) {
+        hipLaunchKernelGGL((k_mm_tile<OT, 256, 256, 2, 4>), dim3(tiles(256, 256)), dim3(512), 0, st, a);
+        return hipGetLastError();
+      }
+    hipLaunchKernelGGL((k_mm_tile<OT, 128, 128, 2, 2>), dim3(tiles(128, 128)), dim3(256), 0, st, a);
   }
   return hipGetLastError();
 }
