@@ -127,6 +127,7 @@ __global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a) {
   // (the two turns' LDS are separate objects: the compiler then sees that loads on their way into one do not concern reads of
   // the other)
   __shared__ __align__(16) char b0[BN * 128], b1[BN * 128], a0[BT * 128], a1[BT * 128];
+  __shared__ float fs[3 * BT * 8];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, g4 = l >> 4, ql = l & 15;
   const int wn = (w % WN) * (BN / WN), wt = (w / WN) * (BT / WT);
   static_assert(W % 2 == 0, "a lane's swizzle is the same in every turn of its rows");
@@ -140,50 +141,52 @@ __global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a) {
   const int rr = w * 8 + (l >> 3), ch = ((l & 7) ^ ((rr >> 1) & 7)) << 4;
   const uint32_t vb = rr * (uint32_t)a.ldb + ch, va = rr * (uint32_t)a.lda + ch;
   const bool tail = (KB - 1) * 128 + ch < a.K;     // does the lane's chunk of the last block exist?
-  auto load = [&](int kb, char* lb, char* la) {
+  constexpr int LB = BN / 8 / W, LA = BT / 8 / W;  // direct loads of a wave and block
+  auto load = [&](int i, int kb, char* lb, char* la) {
     const bool in = (kb < KB - 1) | ((kb == KB - 1) & tail);
-    const uint32_t ob = boff(in, vb), oa = boff(in, va);
-#pragma unroll
-    for (int i = 0; i < BN / 8 / W; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(bb.r, (__attribute__((address_space(3))) void*)(lb + (i * W + w) * 1024), 16, (int)ob,
-                                               (int)(i * W * 8 * (uint32_t)a.ldb + kb * 128), 0, 0);
-#pragma unroll
-    for (int i = 0; i < BT / 8 / W; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ba.r, (__attribute__((address_space(3))) void*)(la + (i * W + w) * 1024), 16, (int)oa,
-                                               (int)(i * W * 8 * (uint32_t)a.lda + kb * 128), 0, 0);
+    if (i < LB)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(bb.r, (__attribute__((address_space(3))) void*)(lb + (i * W + w) * 1024), 16,
+                                               (int)boff(in, vb), (int)(i * W * 8 * (uint32_t)a.ldb + kb * 128), 0, 0);
+    else
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ba.r, (__attribute__((address_space(3))) void*)(la + ((i - LB) * W + w) * 1024), 16,
+                                               (int)boff(in, va), (int)((i - LB) * W * 8 * (uint32_t)a.lda + kb * 128), 0, 0);
   };
   auto arrive = [&] {                              // every wave's direct loads are there
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0x0F70);
     __syncthreads();
   };
-  // factors of a lane's tokens (0 behind the last one), and of the wave's rows, which lie in one block of 128
+  // Factors of the tokens: through LDS, for 8 blocks at a time (a row of sa is 4 bytes a block: read block by block, its lines
+  // came from L2 as often as the codes': 4096 x 8192 x 8192 in 306 us, so in FIXME). Of the tile's BT tokens x 8 blocks, BT values are
+  // loaded with every block and put in their place with the next; they are complete when the 8 blocks begin, and the ring's third
+  // place is the one that nobody reads.
   const Buf bs(a.sa + (long)t0 * KB, (uint32_t)min(a.T - t0, BT) * KB * 4),
       bw(a.sb + (long)((n0 + wn) >> 7) * KB, n0 + wn < a.N ? (uint32_t)KB * 4 : 0u);
-  const uint32_t vs = (wt + ql) * (uint32_t)KB * 4;
-  auto factor = [&](int j, int kb) {
-    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bs.r, (int)vs, (int)((j * 16 * KB + kb) * 4), 0));
+  constexpr int SL = BT / 8;                       // tokens of a slice
+  const int ft = (threadIdx.x % BT) >> 3, fk = threadIdx.x & 7;
+  auto fetch = [&](int p) {                        // slice p & 7 of the 8 blocks behind those of block p
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bs.r, (int)((ft * KB + fk) * 4), (int)(((p & 7) * SL * KB + (p & ~7) + 8) * 4), 0));
   };
+  auto place = [&](int p, float v) { fs[((((p >> 3) + 1) % 3) * BT + (p & 7) * SL + ft) * 8 + fk] = v; };
   auto weight = [&](int kb) { return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bw.r, 0, kb * 4, 0)); };
   f32x4 acc[MI][NI];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  load(0, b0, a0);
-  float g[NI], s = weight(0);
 #pragma unroll
-  for (int j = 0; j < NI; ++j) g[j] = factor(j, 0);
+  for (int i = 0; i < LB + LA; ++i) load(i, 0, b0, a0);
+  for (int p = -8; p < 2; ++p) place(p, fetch(p));
+  float s = weight(0), fv = fetch(2);
   arrive();
   // One block: its products' results are scaled and added while the next row's products run, whose operands are read meanwhile.
   auto block = [&](int kb, const char* lb, const char* la, char* nb, char* na) {
-#pragma unroll
-    for (int j = 0; j < NI; ++j) g[j] *= s;
-    float gn[NI];                                    // (past the last block: another one's, or 0; not used)
+    place(kb + 2, fv);
+    fv = fetch(kb + 3);
     const float sn = weight(kb + 1);
+    float g[NI];
 #pragma unroll
-    for (int j = 0; j < NI; ++j) gn[j] = factor(j, kb + 1);
-    load(kb + 1, nb, na);
+    for (int j = 0; j < NI; ++j) g[j] = fs[(((kb >> 3) % 3) * BT + wt + j * 16 + ql) * 8 + (kb & 7)] * s;
     auto frag = [&](const char* tile, int row) {     // chunks g4 and 4 + g4 of a row
       Codes<OT == T_F32> c;
       const int z = (row >> 1) & 7;
@@ -199,6 +202,9 @@ __global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a) {
     for (int i = 0; i <= MI; ++i) {
       Codes<OT == T_F32> xn;
       if (i + 1 < MI) xn = frag(lb, wn + (i + 1) * 16 + ql);
+      // the next block's direct loads are spread over the rows: issued at once they would hold up the wave
+#pragma unroll
+      for (int c = i * (LB + LA) / MI; c < (i + 1) * (LB + LA) / MI && c < LB + LA; ++c) load(c, kb + 1, nb, na);
 #pragma unroll
       for (int j = 0; j < NI; ++j) {
         f32x4 q;
@@ -215,8 +221,6 @@ __global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a) {
     }
     arrive();
     s = sn;
-#pragma unroll
-    for (int j = 0; j < NI; ++j) g[j] = gn[j];
   };
   int kb = 0;
   for (; kb + 1 < KB; kb += 2) {
