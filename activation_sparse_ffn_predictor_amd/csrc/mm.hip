@@ -174,53 +174,65 @@ __global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a) {
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto frag = [&](const char* tile, int row) {       // chunks g4 and 4 + g4 of a row
+    Codes<OT == T_F32> c;
+    const int z = (row >> 1) & 7;
+    c.set(*reinterpret_cast<const uint4*>(tile + row * 128 + ((g4 ^ z) << 4)),
+          *reinterpret_cast<const uint4*>(tile + row * 128 + (((4 + g4) ^ z) << 4)));
+    return c;
+  };
 #pragma unroll
   for (int i = 0; i < LB + LA; ++i) load(i, 0, b0, a0);
   for (int p = -8; p < 2; ++p) place(p, fetch(p));
   float s = weight(0), fv = fetch(2);
   arrive();
-  // One block: its products' results are scaled and added while the next row's products run, whose operands are read meanwhile.
-  auto block = [&](int kb, const char* lb, const char* la, char* nb, char* na) {
+#pragma unroll
+  for (int i = 0; i < LB + LA; ++i) load(i, 1, b1, a1);
+  // One block. Results are scaled and added while the next row's products run (those of the last row under the next block's
+  // first), a row's operand is read one row ahead. Before the last row the waves meet: nobody reads this block's LDS any more,
+  // which the block after the next is loaded into, and the next block's has arrived, so the last row's products run while the next
+  // block's first operands are read (waves that met at the end of a block: FIXME).
+  Codes<OT == T_F32> x = frag(b0, wn + ql), y[NI];
+  f32x4 p[NI];
+  float gp[NI];
+#pragma unroll
+  for (int j = 0; j < NI; ++j) {
+    y[j] = frag(a0, wt + j * 16 + ql);
+    p[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    gp[j] = 0.f;
+  }
+  auto block = [&](int kb, char* lb, char* la, const char* nb, const char* na) {
     place(kb + 2, fv);
     fv = fetch(kb + 3);
     const float sn = weight(kb + 1);
     float g[NI];
 #pragma unroll
-    for (int j = 0; j < NI; ++j) g[j] = fs[(((kb >> 3) % 3) * BT + wt + j * 16 + ql) * 8 + (kb & 7)] * s;
-    auto frag = [&](const char* tile, int row) {     // chunks g4 and 4 + g4 of a row
-      Codes<OT == T_F32> c;
-      const int z = (row >> 1) & 7;
-      c.set(*reinterpret_cast<const uint4*>(tile + row * 128 + ((g4 ^ z) << 4)),
-            *reinterpret_cast<const uint4*>(tile + row * 128 + (((4 + g4) ^ z) << 4)));
-      return c;
-    };
-    Codes<OT == T_F32> y[NI], x = frag(lb, wn + ql);
+    for (int i = 0; i < MI; ++i) {
+      if (i == MI - 1) arrive();
+      if (i == 1) {
 #pragma unroll
-    for (int j = 0; j < NI; ++j) y[j] = frag(la, wt + j * 16 + ql);
-    f32x4 p[NI];
-#pragma unroll
-    for (int i = 0; i <= MI; ++i) {
-      Codes<OT == T_F32> xn;
-      if (i + 1 < MI) xn = frag(lb, wn + (i + 1) * 16 + ql);
-      // the next block's direct loads are spread over the rows: issued at once they would hold up the wave
-#pragma unroll
-      for (int c = i * (LB + LA) / MI; c < (i + 1) * (LB + LA) / MI && c < LB + LA; ++c) load(c, kb + 1, nb, na);
+        for (int j = 0; j < NI; ++j) g[j] = fs[(((kb >> 3) % 3) * BT + wt + j * 16 + ql) * 8 + (kb & 7)] * s;
+      }
+      const Codes<OT == T_F32> xn = i < MI - 1 ? frag(lb, wn + (i + 1) * 16 + ql) : frag(nb, wn + ql);
 #pragma unroll
       for (int j = 0; j < NI; ++j) {
-        f32x4 q;
-        if (i < MI) q = block_sum(x, y[j]);
-        if (i > 0) {
+        const f32x4 q = block_sum(x, y[j]);
+        if (i == MI - 1) {
+          y[j] = frag(na, wt + j * 16 + ql);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i - 1][j][e] = fmaf(p[j][e], g[j], acc[i - 1][j][e]);
+          for (int c = j * (LB + LA) / NI; c < (j + 1) * (LB + LA) / NI; ++c) load(c, kb + 2, lb, la);
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[(i + MI - 1) % MI][j][e] = fmaf(p[j][e], i ? g[j] : gp[j], acc[(i + MI - 1) % MI][j][e]);
         p[j] = q;
-        // (in this order: a product's 8 cycles of issue leave room for four vector instructions, its result is ready four later)
+        // (in this order: a product occupies the matrix core for as long as eight vector instructions take)
         if (OT != T_F32) __builtin_amdgcn_sched_barrier(0);
       }
       x = xn;
     }
-    arrive();
     s = sn;
+#pragma unroll
+    for (int j = 0; j < NI; ++j) gp[j] = g[j];
   };
   int kb = 0;
   for (; kb + 1 < KB; kb += 2) {
@@ -228,6 +240,10 @@ __global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a) {
     block(kb + 1, b1, a1, b0, a0);
   }
   if (kb < KB) block(kb, b0, a0, b1, a1);
+#pragma unroll
+  for (int j = 0; j < NI; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[MI - 1][j][e] = fmaf(p[j][e], gp[j], acc[MI - 1][j][e]);
 #pragma unroll
   for (int j = 0; j < NI; ++j) {
     const int t = t0 + wt + j * 16 + ql;
