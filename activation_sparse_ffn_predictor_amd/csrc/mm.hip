@@ -9,6 +9,10 @@
 // 1.4e-4 of a sum of independent terms, fp16's own rounding 2.1e-4, bf16's 1.7e-3.
 #include "mm.h"
 
+#include <math.h>
+
+#include <algorithm>
+
 using namespace sffn;
 
 namespace {
@@ -56,64 +60,185 @@ __device__ __forceinline__ Buf rows_of(const char* p, long ld, long r0, long row
 }
 
 // ------------------------------------------------------------------------------------------------ few tokens
-// 16 rows of B a workgroup, whose 8 waves take blocks of k in turn and are added up in LDS. Bound by B's bytes.
-constexpr int FEW_W = 8;
-template <int OT, int TB>
-__global__ __launch_bounds__(FEW_W * 64) void k_mm_few(MmArgs a) {
-  __shared__ f32x4 part[FEW_W][TB][64];
+// Up to 16 tokens: 16 rows of B a workgroup, whose NW waves take blocks of k in turn and are added up in LDS. Bound by B's bytes;
+// a wave has U blocks on their way all the time.
+template <int OT, int NW>
+__global__ __launch_bounds__(NW * 64) void k_mm_few(MmArgs a) {
+  __shared__ f32x4 part[NW][64];
+  constexpr int U = 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, g4 = l >> 4, ql = l & 15;
   const int n0 = blockIdx.x * 16, KB = (a.K + 127) >> 7;
-  const Buf bb = rows_of(a.b, a.ldb, n0, a.N, 16, a.K), ba = rows_of(a.a, a.lda, 0, a.T, TB * 16, a.K);
-  const float* sb = a.sb + (long)(n0 >> 7) * KB;
-  f32x4 acc[TB];
+  const Buf bb = rows_of(a.b, a.ldb, n0, a.N, 16, a.K), ba = rows_of(a.a, a.lda, 0, a.T, 16, a.K), bs(a.sa, (uint32_t)a.T * KB * 4),
+      bw(a.sb + (long)(n0 >> 7) * KB, (uint32_t)KB * 4);
+  const uint32_t vb = ql * (uint32_t)a.ldb + g4 * 16, va = ql * (uint32_t)a.lda + g4 * 16, vs = boff(ql < a.T, ql * (uint32_t)KB * 4);
+  uint4 x[U][2], y[U][2];
+  float f[U], s[U];
+  // workgroups begin at different blocks: rows are often a power of two apart, and those that read the same columns of theirs wait
+  // for the same memory channels (1 x 10240 x 8192: 25 us, so 22)
+  const int turn = blockIdx.x * 5 % KB;
+  auto load = [&](int u, int i) {                  // (past the end nothing is loaded)
+    int kb = i + turn;
+    kb = kb >= KB ? kb - KB : kb;
+    const bool some = i < KB;
 #pragma unroll
-  for (int t = 0; t < TB; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  constexpr int U = 4;                             // blocks in flight
-  for (int k0 = w; k0 < KB; k0 += FEW_W * U) {
-    uint4 x[U][2], y[U][TB][2];
-    float f[U][TB];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int kb = k0 + u * FEW_W;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int col = kb * 128 + (c * 4 + g4) * 16;
-        const bool in = col < a.K;
-        x[u][c] = bb.ld16(boff(in, ql * (uint32_t)a.ldb + col));
-#pragma unroll
-        for (int t = 0; t < TB; ++t) y[u][t][c] = ba.ld16(boff(in, (t * 16 + ql) * (uint32_t)a.lda + col));
-      }
-#pragma unroll
-      for (int t = 0; t < TB; ++t) f[u][t] = kb < KB && t * 16 + ql < a.T ? a.sa[(long)(t * 16 + ql) * KB + kb] : 0.f;
+    for (int c = 0; c < 2; ++c) {
+      const uint32_t col = kb * 128 + c * 64;
+      const bool in = some & (col + g4 * 16 < (uint32_t)a.K);
+      x[u][c] = bb.ld16(boff(in, vb + col));
+      y[u][c] = ba.ld16(boff(in, va + col));
     }
+    f[u] = bs.ldf(boff(some, vs + kb * 4));
+    s[u] = bw.ldf(boff(some, kb * 4));
+  };
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(u, w + u * NW);
+  for (int k0 = w; k0 < KB; k0 += NW * U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int kb = k0 + u * FEW_W;
-      if (kb >= KB) break;
-      const float s = sb[kb];
-      Codes<true> c;
+      Codes<true> c, z;
       c.set(x[u][0], x[u][1]);
+      z.set(y[u][0], y[u][1]);
+      const float g = f[u] * s[u];
+      load(u, k0 + (U + u) * NW);
+      const f32x4 p = block_sum(c, z);
 #pragma unroll
-      for (int t = 0; t < TB; ++t) {
-        Codes<true> z;
-        z.set(y[u][t][0], y[u][t][1]);
-        const f32x4 p = block_sum(c, z);
-        const float g = f[u][t] * s;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(p[i], g, acc[t][i]);
-      }
+      for (int i = 0; i < 4; ++i) acc[i] = fmaf(p[i], g, acc[i]);
     }
   }
-#pragma unroll
-  for (int t = 0; t < TB; ++t) part[w][t][l] = acc[t];
+  part[w][l] = acc;
   __syncthreads();
-  if (threadIdx.x < TB * 64) {
-    const int t = threadIdx.x >> 6, tok = t * 16 + ql, n = n0 + 4 * g4;
-    f32x4 v = part[0][t][l];
+  if (threadIdx.x < 64) {
+    const int n = n0 + 4 * g4;
+    f32x4 v = part[0][l];
 #pragma unroll
-    for (int i = 1; i < FEW_W; ++i) v += part[i][t][l];
-    if (tok < a.T && n < a.N) store4<OT>(a.out, tok * a.ldo + n, v);
+    for (int i = 1; i < NW; ++i) v += part[i][l];
+    if (ql < a.T && n < a.N) store4<OT>(a.out, ql * a.ldo + n, v);
   }
+}
+
+// ------------------------------------------------------------------------------------------------ some tokens
+// BN rows of B x BT tokens a workgroup of WN x WT waves, for calls that B's bytes or a few tiles bound: four blocks of k in LDS,
+// three of them on their way (direct loads) while one is multiplied; k may be spread over workgroups, whose fp32 partial results
+// a second kernel adds up in order. Swizzle as below.
+template <int OT, bool EXACT, int BN, int BT, int WN, int WT>
+__global__ __launch_bounds__(WN * WT * 64) void k_mm_some(MmArgs a, int ks) {
+  constexpr int W = WN * WT, MI = BN / WN / 16, NI = BT / WT / 16, FC = 32;   // FC: blocks whose factors LDS holds
+  constexpr int LB = BN / 8 / W, LA = BT / 8 / W, L = LB + LA;
+  static_assert(LB * 8 * W == BN && LA * 8 * W == BT && BN <= 128, "whole direct loads, one block of 128 rows");
+  constexpr int SW = BN + BT;
+  __shared__ __align__(16) char s0[SW * 128], s1[SW * 128], s2[SW * 128], s3[SW * 128];
+  __shared__ float fs[BT * (FC + 1)], ws[FC];
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, g4 = l >> 4, ql = l & 15;
+  const int wn = (w % WN) * (BN / WN), wt = (w / WN) * (BT / WT);
+  const int tn = (a.N + BN - 1) / BN, share = blockIdx.x % ks, id = blockIdx.x / ks, n0 = id % tn * BN, t0 = id / tn * BT;
+  const int KB = (a.K + 127) >> 7, per = (KB + ks - 1) / ks, k0 = min(KB, share * per), n = min(KB, k0 + per) - k0;   // (its n blocks)
+  const Buf bb = rows_of(a.b, a.ldb, n0, a.N, BN, a.K), ba = rows_of(a.a, a.lda, t0, a.T, BT, a.K);
+  const int rr = w * 8 + (l >> 3), ch = ((l & 7) ^ ((rr >> 1) & 7)) << 4;
+  const uint32_t vb = rr * (uint32_t)a.ldb + ch, va = rr * (uint32_t)a.lda + ch;
+  const bool tail = (KB - 1) * 128 + ch < a.K;
+  auto load = [&](int i0, char* st) {              // (past the end: nothing is read)
+    const int kb = k0 + i0;
+    const bool in = (i0 < n) & ((kb < KB - 1) | tail);
+#pragma unroll
+    for (int i = 0; i < LB; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(bb.r, (__attribute__((address_space(3))) void*)(st + (i * W + w) * 1024), 16,
+                                               (int)boff(in, vb), (int)(i * W * 8 * (uint32_t)a.ldb + kb * 128), 0, 0);
+#pragma unroll
+    for (int i = 0; i < LA; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ba.r, (__attribute__((address_space(3))) void*)(st + BN * 128 + (i * W + w) * 1024), 16,
+                                               (int)boff(in, va), (int)(i * W * 8 * (uint32_t)a.lda + kb * 128), 0, 0);
+  };
+  auto frag = [&](const char* tile, int row) {     // chunks g4 and 4 + g4 of a row
+    Codes<EXACT> c;
+    const int z = (row >> 1) & 7;
+    c.set(*reinterpret_cast<const uint4*>(tile + row * 128 + ((g4 ^ z) << 4)),
+          *reinterpret_cast<const uint4*>(tile + row * 128 + (((4 + g4) ^ z) << 4)));
+    return c;
+  };
+  f32x4 acc[MI][NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // block kb of stage st; the stage that the block before it left is loaded for block kb + 3
+  auto block = [&](int kb, const char* st, char* left) {
+    asm volatile("" ::: "memory");
+    // this wave's loads for kb are there, those of two more blocks may be on their way; then everyone's are, and all have left
+    // the former block's stage
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (2 * L & 15) | ((2 * L >> 4) << 14));
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    load(kb + 3, left);
+    const float s = ws[kb % FC];
+    Codes<EXACT> y[NI];
+    float g[NI];
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      y[j] = frag(st + BN * 128, wt + j * 16 + ql);
+      g[j] = fs[(wt + j * 16 + ql) * (FC + 1) + kb % FC] * s;
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const Codes<EXACT> x = frag(st, wn + i * 16 + ql);
+#pragma unroll
+      for (int j = 0; j < NI; ++j) {
+        const f32x4 p = block_sum(x, y[j]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], g[j], acc[i][j][e]);
+      }
+    }
+  };
+  auto factors = [&](int i0) {                     // of FC blocks from the i0-th on
+    __syncthreads();                               // (also waits for every load on its way)
+    for (int i = threadIdx.x; i < BT * FC; i += W * 64) {
+      const int t = i / FC, k = i0 + i % FC;
+      fs[t * (FC + 1) + i % FC] = t0 + t < a.T && k < n ? a.sa[(long)(t0 + t) * KB + k0 + k] : 0.f;
+    }
+    const int k = i0 + threadIdx.x;
+    if (threadIdx.x < FC) ws[threadIdx.x] = k < n ? a.sb[(long)(n0 >> 7) * KB + k0 + k] : 0.f;
+    __syncthreads();
+  };
+  for (int ic = 0; ic < n; ic += FC) {
+    factors(ic);
+    const int ie = min(n, ic + FC);
+    if (ic == 0) {
+      load(0, s0);
+      load(1, s1);
+      load(2, s2);
+    }
+    // (FC is a multiple of the stages)
+    for (int i = ic; i < ie; i += 4) {
+      block(i, s0, s3);
+      if (i + 1 < ie) block(i + 1, s1, s0);
+      if (i + 2 < ie) block(i + 2, s2, s1);
+      if (i + 3 < ie) block(i + 3, s3, s2);
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);              // (the loads past the end are on their way to this workgroup's LDS)
+#pragma unroll
+  for (int j = 0; j < NI; ++j) {
+    const int t = t0 + wt + j * 16 + ql;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int n = n0 + wn + i * 16 + 4 * g4;
+      if (t >= a.T || n >= a.N) continue;
+      if (ks > 1) *reinterpret_cast<f32x4*>((float*)a.ws + ((long)share * a.T + t) * a.N + n) = acc[i][j];
+      else store4<OT>(a.out, t * a.ldo + n, acc[i][j]);
+    }
+  }
+}
+
+// partial results of the shares of k, added up in their order
+template <int OT>
+__global__ __launch_bounds__(256) void k_mm_join(MmArgs a, int ks) {
+  const long all = (long)a.T * a.N, i = ((long)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= all) return;
+  const int t = (int)(i / a.N), n = (int)(i - (long)t * a.N);
+  f32x4 v = *reinterpret_cast<const f32x4*>((const float*)a.ws + i);
+  for (int s = 1; s < ks; ++s) v += *reinterpret_cast<const f32x4*>((const float*)a.ws + s * all + i);
+  store4<OT>(a.out, t * a.ldo + n, v);
 }
 
 // ------------------------------------------------------------------------------------------------ many tokens
@@ -122,7 +247,7 @@ __global__ __launch_bounds__(FEW_W * 64) void k_mm_few(MmArgs a) {
 // read touches at one chunk spread over all banks. Workgroups of one XCD take neighbouring tiles, 4 along the tokens, so that
 // what they load at one time is shared in its L2.
 template <int OT, int BN, int BT, int WN, int WT>
-__global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a) {
+__global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a, int ks) {
   constexpr int W = WN * WT, MI = BN / WN / 16, NI = BT / WT / 16;        // waves; 16-blocks of a wave
   // (the two turns' LDS are separate objects: the compiler then sees that loads on their way into one do not concern reads of
   // the other)
@@ -131,10 +256,12 @@ __global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a) {
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, g4 = l >> 4, ql = l & 15;
   const int wn = (w % WN) * (BN / WN), wt = (w / WN) * (BT / WT);
   static_assert(W % 2 == 0, "a lane's swizzle is the same in every turn of its rows");
-  const int tn = (a.N + BN - 1) / BN, tt = (a.T + BT - 1) / BT, id = xcd_slice(blockIdx.x, gridDim.x);
+  const int tn = (a.N + BN - 1) / BN, tt = (a.T + BT - 1) / BT, each = xcd_slice(blockIdx.x, gridDim.x),
+            share = each % ks, id = each / ks;
   if (id >= tn * tt) return;
   const int first = id / (4 * tn) * 4, wide = min(4, tt - first), in = id % (4 * tn);
-  const int n0 = in / wide * BN, t0 = (first + in % wide) * BT, KB = (a.K + 127) >> 7;
+  const int n0 = in / wide * BN, t0 = (first + in % wide) * BT;
+  const int KB = (a.K + 127) >> 7, per = (KB + ks - 1) / ks, k0 = min(KB, share * per), nk = min(KB, k0 + per) - k0;   // (its nk blocks)
   const Buf bb = rows_of(a.b, a.ldb, n0, a.N, BN, a.K), ba = rows_of(a.a, a.lda, t0, a.T, BT, a.K);
   // direct loads: a wave's 8 rows at a time, W waves beside each other; a lane's row keeps its swizzle from turn to turn, so one
   // offset serves all, with the rows and blocks passed as the wave's own. Past the last row, and past K, zeros are read.
@@ -143,13 +270,13 @@ __global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a) {
   const bool tail = (KB - 1) * 128 + ch < a.K;     // does the lane's chunk of the last block exist?
   constexpr int LB = BN / 8 / W, LA = BT / 8 / W;  // direct loads of a wave and block
   auto load = [&](int i, int kb, char* lb, char* la) {
-    const bool in = (kb < KB - 1) | ((kb == KB - 1) & tail);
+    const bool in = (kb < nk) & ((k0 + kb < KB - 1) | tail);
     if (i < LB)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(bb.r, (__attribute__((address_space(3))) void*)(lb + (i * W + w) * 1024), 16,
-                                               (int)boff(in, vb), (int)(i * W * 8 * (uint32_t)a.ldb + kb * 128), 0, 0);
+                                               (int)boff(in, vb), (int)(i * W * 8 * (uint32_t)a.ldb + (k0 + kb) * 128), 0, 0);
     else
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ba.r, (__attribute__((address_space(3))) void*)(la + ((i - LB) * W + w) * 1024), 16,
-                                               (int)boff(in, va), (int)((i - LB) * W * 8 * (uint32_t)a.lda + kb * 128), 0, 0);
+                                               (int)boff(in, va), (int)((i - LB) * W * 8 * (uint32_t)a.lda + (k0 + kb) * 128), 0, 0);
   };
   auto arrive = [&] {                              // every wave's direct loads are there
     asm volatile("" ::: "memory");
@@ -157,7 +284,7 @@ __global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a) {
     __syncthreads();
   };
   // Factors of the tokens: through LDS, for 8 blocks at a time (a row of sa is 4 bytes a block: read block by block, its lines
-  // came from L2 as often as the codes': 4096 x 8192 x 8192 in 306 us, so in FIXME). Of the tile's BT tokens x 8 blocks, BT values are
+  // came from L2 as often as the codes': 4096 x 8192 x 8192 in 311 us, so in 282). Of the tile's BT tokens x 8 blocks, BT values are
   // loaded with every block and put in their place with the next; they are complete when the 8 blocks begin, and the ring's third
   // place is the one that nobody reads.
   const Buf bs(a.sa + (long)t0 * KB, (uint32_t)min(a.T - t0, BT) * KB * 4),
@@ -165,10 +292,10 @@ __global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a) {
   constexpr int SL = BT / 8;                       // tokens of a slice
   const int ft = (threadIdx.x % BT) >> 3, fk = threadIdx.x & 7;
   auto fetch = [&](int p) {                        // slice p & 7 of the 8 blocks behind those of block p
-    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bs.r, (int)((ft * KB + fk) * 4), (int)(((p & 7) * SL * KB + (p & ~7) + 8) * 4), 0));
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bs.r, (int)((ft * KB + fk) * 4), (int)(((p & 7) * SL * KB + (p & ~7) + 8 + k0) * 4), 0));
   };
   auto place = [&](int p, float v) { fs[((((p >> 3) + 1) % 3) * BT + (p & 7) * SL + ft) * 8 + fk] = v; };
-  auto weight = [&](int kb) { return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bw.r, 0, kb * 4, 0)); };
+  auto weight = [&](int kb) { return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bw.r, 0, (k0 + kb) * 4, 0)); };
   f32x4 acc[MI][NI];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
@@ -191,7 +318,7 @@ __global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a) {
   // One block. Results are scaled and added while the next row's products run (those of the last row under the next block's
   // first), a row's operand is read one row ahead. Before the last row the waves meet: nobody reads this block's LDS any more,
   // which the block after the next is loaded into, and the next block's has arrived, so the last row's products run while the next
-  // block's first operands are read (waves that met at the end of a block: FIXME).
+  // block's first operands are read (with waves that meet at the end of a block: 362 us for 357, fp32 results 666 for 599).
   Codes<OT == T_F32> x = frag(b0, wn + ql), y[NI];
   f32x4 p[NI];
   float gp[NI];
@@ -235,11 +362,12 @@ __global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a) {
     for (int j = 0; j < NI; ++j) gp[j] = g[j];
   };
   int kb = 0;
-  for (; kb + 1 < KB; kb += 2) {
+  for (; kb + 1 < nk; kb += 2) {
     block(kb, b0, a0, b1, a1);
     block(kb + 1, b1, a1, b0, a0);
   }
-  if (kb < KB) block(kb, b0, a0, b1, a1);
+  if (kb < nk) block(kb, b0, a0, b1, a1);
+  __builtin_amdgcn_s_waitcnt(0x0F70);                // (the loads past the end are on their way to this workgroup's LDS)
 #pragma unroll
   for (int j = 0; j < NI; ++j)
 #pragma unroll
@@ -250,32 +378,80 @@ __global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a) {
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
       const int n = n0 + wn + i * 16 + 4 * g4;
-      if (t < a.T && n < a.N) store4<OT>(a.out, t * a.ldo + n, acc[i][j]);
+      if (t >= a.T || n >= a.N) continue;
+      if (ks > 1) *reinterpret_cast<f32x4*>((float*)a.ws + ((long)share * a.T + t) * a.N + n) = acc[i][j];
+      else store4<OT>(a.out, t * a.ldo + n, acc[i][j]);
     }
   }
 }
 
+// Which kernel, and over how many workgroups k is spread: the sum of measured costs decides. Workgroups take a block of k in `one`
+// us when a compute unit has one of them and in `all` when it has as many as fit; a join starts in 4 us and moves each partial
+// result out and in at 5 TB/s. 10240 rows of K = 8192, us: 128 tokens SOME128 40, TILE128 in three shares 31; 256 tokens TILE128 59, in
+// three shares 45; 512 tokens TILE128 82, TILE256 in three shares 63; 1024 tokens TILE128 128, TILE256
+// 109; 2048 tokens 204 and 218; 4096 TILE256 340.
+enum { FEW, SOME32, SOME64, SOME128, TILE128, TILE256 };
+struct Shape {
+  int n, t, fit;                                   // rows and tokens of a workgroup, workgroups a compute unit
+  double one, all;
+};
+constexpr Shape SHAPES[] = {{16, 16, 4, 0, 0},        {64, 32, 3, 0.42, 0.75},   {64, 64, 2, 0.62, 0.9},
+                            {64, 128, 1, 0.6, 0.6},   {128, 128, 2, 0.92, 1.28}, {256, 256, 1, 1.75, 1.75}};
+struct Plan {
+  int how, ks;
+};
+Plan plan(int T, int N, int K, bool f32) {
+  // few tokens' rows go to registers; past 4 tokens and 16 MB their loads outweigh what LDS costs (10240 x 8192: 16 tokens 31 us, by
+  // LDS 22; 512 x 1024, 8 tokens: 4.9 and 5.6)
+  if (T <= 4 || (T <= 16 && (long)N * K <= 1 << 24)) return {FEW, 1};
+  const int KB = (K + 127) / 128, from = T <= 32 ? SOME32 : T <= 64 ? SOME64 : SOME128,
+            to = T <= 32 ? SOME32 : T <= 64 ? SOME64 : f32 ? TILE128 : TILE256;
+  Plan best{from, 1};
+  double least = 0;
+  for (int how = from; how <= to; ++how) {
+    const Shape& c = SHAPES[how];
+    const double tiles = (double)((N + c.n - 1) / c.n) * ((T + c.t - 1) / c.t);
+    for (const int ks : {1, 2, 3, 4, 6, 8}) {
+      if (ks > 1 && (KB < 4 * ks || tiles * ks > 512)) break;
+      const double wgs = tiles * ks, fit = 256.0 * c.fit, turns = c.fit == 1 ? ceil(wgs / fit) : std::max(wgs / fit, ceil(wgs / fit) - 0.4);
+      double us = turns * ((KB + ks - 1) / ks) * (wgs <= 256 ? c.one : c.all);
+      if (ks > 1) us += 4.0 + (double)ks * T * N * 8 / 5e6;
+      if (least == 0 || us < least) best = {how, ks}, least = us;
+    }
+  }
+  return best;
+}
+
 template <int OT>
 hipError_t go(const MmArgs& a, hipStream_t st) {
-  const dim3 few((a.N + 15) / 16);
-  if (a.T <= 16) hipLaunchKernelGGL((k_mm_few<OT, 1>), few, dim3(FEW_W * 64), 0, st, a);
-  else if (a.T <= 32) hipLaunchKernelGGL((k_mm_few<OT, 2>), few, dim3(FEW_W * 64), 0, st, a);
-  else if (a.T <= 64) hipLaunchKernelGGL((k_mm_few<OT, 4>), few, dim3(FEW_W * 64), 0, st, a);
-  else {
-    auto tiles = [&](int n, int t) { return (unsigned)(((long)(a.N + n - 1) / n * ((a.T + t - 1) / t) + 7) / 8 * 8); };
-    if constexpr (OT != T_F32)
-      if (tiles(256, 256) >= 200) {
-        hipLaunchKernelGGL((k_mm_tile<OT, 256, 256, 2, 4>), dim3(tiles(256, 256)), dim3(512), 0, st, a);
-        return hipGetLastError();
-      }
-    hipLaunchKernelGGL((k_mm_tile<OT, 128, 128, 2, 2>), dim3(tiles(128, 128)), dim3(256), 0, st, a);
-  }
+  const Plan p = plan(a.T, a.N, a.K, OT == T_F32);
+  auto tiles = [&](int n, int t) { return (unsigned)((long)((a.N + n - 1) / n) * ((a.T + t - 1) / t)); };
+  auto whole = [&](unsigned v) { return dim3((v + 7) / 8 * 8); };
+  if (p.how == FEW) {
+    // (waves as many as leave 16 on a compute unit)
+    const unsigned n = tiles(16, 16);
+    if (n >= 512) hipLaunchKernelGGL((k_mm_few<OT, 4>), dim3(n), dim3(256), 0, st, a);
+    else if (n >= 256) hipLaunchKernelGGL((k_mm_few<OT, 8>), dim3(n), dim3(512), 0, st, a);
+    else hipLaunchKernelGGL((k_mm_few<OT, 16>), dim3(n), dim3(1024), 0, st, a);
+  } else if (p.how == SOME32) hipLaunchKernelGGL((k_mm_some<OT, true, 64, 32, 4, 1>), dim3(tiles(64, 32) * p.ks), dim3(256), 0, st, a, p.ks);
+  else if (p.how == SOME64) hipLaunchKernelGGL((k_mm_some<OT, true, 64, 64, 2, 2>), dim3(tiles(64, 64) * p.ks), dim3(256), 0, st, a, p.ks);
+  else if (p.how == SOME128) hipLaunchKernelGGL((k_mm_some<OT, OT == T_F32, 64, 128, 2, 4>), dim3(tiles(64, 128) * p.ks), dim3(512), 0, st, a, p.ks);
+  else if (p.how == TILE128 || OT == T_F32) hipLaunchKernelGGL((k_mm_tile<OT, 128, 128, 2, 2>), whole(tiles(128, 128) * p.ks), dim3(256), 0, st, a, p.ks);
+  else if constexpr (OT != T_F32) hipLaunchKernelGGL((k_mm_tile<OT, 256, 256, 2, 4>), whole(tiles(256, 256) * p.ks), dim3(512), 0, st, a, p.ks);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.ks == 1) return e;
+  hipLaunchKernelGGL(k_mm_join<OT>, dim3((unsigned)(((long)a.T * a.N / 4 + 255) / 256)), dim3(256), 0, st, a, p.ks);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t sffn_mm_workspace(int T, int N, int K) { (void)T, (void)N, (void)K; return 0; }
+size_t sffn_mm_workspace(int T, int N, int K) {
+  // (whichever type the results are of)
+  const Plan p = plan(T, N, K, false), q = plan(T, N, K, true);
+  const int ks = p.ks > q.ks ? p.ks : q.ks;
+  return ks > 1 ? (size_t)ks * T * N * sizeof(float) : 0;
+}
 
 hipError_t sffn_launch_mm(const MmArgs& a, int ot, hipStream_t st) {
   return ot == T_F32 ? go<T_F32>(a, st) : ot == T_F16 ? go<T_F16>(a, st) : go<T_BF16>(a, st);

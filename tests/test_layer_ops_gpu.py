@@ -109,7 +109,11 @@ def test_quant_nonfinite_and_small(gpu_ready, xt, rows):
 MM = [(1, 8, 16, "f32"), (1, 4096, 4096, "f16"), (1, 1032, 8192, "bf16"), (3, 136, 144, "f32"), (16, 128, 1024, "f16"),
       (17, 264, 272, "bf16"), (32, 72, 128, "f32"), (37, 15360, 5120, "bf16"), (64, 512, 2048, "f16"), (65, 128, 128, "f32"),
       (100, 1000, 1040, "f16"), (128, 136, 384, "f32"), (129, 648, 528, "bf16"), (257, 264, 16, "f32"), (300, 2048, 4096, "f32"),
-      (1000, 776, 656, "f16"), (2, 16, 65536, "f32"), (513, 1288, 1536, "f32"), (80, 8, 1024, "f32"), (2048, 2304, 2048, "bf16")]
+      (1000, 776, 656, "f16"), (2, 16, 65536, "f32"), (513, 1288, 1536, "f32"), (80, 8, 1024, "f32"), (2048, 2304, 2048, "bf16"),
+      # every kernel that larger calls choose, k in one share and in several, with ends inside tiles, blocks and shares
+      (4, 20008, 1168, "f16"), (9, 5128, 4112, "bf16"), (24, 1032, 4096, "f16"), (31, 24584, 640, "f32"), (48, 2056, 8208, "bf16"),
+      (60, 16392, 912, "f16"), (100, 2056, 4112, "f32"), (90, 12808, 528, "f32"), (128, 10248, 4112, "f16"), (300, 4104, 4112, "bf16"),
+      (512, 10248, 8208, "f16"), (200, 2056, 4096, "f32"), (2100, 8200, 656, "bf16"), (640, 10240, 1040, "f16"), (1500, 1032, 2064, "f32")]
 
 
 def mm_case(T, N, K, seed=0):
