@@ -423,7 +423,9 @@ int sffn_attn_mass(sffn_kv c, sffn_seqs q, const int32_t* seq_len, int type, con
 
 size_t sffn_kv_evict_workspace_size(int S, int n_kv_heads, int W, int keep) {
   if (S < 1 || S > MAX_S || n_kv_heads < 1 || n_kv_heads > 65535 || keep < 1 || keep > W) return 0;
-  return align256((size_t)S * n_kv_heads * keep * sizeof(int));
+  sffn::EvictArgs a{};
+  a.S = S, a.W = W, a.keep = keep;
+  return sffn::evict_plan(a, n_kv_heads, nullptr);
 }
 
 int sffn_kv_evict(sffn_kv c, const int32_t* kv_len, const int32_t* seq_len, const int32_t* table, int S, int max_pages,
@@ -448,11 +450,12 @@ int sffn_kv_evict(sffn_kv c, const int32_t* kv_len, const int32_t* seq_len, cons
       if (all[i] == all[j] && !(j == 0 && i == 3) && !(j == 1 && i == 4) && !(j == 5 && (i == 6 || i == 7)))
         return fail(SFFN_ERR_ARG, "kv_evict: an output overlaps another tensor");
   if ((s = check_workspace(ws, ws_bytes, sffn_kv_evict_workspace_size(S, c.n_kv_heads, W, keep)))) return s;
-  // fewer than 2^32 threads a launch, 8 slots a workgroup at least
-  if ((int64_t)((keep + 7) / 8) * S * c.n_kv_heads >= ((int64_t)1 << 24))
+  // fewer than 2^32 threads a launch, 8 slots a workgroup at least, and 256 of weights and positions
+  if ((int64_t)((keep + 7) / 8 + (keep + 255) / 256) * S * c.n_kv_heads >= ((int64_t)1 << 24))
     return fail(SFFN_ERR_SHAPE, "S=%d, n_kv_heads=%d, keep=%d: too many slots", S, c.n_kv_heads, keep);
-  const sffn::EvictArgs a{kv_of(c), kv_len, seq_len, table, mass, pos, mass_out, pos_out, kv_len_out, src, (int*)ws, S, max_pages,
-                          table_stride, W, keep, sinks, recent};
+  sffn::EvictArgs a{kv_of(c), kv_len, seq_len, table, mass, pos, mass_out, pos_out, kv_len_out, src, S, max_pages, table_stride, W, keep,
+                    sinks, recent};
+  sffn::evict_plan(a, c.n_kv_heads, ws);
   const hipError_t e = sffn_launch_evict(a, c.type, (hipStream_t)stream);
   return e == hipSuccess ? SFFN_OK : sffn_err_hip(e, "kv_evict launch");
 }

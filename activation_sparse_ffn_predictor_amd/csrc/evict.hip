@@ -4,9 +4,10 @@
 // What stays in a slot at or behind `keep` moves, in order, into the slots below it that are given up, in order: nothing that
 // may stay where it is is moved, no row is both read and written, so all moves run at once.
 //
-// Selection: one workgroup a sequence and head. A token's place in the order is a 32-bit key; the key of the last one that stays
-// is found digit by digit (11, 11 and 10 bits) with counts in LDS. Bound by memory: weights and positions once, then the moved
-// rows in and out.
+// Selection: a token's place in the order is a 32-bit key; the key of the last one that stays is found digit by digit (11, 11 and
+// 10 bits) with counts in LDS. Up to 8192 slots one workgroup does all of it with the keys in registers; more slots are spread
+// over workgroups, a kernel a digit, since one workgroup's passes are bound by its instructions (6 x 8 heads of 40001 slots in
+// 48 workgroups: 69 us). The moves are bound by memory: the moved rows in and out.
 #include "evict.h"
 
 using namespace sffn;
@@ -14,6 +15,7 @@ using namespace sffn;
 namespace {
 
 constexpr int NT = 1024, BINS = 2048;
+constexpr int REGS = 8;                            // keys that a thread keeps in registers
 
 // Order of a slot's token: 0 holds none, 1 no weight (what is negative or NaN counts as none), then by weight, protected last
 struct Keys {
@@ -30,137 +32,362 @@ struct Keys {
   }
 };
 
-// KPT keys a thread stay in registers (0: they are worked out again each time). Wave w owns slots w * seg .. (w + 1) * seg - 1.
-template <int KPT>
-__global__ __launch_bounds__(NT) void k_select(EvictArgs a) {
-  __shared__ int hist[BINS];
-  __shared__ int tmp[NT / 64 + 1];
-  __shared__ int found[2];
-  const int hk = blockIdx.x, s = blockIdx.y, w = threadIdx.x >> 6, l = threadIdx.x & 63, keep = a.keep;
-  const long sh = (long)s * a.kv.hkv + hk;
-  int* src = a.src + sh * keep;
-  const int n = min(max(a.len[s], 0), min(a.cols << a.kv.psh, a.W));
-  if (n <= keep) {
-    for (int j = threadIdx.x; j < keep; j += NT) src[j] = j;
-    return;
+// inclusive sum over the wave's lanes (row shifts and broadcasts of DPP: no LDS crossbar)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int shift_add(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, true);
+}
+__device__ __forceinline__ int row_scan(int v) {
+  v = shift_add<0x111, 0xF>(v);
+  v = shift_add<0x112, 0xF>(v);
+  v = shift_add<0x114, 0xF>(v);
+  return shift_add<0x118, 0xF>(v);
+}
+__device__ __forceinline__ int wave_scan(int v) {
+  v = row_scan(v);
+  v = shift_add<0x142, 0xA>(v);
+  return shift_add<0x143, 0xC>(v);
+}
+// a wave's number before it among the workgroup's (tmp: one a wave, written and synchronised), and all of them together
+__device__ __forceinline__ int before_wave(const int* tmp, int& total) {
+  const int l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = row_scan(tmp[l & 15]);
+  total = __builtin_amdgcn_readlane(c, 15);
+  return w ? __builtin_amdgcn_readlane(c, w - 1) : 0;
+}
+
+// Counts of one digit of the keys (bits 31 .. 21, 20 .. 10, 9 .. 0) among those that share the cut's digits above it. Protected
+// tokens, and those without weight, would all count in one place: those are counted by the wave. In every lane of the wave.
+struct Digit {
+  int low, up, mask;
+  uint32_t over;
+  __device__ __forceinline__ Digit(int d, uint32_t cut) : low(d == 0 ? 21 : d == 1 ? 10 : 0), up(low + (d == 2 ? 10 : 11)), mask(d == 2 ? 1023 : 2047), over(d ? cut >> up : 0) {}
+  __device__ __forceinline__ void count(int* hist, uint32_t x, bool in, int& tops, int& ones) const {
+    const bool top = in && x == 0xFFFFFFFFu, mine = in && !top && (low == 21 || x >> up == over);
+    tops += __popcll(__ballot(top));
+    ones += __popcll(__ballot(mine && x == 1u));
+    if (mine && x != 1u) atomicAdd(&hist[(x >> low) & mask], 1);
   }
-  const Keys key{a.mass + sh * a.W, a.pos + sh * a.W, a.table + (long)s * a.ldt, a.kv.psh, a.kv.n_pages, a.cols, a.sinks,
-                 a.recent ? (int)max((long)a.plen[s] - a.recent, -2147483648l) : 2147483647};
-  const int steps = (n + NT - 1) / NT, j0 = w * steps * 64 + l;      // slots j0, j0 + 64, ... of this lane
-  uint32_t k[KPT ? KPT : 1];
-#pragma unroll
-  for (int i = 0; i < KPT; ++i) k[i] = i < steps && j0 + i * 64 < n ? key(j0 + i * 64) : 0;
-  auto each = [&](auto f) {                        // f(slot, key, does it exist) in every lane of the wave
-    if constexpr (KPT > 0) {
-#pragma unroll
-      for (int i = 0; i < KPT; ++i)
-        if (i < steps) f(j0 + i * 64, k[i], j0 + i * 64 < n);
-    } else {
-      for (int i = 0; i < steps; ++i) f(j0 + i * 64, j0 + i * 64 < n ? key(j0 + i * 64) : 0u, j0 + i * 64 < n);
-    }
-  };
+  __device__ __forceinline__ int of_ones() const { return low ? 0 : 1; }
+};
+// The digit of the last key that stays, and how many of its keys do, where `need` of the counted ones stay: thread t has the
+// counts n1 and n0 of the digits 2047 - 2 t and the one below it. found: of LDS; synchronised afterwards.
+__device__ __forceinline__ void find_digit(int n1, int n0, int need, int* tmp, int* found) {
   int total;
-  // protected ones, which would all count in one place
-  int c = 0;
-  each([&](int, uint32_t x, bool in) { c += __popcll(__ballot(in && x == 0xFFFFFFFFu)); });
-  block_exclusive_scan<NT>(l == 0 ? c : 0, tmp, total);
+  const int b1 = BINS - 1 - 2 * threadIdx.x, inc = wave_scan(n1 + n0);
+  if ((threadIdx.x & 63) == 63) tmp[threadIdx.x >> 6] = inc;
   __syncthreads();
-  uint32_t cut = 0xFFFFFFFFu;                      // the last key that stays, and how many of those do
-  int ties = keep;
-  if (total < keep) {
-    ties = keep - total;
-    cut = 0;
-    // digits: bits 31 .. 21, 20 .. 10, 9 .. 0
-#pragma unroll 1
-    for (int d = 0; d < 3; ++d) {
-      const int low = d == 0 ? 21 : d == 1 ? 10 : 0;
-      hist[threadIdx.x] = hist[threadIdx.x + NT] = 0;
-      __syncthreads();
-      int ones = 0;                                // tokens without weight, which would all count in one place too
-      each([&](int, uint32_t x, bool in) {
-        const bool mine = in && x != 0xFFFFFFFFu && (d == 0 || (x >> (low + (d == 1 ? 11 : 10))) == (cut >> (low + (d == 1 ? 11 : 10))));
-        ones += __popcll(__ballot(mine && x == 1u));
-        if (mine && x != 1u) atomicAdd(&hist[(x >> low) & (d == 2 ? 1023 : 2047)], 1);
-      });
-      if (l == 0 && ones) atomicAdd(&hist[(1u >> low) & 2047], ones);
-      __syncthreads();
-      // from the largest digit down: thread t has 2047 - 2 t and the one below it
-      const int b1 = BINS - 1 - 2 * threadIdx.x, n1 = hist[b1], n0 = hist[b1 - 1];
-      const int above = block_exclusive_scan<NT>(n1 + n0, tmp, total);
-      if (above < ties && ties <= above + n1) { found[0] = b1; found[1] = ties - above; }
-      else if (above + n1 < ties && ties <= above + n1 + n0) { found[0] = b1 - 1; found[1] = ties - above - n1; }
-      __syncthreads();
-      cut |= (uint32_t)found[0] << low;
-      ties = found[1];
-      __syncthreads();
+  const int above = before_wave(tmp, total) + inc - n1 - n0;
+  if (above < need && need <= above + n1) { found[0] = b1; found[1] = need - above; }
+  else if (above + n1 < need && need <= above + n1 + n0) { found[0] = b1 - 1; found[1] = need - above - n1; }
+  __syncthreads();
+}
+// A workgroup's slots j0, j0 + 64, ... of this lane, `steps` of them, below `end`; wave w owns (w * steps .. (w + 1) * steps - 1) * 64, so
+// that ranks in slot order need one prefix over the waves. Keys are in registers, or (WS) read REGS at a time.
+template <bool WS>
+struct Slots {
+  int j0, steps, end;
+  const uint32_t* kept;
+  uint32_t k[REGS];
+  template <class F>
+  __device__ __forceinline__ void each(F f) {      // f(slot, key, does it exist) in every lane of the wave
+    for (int i0 = 0; i0 < steps; i0 += REGS) {
+      if constexpr (WS) {
+#pragma unroll
+        for (int i = 0; i < REGS; ++i) k[i] = kept[min(j0 + (i0 + i) * 64, end - 1)];
+      }
+#pragma unroll
+      for (int i = 0; i < REGS; ++i) {
+        const int j = j0 + (i0 + i) * 64;
+        if (i0 + i < steps) f(j, k[i], j < end);
+      }
     }
   }
-  // keys over `cut` stay, and of those equal to it the first `ties`
+};
+// Keys over `cut` stay, and of those equal to it the first `ties` in slot order, `rank` of which stand before this workgroup's. Writes
+// the slots below `keep` that are given up to to[holes ...], those at or behind it that stay to from[movers ...], in order, and the
+// others' src (given-up ones: -1, until the move). tmp: three of an int a wave.
+template <bool WS>
+__device__ __forceinline__ void emit(Slots<WS>& sl, const EvictArgs& a, long sh, uint32_t cut, int ties, int rank, int movers, int holes,
+                                     int (*tmp)[NT / 64], int* moves) {
+  const int l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), keep = a.keep;
   const uint64_t below = l ? ~0ull >> (64 - l) : 0ull;
-  c = 0;
-  each([&](int, uint32_t x, bool in) { c += __popcll(__ballot(in && x == cut)); });
-  int run = __shfl(block_exclusive_scan<NT>(l == 0 ? c : 0, tmp, total), 0, WAVE);
-  __syncthreads();
-  const int tie0 = run;
-  int movers = 0, holes = 0;
-  each([&](int j, uint32_t x, bool in) {
-    const uint64_t eq = __ballot(in && x == cut);
-    const bool stay = in && (x > cut || (x == cut && run + __popcll(eq & below) < ties));
-    run += __popcll(eq);
-    movers += __popcll(__ballot(stay && j >= keep));
-    holes += __popcll(__ballot(in && !stay && j < keep));
+  int eq_lo = 0, eq_hi = 0, gt_lo = 0, gt_hi = 0, lows = 0, total;
+  sl.each([&](int j, uint32_t x, bool in) {
+    const uint64_t lo = __ballot(in && j < keep), e = __ballot(in && x == cut), g = __ballot(in && x > cut);
+    lows += __popcll(lo);
+    eq_lo += __popcll(e & lo);
+    eq_hi += __popcll(e & ~lo);
+    gt_lo += __popcll(g & lo);
+    gt_hi += __popcll(g & ~lo);
   });
-  const int m0 = __shfl(block_exclusive_scan<NT>(l == 0 ? movers : 0, tmp, total), 0, WAVE);
+  if (l == 0) tmp[0][w] = eq_lo + eq_hi;
   __syncthreads();
-  const int h0 = __shfl(block_exclusive_scan<NT>(l == 0 ? holes : 0, tmp, total), 0, WAVE);
-  int* line = a.line + sh * keep;                  // the movers' slots in order
-  run = tie0;
-  int m = m0;
-  each([&](int j, uint32_t x, bool in) {
-    const uint64_t eq = __ballot(in && x == cut);
-    const bool stay = in && (x > cut || (x == cut && run + __popcll(eq & below) < ties));
-    run += __popcll(eq);
-    const uint64_t mv = __ballot(stay && j >= keep);
-    if (stay && j >= keep) line[m + __popcll(mv & below)] = j;
+  rank += before_wave(tmp[0], total);              // of the wave's first key equal to `cut`
+  const int left = max(0, ties - rank), stay_lo = min(eq_lo, left), stay_hi = min(eq_hi, left - stay_lo);
+  if (l == 0) {
+    tmp[1][w] = gt_hi + stay_hi;                   // the wave's movers and holes
+    tmp[2][w] = lows - gt_lo - stay_lo;
+  }
+  __syncthreads();
+  int h = holes + before_wave(tmp[2], total), m = movers + before_wave(tmp[1], total);
+  if (moves && threadIdx.x == 0) *moves = total;   // (as many move as there are holes)
+  int *src = a.src + sh * keep, *from = a.from + sh * keep, *to = a.to + sh * keep;
+  sl.each([&](int j, uint32_t x, bool in) {
+    const uint64_t e = __ballot(in && x == cut);
+    const bool stay = in && (x > cut || (x == cut && rank + __popcll(e & below) < ties));
+    rank += __popcll(e);
+    const uint64_t mv = __ballot(stay && j >= keep), hv = __ballot(in && !stay && j < keep);
+    if (stay && j >= keep) from[m + __popcll(mv & below)] = j;
+    if (in && j < keep) {
+      src[j] = stay ? j : -1;
+      if (!stay) to[h + __popcll(hv & below)] = j;
+    }
     m += __popcll(mv);
-  });
-  __syncthreads();                                 // (orders the workgroup's own writes of the list before its reads)
-  run = tie0;
-  int h = h0;
-  each([&](int j, uint32_t x, bool in) {
-    const uint64_t eq = __ballot(in && x == cut);
-    const bool stay = in && (x > cut || (x == cut && run + __popcll(eq & below) < ties));
-    run += __popcll(eq);
-    const bool hole = in && !stay && j < keep;
-    const uint64_t hv = __ballot(hole);
-    if (in && j < keep) src[j] = hole ? line[h + __popcll(hv & below)] : j;
     h += __popcll(hv);
   });
 }
 
-// The moves: LPR lanes a slot, 16 bytes each of K and V; weights, positions and scales with them.
-template <int LPR>
-__global__ __launch_bounds__(256) void k_move(EvictArgs a, int eb, int groups) {
-  const int hk = blockIdx.x % a.kv.hkv, g = blockIdx.x / a.kv.hkv % groups, s = blockIdx.x / a.kv.hkv / groups;
-  const int lane = threadIdx.x % LPR, j = g * (256 / LPR) + threadIdx.x / LPR;
+__device__ __forceinline__ int slots_of(const EvictArgs& a, int s) { return min(max(a.len[s], 0), min(a.cols << a.kv.psh, a.W)); }
+__device__ __forceinline__ Keys keys_of(const EvictArgs& a, int s, long sh) {
+  return {a.mass + sh * a.W, a.pos + sh * a.W, a.table + (long)s * a.ldt, a.kv.psh, a.kv.n_pages, a.cols, a.sinks,
+          a.recent ? (int)max((long)a.plen[s] - a.recent, -2147483648l) : 2147483647};
+}
+__device__ __forceinline__ void keep_all(const EvictArgs& a, long sh, int first, int step) {
+  for (int j = first; j < a.keep; j += step) a.src[sh * a.keep + j] = j;
+  if (first == 0) a.moves[sh] = 0;
+}
+
+// up to REGS * NT slots: one workgroup
+__global__ __launch_bounds__(NT) void k_select(EvictArgs a) {
+  __shared__ int hist[BINS];
+  __shared__ int tmp[3][NT / 64];
+  __shared__ int prot, found[3][2];
+  const int hk = blockIdx.x, s = blockIdx.y, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
   const long sh = (long)s * a.kv.hkv + hk;
-  const int n = min(max(a.len[s], 0), min(a.cols << a.kv.psh, a.W));
-  // (the lengths may be updated in place while other workgroups read them: n, cut off at keep, is the same before and after)
-  if (g == 0 && hk == 0 && threadIdx.x == 0) {
-    const int old = a.len[s];
-    a.len_out[s] = n > a.keep ? a.keep : old;
+  const int n = slots_of(a, s);
+  if (n <= a.keep) return keep_all(a, sh, threadIdx.x, NT);
+  const Keys key = keys_of(a, s, sh);
+  Slots<false> sl;
+  sl.steps = (n + NT - 1) / NT;
+  sl.j0 = w * sl.steps * 64 + l;
+  sl.end = n;
+#pragma unroll
+  for (int i = 0; i < REGS; ++i)
+    if (i < sl.steps) sl.k[i] = key(min(sl.j0 + i * 64, n - 1));
+  hist[threadIdx.x] = hist[threadIdx.x + NT] = 0;
+  if (threadIdx.x == 0) prot = 0;
+  __syncthreads();
+  uint32_t cut = 0;                                // the last key that stays, and how many of those do
+  int ties = a.keep;
+#pragma unroll 1
+  for (int d = 0; d < 3; ++d) {
+    const Digit g(d, cut);
+    int tops = 0, ones = 0;
+    sl.each([&](int, uint32_t x, bool in) { g.count(hist, x, in, tops, ones); });
+    if (l == 0 && ones) atomicAdd(&hist[g.of_ones()], ones);
+    if (l == 0 && tops && d == 0) atomicAdd(&prot, tops);
+    __syncthreads();
+    if (d == 0) {
+      if (prot >= a.keep) {
+        cut = 0xFFFFFFFFu;
+        break;
+      }
+      ties -= prot;
+    }
+    const int b1 = BINS - 1 - 2 * threadIdx.x, n1 = hist[b1], n0 = hist[b1 - 1];
+    hist[b1] = hist[b1 - 1] = 0;
+    find_digit(n1, n0, ties, tmp[d], found[d]);
+    cut |= (uint32_t)found[d][0] << g.low;
+    ties = found[d][1];
   }
-  if (j >= min(n, a.keep)) return;
-  const int from = a.src[sh * a.keep + j];
+  emit<false>(sl, a, sh, cut, ties, 0, 0, 0, tmp, a.moves + sh);
+}
+
+// More slots: chunks of them a workgroup each, which never reach over `keep`. Three kernels count a digit each and hand the counts
+// on; each begins with the sum of the former's over the chunks.
+struct Chunk {
+  int c, n, begin, end;
+  long sh;
+  __device__ __forceinline__ Chunk(const EvictArgs& a, int s) {
+    c = blockIdx.x % a.chunks;
+    sh = (long)s * a.kv.hkv + blockIdx.x / a.chunks;
+    n = slots_of(a, s);
+    const long b = c < a.chunks_lo ? (long)c * a.chunk : a.keep + (long)(c - a.chunks_lo) * a.chunk;
+    begin = (int)min(b, (long)n);
+    end = (int)min(b + a.chunk, (long)(c < a.chunks_lo ? a.keep : n));
+    end = max(end, begin);
+  }
+};
+template <int D>
+__global__ __launch_bounds__(NT) void k_digit(EvictArgs a) {
+  __shared__ int hist[BINS];
+  __shared__ int tmp[NT / 64], prot, found[2], more;
+  const int s = blockIdx.y, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
+  const Chunk ch(a, s);
+  const long sh = ch.sh, at = sh * a.chunks + ch.c;
+  if (ch.n <= a.keep) {
+    if (D == 0) keep_all(a, sh, ch.c * NT + threadIdx.x, a.chunks * NT);
+    return;
+  }
+  EvictFound* state = a.found + sh * 3;
+  uint32_t cut = 0;
+  int need = a.keep;
+  hist[threadIdx.x] = hist[threadIdx.x + NT] = 0;
+  if (threadIdx.x == 0) prot = more = 0;
+  __syncthreads();
+  const int b1 = BINS - 1 - 2 * threadIdx.x;
+  if constexpr (D > 0) {
+    // the digit before this one, from the counts of all chunks; and how many of this chunk's keys lie over it
+    const int* before = a.hist + ((long)(D - 1) * a.kv.hkv * a.S + sh) * a.chunks * BINS;
+    int n1 = 0, n0 = 0;
+    for (int c = 0; c < a.chunks; ++c) {
+      const int2 v = *reinterpret_cast<const int2*>(before + (long)c * BINS + b1 - 1);
+      n0 += v.x;
+      n1 += v.y;
+    }
+    if (D == 1) {
+      if (l < 64) {
+        int p = 0;
+        for (int c = l; c < a.chunks; c += 64) p += a.tops[sh * a.chunks + c];
+        need -= __builtin_amdgcn_readlane(wave_scan(p), 63);
+      }
+    } else {
+      cut = state[D - 2].cut;
+      need = state[D - 2].ties;
+    }
+    const bool full = D == 1 ? need <= 0 : cut == 0xFFFFFFFFu;       // protected tokens alone take every place
+    if (full) {
+      cut = 0xFFFFFFFFu;
+      need = a.keep;
+    } else {
+      find_digit(n1, n0, need, tmp, found);
+      cut |= (uint32_t)found[0] << Digit(D - 1, 0).low;
+      need = found[1];
+      const int2 v = *reinterpret_cast<const int2*>(before + (long)ch.c * BINS + b1 - 1);
+      const int mine = (b1 > found[0] ? v.y : 0) + (b1 - 1 > found[0] ? v.x : 0), sum = wave_scan(mine);
+      if (l == 63 && sum) atomicAdd(&more, sum);
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+      a.over[at] = full ? 0 : (D == 1 ? a.tops[at] : a.over[at]) + more;
+      if (ch.c == 0) state[D - 1] = {cut, need};
+    }
+    if (full) return;
+  }
+  const Digit g(D, cut);
+  Slots<true> sl;
+  sl.steps = (ch.end - ch.begin + NT - 1) / NT;
+  sl.j0 = ch.begin + w * sl.steps * 64 + l;
+  sl.end = ch.end;
+  sl.kept = a.keys + sh * a.W;
+  int tops = 0, ones = 0;
+  if constexpr (D == 0) {
+    const Keys key = keys_of(a, s, sh);
+    uint32_t* kept = a.keys + sh * a.W;
+    for (int i0 = 0; i0 < sl.steps; i0 += REGS) {
+#pragma unroll
+      for (int i = 0; i < REGS; ++i) sl.k[i] = key(min(sl.j0 + (i0 + i) * 64, ch.end - 1));
+#pragma unroll
+      for (int i = 0; i < REGS; ++i) {
+        const int j = sl.j0 + (i0 + i) * 64;
+        const bool in = i0 + i < sl.steps && j < ch.end;
+        if (in) kept[j] = sl.k[i];
+        if (i0 + i < sl.steps) g.count(hist, sl.k[i], in, tops, ones);
+      }
+    }
+  } else if (ch.end > ch.begin) {
+    sl.each([&](int, uint32_t x, bool in) { g.count(hist, x, in, tops, ones); });
+  }
+  if (l == 0 && ones) atomicAdd(&hist[g.of_ones()], ones);
+  if (D == 0 && l == 0 && tops) atomicAdd(&prot, tops);
+  __syncthreads();
+  int* out = a.hist + ((long)D * a.kv.hkv * a.S * a.chunks + at) * BINS;
+  *reinterpret_cast<int2*>(out + b1 - 1) = make_int2(hist[b1 - 1], hist[b1]);
+  if (D == 0 && threadIdx.x == 0) a.tops[at] = prot;
+}
+__global__ __launch_bounds__(NT) void k_emit(EvictArgs a) {
+  __shared__ int tmp[3][NT / 64], found[2], over[EVICT_CHUNKS], eq[EVICT_CHUNKS], start[3];
+  const int s = blockIdx.y, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
+  const Chunk ch(a, s);
+  const long sh = ch.sh;
+  if (ch.n <= a.keep) return;
+  uint32_t cut = a.found[sh * 3 + 1].cut;
+  int ties = a.found[sh * 3 + 1].ties;
+  const bool full = cut == 0xFFFFFFFFu;            // then the protected ones are the ties
+  const int* before = a.hist + ((long)2 * a.kv.hkv * a.S + sh) * a.chunks * BINS;
+  const int b1 = BINS - 1 - 2 * threadIdx.x;
+  for (int c = threadIdx.x; c < a.chunks; c += NT) {
+    over[c] = full ? 0 : a.over[sh * a.chunks + c];
+    eq[c] = full ? a.tops[sh * a.chunks + c] : 0;
+  }
+  __syncthreads();
+  if (!full) {
+    int n1 = 0, n0 = 0;
+    for (int c = 0; c < a.chunks; ++c) {
+      const int2 v = *reinterpret_cast<const int2*>(before + (long)c * BINS + b1 - 1);
+      n0 += v.x;
+      n1 += v.y;
+    }
+    find_digit(n1, n0, ties, tmp[0], found);
+    cut |= (uint32_t)found[0];
+    ties = found[1];
+    for (int c = 0; c < a.chunks; ++c) {
+      const int2 v = *reinterpret_cast<const int2*>(before + (long)c * BINS + b1 - 1);
+      const int sum = wave_scan((b1 > found[0] ? v.y : 0) + (b1 - 1 > found[0] ? v.x : 0));
+      if (l == 63 && sum) atomicAdd(&over[c], sum);
+      if (b1 == found[0]) eq[c] = v.y;
+      if (b1 - 1 == found[0]) eq[c] = v.x;
+    }
+    __syncthreads();
+  }
+  // where this chunk's ties, movers and holes begin
+  if (threadIdx.x == 0) {
+    int rank = 0, m = 0, h = 0;
+    for (int c = 0; c < a.chunks; ++c) {
+      if (c == ch.c) start[0] = rank, start[1] = m, start[2] = h;
+      const int stay = over[c] + min(eq[c], max(0, ties - rank));
+      rank += eq[c];
+      if (c < a.chunks_lo) h += min(a.chunk, a.keep - c * a.chunk) - stay;
+      else m += stay;
+    }
+    if (ch.c == 0) a.moves[sh] = m;
+  }
+  __syncthreads();
+  Slots<true> sl;
+  sl.steps = (ch.end - ch.begin + NT - 1) / NT;
+  sl.j0 = ch.begin + w * sl.steps * 64 + l;
+  sl.end = ch.end;
+  sl.kept = a.keys + sh * a.W;
+  if (ch.end > ch.begin) emit<true>(sl, a, sh, cut, ties, start[0], start[1], start[2], tmp, nullptr);
+}
+
+// The moves, `rest` workgroups a sequence and head: LPR lanes a row, 16 bytes each of K and V; its scales, weight and position.
+// Behind them workgroups for the weights and positions of tokens that stay where they are, a thread a slot, and the lengths.
+template <int LPR>
+__global__ __launch_bounds__(256) void k_move(EvictArgs a, int eb, int rest) {
+  const int hk = blockIdx.x % a.kv.hkv, s = blockIdx.x / a.kv.hkv % a.S, g = blockIdx.x / a.kv.hkv / a.S;
+  const long sh = (long)s * a.kv.hkv + hk;
+  if (g >= rest) {
+    const int j = (g - rest) * 256 + threadIdx.x, old = a.len[s], n = slots_of(a, s);
+    // (lengths may be updated in place while other workgroups read them: n, cut off at keep, is the same before and after)
+    if (j == 0 && hk == 0) a.len_out[s] = n > a.keep ? a.keep : old;
+    if (j >= min(n, a.keep) || a.src[sh * a.keep + j] != j) return;
+    if (a.mass_out != a.mass) a.mass_out[sh * a.W + j] = a.mass[sh * a.W + j];
+    if (a.pos_out != a.pos) a.pos_out[sh * a.W + j] = a.pos[sh * a.W + j];
+    return;
+  }
+  const int lane = threadIdx.x % LPR, i = g * (256 / LPR) + threadIdx.x / LPR;
+  if (i >= a.moves[sh]) return;
+  const int f = a.from[sh * a.keep + i], t = a.to[sh * a.keep + i];
   if (lane == 0) {
-    if (from != j || a.mass_out != a.mass) a.mass_out[sh * a.W + j] = a.mass[sh * a.W + from];
-    if (from != j || a.pos_out != a.pos) a.pos_out[sh * a.W + j] = a.pos[sh * a.W + from];
+    a.src[sh * a.keep + t] = f;
+    a.mass_out[sh * a.W + t] = a.mass[sh * a.W + f];
+    a.pos_out[sh * a.W + t] = a.pos[sh * a.W + f];
   }
-  if (from == j) return;
   const int* trow = a.table + (long)s * a.ldt;
-  const int mask = (1 << a.kv.psh) - 1, pf = trow[from >> a.kv.psh], pt = trow[j >> a.kv.psh];
+  const int mask = (1 << a.kv.psh) - 1, pf = trow[f >> a.kv.psh], pt = trow[t >> a.kv.psh];
   if ((unsigned)pf >= (unsigned)a.kv.n_pages || (unsigned)pt >= (unsigned)a.kv.n_pages) return;
-  const long rf = (((long)pf * a.kv.hkv + hk) << a.kv.psh) + (from & mask), rt = (((long)pt * a.kv.hkv + hk) << a.kv.psh) + (j & mask);
+  const long rf = (((long)pf * a.kv.hkv + hk) << a.kv.psh) + (f & mask), rt = (((long)pt * a.kv.hkv + hk) << a.kv.psh) + (t & mask);
   const int row = a.kv.d * eb;
   if (lane * 16 < row) {
     const uint4 k = *reinterpret_cast<const uint4*>(a.kv.k + rf * row + lane * 16);
@@ -177,19 +404,25 @@ __global__ __launch_bounds__(256) void k_move(EvictArgs a, int eb, int groups) {
 }  // namespace
 
 hipError_t sffn_launch_evict(const EvictArgs& a, int kvt, hipStream_t st) {
-  const dim3 grid(a.kv.hkv, a.S);
   const int most = a.W < a.cols << a.kv.psh ? a.W : a.cols << a.kv.psh;
-  if (most <= 8 * NT) hipLaunchKernelGGL(k_select<8>, grid, dim3(NT), 0, st, a);
-  else if (most <= 64 * NT) hipLaunchKernelGGL(k_select<64>, grid, dim3(NT), 0, st, a);
-  else hipLaunchKernelGGL(k_select<0>, grid, dim3(NT), 0, st, a);
+  if (a.chunks == 0) hipLaunchKernelGGL(k_select, dim3(a.kv.hkv, a.S), dim3(NT), 0, st, a);
+  else {
+    const dim3 grid(a.chunks * a.kv.hkv, a.S);
+    hipLaunchKernelGGL(k_digit<0>, grid, dim3(NT), 0, st, a);
+    hipLaunchKernelGGL(k_digit<1>, grid, dim3(NT), 0, st, a);
+    hipLaunchKernelGGL(k_digit<2>, grid, dim3(NT), 0, st, a);
+    hipLaunchKernelGGL(k_emit, grid, dim3(NT), 0, st, a);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int eb = kvt == T_I8 || kvt == T_E4M3 ? 1 : 2, row = a.kv.d * eb;
-  const int lpr = row <= 64 ? 4 : row <= 128 ? 8 : row <= 256 ? 16 : 32, groups = (a.keep + 256 / lpr - 1) / (256 / lpr);
+  // at most as many rows move as there are slots on either side of `keep`
+  const int lpr = row <= 64 ? 4 : row <= 128 ? 8 : row <= 256 ? 16 : 32, rows = most - a.keep < a.keep ? most - a.keep : a.keep;
+  const int rest = rows > 0 ? (rows + 256 / lpr - 1) / (256 / lpr) : 0, groups = rest + (a.keep + 255) / 256;
   const dim3 moves((unsigned)groups * a.kv.hkv * a.S);
-  if (lpr == 4) hipLaunchKernelGGL(k_move<4>, moves, dim3(256), 0, st, a, eb, groups);
-  else if (lpr == 8) hipLaunchKernelGGL(k_move<8>, moves, dim3(256), 0, st, a, eb, groups);
-  else if (lpr == 16) hipLaunchKernelGGL(k_move<16>, moves, dim3(256), 0, st, a, eb, groups);
-  else hipLaunchKernelGGL(k_move<32>, moves, dim3(256), 0, st, a, eb, groups);
+  if (lpr == 4) hipLaunchKernelGGL(k_move<4>, moves, dim3(256), 0, st, a, eb, rest);
+  else if (lpr == 8) hipLaunchKernelGGL(k_move<8>, moves, dim3(256), 0, st, a, eb, rest);
+  else if (lpr == 16) hipLaunchKernelGGL(k_move<16>, moves, dim3(256), 0, st, a, eb, rest);
+  else hipLaunchKernelGGL(k_move<32>, moves, dim3(256), 0, st, a, eb, rest);
   return hipGetLastError();
 }

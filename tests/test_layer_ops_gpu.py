@@ -375,7 +375,7 @@ def test_mass_after_attn(gpu_ready):
 EVICT = [([40, 16, 7], 16, 4, 2, 1, 16, 16, "f16"), ([1100, 1024, 1025, 30], 1024, 256, 4, 8, 128, 16, "f16"),
          ([300], 1, 0, 0, 2, 64, 32, "i8"), ([300, 299], 100, 1, 0, 3, 80, 16, "e4m3"), ([5000], 4999, 0, 0, 1, 32, 64, "bf16"),
          ([9000, 8193], 3000, 500, 16, 2, 48, 128, "i8"), ([70000], 30000, 1000, 4, 1, 16, 1024, "f16"), ([64] * 20, 32, 8, 0, 2, 256, 16, "e4m3"),
-         ([200], 200, 50, 4, 1, 24, 16, "f16"), ([130], 129, 64, 65, 2, 112, 16, "i8")]
+         ([600000], 250000, 70000, 5, 1, 16, 1024, "i8"), ([20000, 8200, 9000], 8500, 8000, 500, 2, 16, 64, "f16"), ([200], 200, 50, 4, 1, 24, 16, "f16"), ([130], 129, 64, 65, 2, 112, 16, "i8")]
 
 
 def evict_case(ks, keep, Hkv, d, page, kvt, seed=0, kind="mixed", extra=0):
@@ -457,6 +457,15 @@ def test_evict_odd(gpu_ready):
         check_evict(gpu_ready, b, W, m, pos, plen, 90, 3, 20, False)
         check_evict(gpu_ready, b, W, m, torch.zeros_like(pos), plen, 90, 3, 20, False)             # everything protected
         check_evict(gpu_ready, b, W, m, pos, plen, 90, 0, 0, True)
+    for kind in ("odd", "zero"):                                                                   # the same over several workgroups
+        b, W, m, pos, plen = evict_case([17000, 9000, 100], 8300, 1, 16, 256, "i8", seed=6, kind=kind)
+        say(f"[evict odd long {kind}]")
+        check_evict(gpu_ready, b, W, m, pos, plen, 8300, 3, 20, False)
+        check_evict(gpu_ready, b, W, m, torch.zeros_like(pos), plen, 8300, 3, 20, True)
+        b.table[0, 40:44], b.table[0, 3] = -1, b.n_pages
+        check_evict(gpu_ready, b, W, m, pos, plen, 8300, 0, 0, False)
+        check_evict(gpu_ready, b, W, m, pos, plen, 100, 0, 0, False)
+    b, W, m, pos, plen = evict_case([250, 100, 260], 90, 2, 32, 16, "i8", seed=5, kind="mixed")
     b.table[0, 2], b.table[0, 12], b.table[2, 0] = -1, b.n_pages, 1 << 30
     check_evict(gpu_ready, b, W, m, pos, plen, 90, 3, 20, False)
     b.kv_len = torch.tensor([100000, -5, 0], dtype=torch.int32)
