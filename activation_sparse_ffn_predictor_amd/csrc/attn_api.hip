@@ -155,7 +155,10 @@ MassPlan mass_plan(int S, int Hkv, int G, int d, int max_q, int max_kv, int W) {
   const int64_t keys = std::max(1, std::min(max_kv, W)), rows = (int64_t)max_q * G, seqs = (int64_t)S * Hkv;
   MassPlan p{1, 1, 0};
   if (sffn::mass_few(rows, d)) {
-    p.tiles = (int)std::max<int64_t>(1, std::min((keys + 127) / 128, (2048 + seqs - 1) / seqs));
+    // Workgroups of 1024 keys, eight units a wave; of fewer where that leaves places free (32 sequences to 6000 tokens on 40 heads,
+    // int8: of 512 keys 105 us, 1024 101, 2048 105)
+    p.tiles = (int)std::min((keys + 127) / 128, std::max((keys + 1023) / 1024, (2048 + seqs - 1) / seqs));
+    p.tiles = std::max(1, std::min(p.tiles, (1 << 22) / (int)seqs));
     return p;
   }
   const int tile = sffn::mass_tile(d);

@@ -105,32 +105,38 @@ __global__ __launch_bounds__(256) void k_mass_few(MassArgs a) {
   const uint32_t dB = (uint32_t)d * EB, ko = (uint32_t)ql * dB + g4 * 16;
   const int units = (m.keys + 31) >> 5, step = gridDim.x * 4;
 
-  uint4 kr[2][KL];
-  float ksc[2];
-  int have[2];
-  float old = 0.f;
+  struct Unit {
+    uint4 kr[2][KL];
+    float ksc[2], old;
+    int have[2];
+  };
   auto visible = [&](int u) { return some_seen(a, m.q.p0, m.p1, u * 32, u * 32 + 31); };
-  auto load = [&](int u) {
+  // page ids are read a unit ahead of the loads that need them, which would wait for everything on its way otherwise
+  int page[2];
+  auto pages = [&](int u) {
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) page[kb] = trow[min((u * 32 + kb * 16) >> a.kv.psh, a.sq.cols - 1)];
+  };
+  auto load = [&](int u, const int (&pg)[2], Unit& x) {
     const int t0 = u * 32;
-    if (l < 32 && t0 + l < m.keys) old = a.mass[base + t0 + l];
+    x.old = 0.f;
+    if (l < 32 && t0 + l < m.keys) x.old = a.mass[base + t0 + l];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      const int t = t0 + kb * 16, pid = __builtin_amdgcn_readfirstlane(trow[min(t >> a.kv.psh, a.sq.cols - 1)]);
-      have[kb] = visible(u) && (unsigned)pid < (unsigned)a.kv.n_pages ? min(16, max(0, m.q.len - t)) : 0;
-      const long r = (((long)(have[kb] ? pid : 0) * a.kv.hkv + hk) << a.kv.psh) + (t & ((1 << a.kv.psh) - 1));
-      const Buf bk(a.kv.k + r * dB, have[kb] * dB);
+      const int t = t0 + kb * 16, pid = __builtin_amdgcn_readfirstlane(pg[kb]);
+      x.have[kb] = visible(u) && (unsigned)pid < (unsigned)a.kv.n_pages ? min(16, max(0, m.q.len - t)) : 0;
+      const long r = (((long)(x.have[kb] ? pid : 0) * a.kv.hkv + hk) << a.kv.psh) + (t & ((1 << a.kv.psh) - 1));
+      const Buf bk(a.kv.k + r * dB, x.have[kb] * dB);
 #pragma unroll
-      for (int i = 0; i < KL; ++i) kr[kb][i] = bk.ld16(boff((uint32_t)((i * 4 + g4) * 16) < dB, ko + i * 64));
-      if constexpr (C8) ksc[kb] = Buf(a.kv.ks + r, have[kb] * 4).ldf(ql * 4);
+      for (int i = 0; i < KL; ++i) x.kr[kb][i] = bk.ld16(boff((uint32_t)((i * 4 + g4) * 16) < dB, ko + i * 64));
+      if constexpr (C8) x.ksc[kb] = Buf(a.kv.ks + r, x.have[kb] * 4).ldf(ql * 4);
     }
   };
-  int u = blockIdx.x * 4 + w;
-  if (u < units) load(u);
-  for (; u < units; u += step) {
-    const int t0 = u * 32, h0 = have[0], h1 = have[1];
-    const float before = old;
+  auto work = [&](int u, const Unit& now) {
+    const int t0 = u * 32, h0 = now.have[0], h1 = now.have[1];
     float sum[2] = {0.f, 0.f};
-    if (visible(u)) {
+    const bool some = visible(u);
+    if (some) {
       f32x4 sc[QB][2];
 #pragma unroll
       for (int qb = 0; qb < QB; ++qb)
@@ -141,7 +147,7 @@ __global__ __launch_bounds__(256) void k_mass_few(MassArgs a) {
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
           if constexpr (C8) {
-            const uint4 t = kr[kb][i];
+            const uint4 t = now.kr[kb][i];
             const uint2 x0 = codes4<KVM == 2>(t.x), x1 = codes4<KVM == 2>(t.y), x2 = codes4<KVM == 2>(t.z), x3 = codes4<KVM == 2>(t.w);
             const uint4 ka = make_uint4(x0.x, x0.y, x1.x, x1.y), kc = make_uint4(x2.x, x2.y, x3.x, x3.y);
 #pragma unroll
@@ -151,28 +157,48 @@ __global__ __launch_bounds__(256) void k_mass_few(MassArgs a) {
             }
           } else {
 #pragma unroll
-            for (int qb = 0; qb < QB; ++qb) sc[qb][kb] = mfma16<CB>(qf[qb][i], kr[kb][i], sc[qb][kb]);
+            for (int qb = 0; qb < QB; ++qb) sc[qb][kb] = mfma16<CB>(qf[qb][i], now.kr[kb][i], sc[qb][kb]);
           }
         }
-      const float f0 = C8 ? ksc[0] * c : c, f1 = C8 ? ksc[1] * c : c;
-      __builtin_amdgcn_sched_barrier(0);
-      if (u + step < units) load(u + step);          // the next unit's loads run under the exponentials
+      // most units are seen whole by every row: then rows alone decide
+      const bool full = h0 + h1 == 32 && all_seen(a, m.q.p0, m.p1, t0, t0 + 31);
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
+        const float f = C8 ? now.ksc[kb] * c : c;
         const int j = t0 + kb * 16 + ql;
         const bool held = ql < (kb ? h1 : h0);
 #pragma unroll
         for (int qb = 0; qb < QB; ++qb)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float x = exp2_fast(fmaf(sc[qb][kb][e], kb ? f1 : f0, -L[qb][e]));
-            sum[kb] += (held & seen(a, pr[qb][e], j)) ? x : 0.f;
+            const float x = exp2_fast(fmaf(sc[qb][kb][e], f, -L[qb][e]));
+            bool see = pr[qb][e] >= 0;
+            if (!full) see = held & seen(a, pr[qb][e], j);
+            sum[kb] += see ? x : 0.f;
           }
         sum[kb] = over32<false>(over16<false>(sum[kb]));
       }
-    } else if (u + step < units) load(u + step);
+    }
     const int j = t0 + l;
-    if (l < 32 && j < m.keys && (copy || j >= m.q.p0 || visible(u))) give(a, m, base, j, before, l < 16 ? sum[0] : sum[1]);
+    if (l < 32 && j < m.keys && (copy || j >= m.q.p0 || some)) give(a, m, base, j, now.old, l < 16 ? sum[0] : sum[1]);
+  };
+  // a unit's loads are on their way while the one before it is worked on; two turns in one, so that nothing is copied
+  int u = blockIdx.x * 4 + w;
+  if (u >= units) return;
+  auto fetch = [&](int v, Unit& x) {
+    if (v >= units) return;
+    const int pg[2] = {page[0], page[1]};
+    pages(v + step);
+    load(v, pg, x);
+  };
+  Unit x0, x1;
+  pages(u);
+  fetch(u, x0);
+  for (; u < units; u += 2 * step) {
+    fetch(u + step, x1);
+    work(u, x0);
+    fetch(u + 2 * step, x0);
+    if (u + step < units) work(u + step, x1);
   }
 }
 
@@ -182,7 +208,7 @@ __global__ __launch_bounds__(256) void k_mass_few(MassArgs a) {
 // until the rows are through; 32 lanes are joined once. 8-bit codes are widened once, exactly, to the queries' type.
 constexpr int MROWS = 64;
 template <bool BF, int KVM, int DP, int KT>
-__global__ __launch_bounds__(256) void k_mass_many(MassArgs a) {
+__global__ __launch_bounds__(256, 2) void k_mass_many(MassArgs a) {
   constexpr bool C8 = KVM != 0;
   constexpr int KS = DP / 16, CPR = DP / 8, RB = DP * 2, WG = 4 * KT * 32, LOADS = MROWS * CPR / 256;
   __shared__ __align__(16) char qs[2][MROWS * RB];
@@ -310,11 +336,18 @@ __global__ __launch_bounds__(256) void k_mass_many(MassArgs a) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) sum[x][i] += exp2_fast(fmaf(sc[x][i], f[x][i], -L));
           } else if (some_seen(a, pa, pb, ka, ka + 31)) {
+            // this lane's row sees its keys up to `last`, from `from` on or before `sink`, where they are held (the numbers are hidden
+            // from the compiler, which would keep 32 comparisons' results over the loop)
+            int last = p - ka - 4 * hi, from = last - a.window, sink = a.sinks - ka - 4 * hi;
+            if (a.window <= 0) from = -1000;
+            uint32_t have = held[x] >> (4 * hi);
+            asm volatile("" : "+v"(last), "+v"(from), "+v"(sink), "+v"(have));
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const int kk = 8 * (i >> 2) + 4 * hi + (i & 3);
+              const int kk = 8 * (i >> 2) + (i & 3);
               const float e = exp2_fast(fmaf(sc[x][i], f[x][i], -L));
-              sum[x][i] += (((held[x] >> kk) & 1) && seen(a, p, ka + kk)) ? e : 0.f;
+              const bool see = (kk <= last) & ((kk > from) | (kk < sink)) & (((have >> kk) & 1) != 0);
+              sum[x][i] += see ? e : 0.f;
             }
           }
         }
