@@ -276,27 +276,44 @@ __global__ __launch_bounds__(256, 2) void k_mass_many(MassArgs a) {
       n_t = min(n_t, t_0 + per);
     }
 
+    // A thread's rows of a tile, and of its statistics: token and query head of each are kept and moved on a tile at a time
+    constexpr int RPL = 256 / CPR;                   // rows a load of the workgroup covers
+    const int ch = threadIdx.x % CPR, row = threadIdx.x / CPR, r_0 = r0 + t_0 * MROWS, step_i = MROWS / G, step_g = MROWS - step_i * G;
+    int ti[LOADS], tg[LOADS], si = (r_0 + (int)(threadIdx.x % MROWS)) / G, sg = r_0 + threadIdx.x % MROWS - si * G, left = r1 - r_0;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      ti[i] = (r_0 + i * RPL + row) / G;
+      tg[i] = r_0 + i * RPL + row - ti[i] * G;
+    }
+    const char* qb = a.q + ((long)m.q.q0 * a.ldq + (long)hk * G * d) * 2 + ch * 16;
+    const float* lb = a.lse + (long)m.q.q0 * a.hq + hk * G;
+    auto on = [&](int& i, int& g) {
+      g += step_g;
+      i += step_i + (g >= G);
+      g -= g >= G ? G : 0;
+    };
     uint4 st[LOADS];
     float sl = 0.f;
     int sp = 0;
-    auto fetch = [&](int t) {
+    auto fetch = [&] {                               // the next tile's
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) {
-        const int row = (i * 256 + threadIdx.x) / CPR, ch = threadIdx.x % CPR, r = r0 + t * MROWS + row, ii = r / G;
-        st[i] = r < r1 && ch * 8 < d ? *reinterpret_cast<const uint4*>(a.q + ((long)(m.q.q0 + ii) * a.ldq + (long)(hk * G + r - ii * G) * d) * 2 + ch * 16)
-                                     : make_uint4(0, 0, 0, 0);
+        st[i] = make_uint4(0, 0, 0, 0);
+        if (i * RPL + row < left && ch * 8 < d) st[i] = *reinterpret_cast<const uint4*>(qb + (long)ti[i] * (a.ldq * 2) + tg[i] * d * 2);
+        on(ti[i], tg[i]);
       }
       if (threadIdx.x < MROWS) {
-        const int r = r0 + t * MROWS + threadIdx.x, ii = r / G;
-        sl = r < r1 ? a.lse[(long)(m.q.q0 + ii) * a.hq + hk * G + r - ii * G] : -INFINITY;
-        sp = sl == -INFINITY ? -1 : m.q.p0 + ii;
+        sl = (int)threadIdx.x < left ? lb[(long)si * a.hq + sg] : -INFINITY;
+        sp = sl == -INFINITY ? -1 : m.q.p0 + si;
+        on(si, sg);
       }
+      left -= MROWS;
     };
     auto put = [&](int b) {
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) {
-        const int row = (i * 256 + threadIdx.x) / CPR, ch = threadIdx.x % CPR;
-        *reinterpret_cast<uint4*>(qs[b] + row * RB + ((ch ^ (row & (CPR - 1))) << 4)) = st[i];
+        const int to = i * RPL + row;
+        *reinterpret_cast<uint4*>(qs[b] + to * RB + ((ch ^ (to & (CPR - 1))) << 4)) = st[i];
       }
       if (threadIdx.x < MROWS) {
         Ls[b][threadIdx.x] = sl * LOG2E;
@@ -304,14 +321,14 @@ __global__ __launch_bounds__(256, 2) void k_mass_many(MassArgs a) {
       }
     };
     if (t_0 < n_t) {
-      fetch(t_0);
+      fetch();
       __syncthreads();                               // (a former tile's readers are through)
       put(0);
     }
     for (int t = t_0; t < n_t; ++t) {
       const int b = (t - t_0) & 1;
       __syncthreads();
-      if (t + 1 < n_t) fetch(t + 1);
+      if (t + 1 < n_t) fetch();
 #pragma unroll
       for (int h = 0; h < MROWS / 32; ++h) {
         const int row = h * 32 + lc;
