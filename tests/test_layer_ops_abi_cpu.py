@@ -1,0 +1,191 @@
+"""Refusals of the block quantisation, 8-bit product, head norms with rotation, attention mass and eviction: bad arguments are
+turned away on the host before anything is enqueued (fake pointers that are never followed), and the binding checks what the
+C ABI cannot see. No GPU."""
+import math
+
+import pytest
+import torch
+
+from activation_sparse_ffn_predictor_amd import _lib
+from test_attention_abi_cpu import CACHE_BAD, SEQ_BAD, kv, sq
+
+A = 0x10000
+LAST = "the tensors must be on the GPU"
+
+
+def call(fn, args, kw):
+    a = dict(args)
+    for k in kw:
+        assert k in a, k
+    a.update(kw)
+    rc = getattr(_lib.lib(), fn)(*a.values())
+    assert (rc == 0) == (_lib.lib().sffn_last_error().decode() == "")
+    return rc
+
+
+QUANT = dict(xt=0, x=A, ldx=256, T=3, D=256, rows=1, y=2 * A, ldy=256, scale=3 * A, stream=None)
+MM = dict(a=A, lda=256, sa=2 * A, b=3 * A, ldb=256, sb=4 * A, T=3, N=64, K=256, ot=1, out=5 * A, ldo=64, ws=None, ws_bytes=0, stream=None)
+ROPE = dict(type=1, cu=A, len=A, S=2, T=5, q=2 * A, ldq=512, Hq=8, k=3 * A, ldk=128, Hk=2, d=64, norm=1, wq=A, wk=A, eps=1e-6, freq=A,
+            rot=64, inter=0, qo=4 * A, ldqo=512, ko=5 * A, ldko=128, stream=None)
+MASS = dict(cache=None, seqs=None, plen=A, type=1, q=A, ldq=512, Hq=8, max_q=4, max_kv=40, scale=0.1, window=0, sinks=0, lse=A, mass=2 * A,
+            out=2 * A, pos=3 * A, W=48, ws=None, ws_bytes=0, stream=None)
+EVICT = dict(cache=None, len=A, plen=2 * A, table=3 * A, S=2, cols=3, ldt=3, mass=4 * A, pos=5 * A, W=48, keep=32, sinks=4, recent=8, src=6 * A,
+             mass_out=4 * A, pos_out=5 * A, len_out=A, ws=7 * A, ws_bytes=1 << 20, stream=None)
+
+
+@pytest.mark.parametrize("kw,st", [
+    (dict(xt=3), 6), (dict(rows=0), 6), (dict(rows=64), 6), (dict(T=-1), 2), (dict(T=(1 << 24) + 1), 2), (dict(D=4), 2), (dict(D=252), 2),
+    (dict(D=65544, ldx=65544, ldy=65544), 2), (dict(x=None), 1), (dict(y=None), 1), (dict(scale=None), 1), (dict(ldx=248), 2), (dict(ldy=260), 2),
+    (dict(x=A + 8), 3), (dict(y=2 * A + 8), 3), (dict(scale=3 * A + 2), 3), (dict(y=A), 6), (dict(scale=A), 6), (dict(scale=2 * A), 6),
+    (dict(T=0, x=None, y=None), 0)])
+def test_quant_rejects(kw, st):
+    assert call("sffn_quant128", QUANT, kw) == st
+
+
+@pytest.mark.parametrize("kw,st", [
+    (dict(ot=3), 6), (dict(T=-1), 2), (dict(T=(1 << 24) + 1), 2), (dict(N=4), 2), (dict(N=60), 2), (dict(N=(1 << 22) + 8), 2), (dict(K=8), 2),
+    (dict(K=248), 2), (dict(K=65552), 2), (dict(T=1 << 24, N=1 << 21, ldo=1 << 21), 2), (dict(a=None), 1), (dict(b=None), 1), (dict(out=None), 1),
+    (dict(sa=None), 1), (dict(sb=None), 1), (dict(lda=240), 2), (dict(lda=264), 2), (dict(ldb=264), 2), (dict(ldo=60), 2),
+    (dict(lda=(1 << 22) + 16), 2), (dict(ldb=(1 << 22) + 16), 2), (dict(a=A + 8), 3), (dict(b=A + 8), 3), (dict(out=A + 8), 3), (dict(sa=A + 2), 3),
+    (dict(sb=A + 1), 3), (dict(out=A), 6), (dict(out=2 * A), 6), (dict(out=3 * A), 6), (dict(T=64, N=1024, ldo=1024, K=8192, lda=8192, ldb=8192), 1),
+    (dict(T=64, N=1024, ldo=1024, K=8192, lda=8192, ldb=8192, ws=6 * A + 16, ws_bytes=1 << 30), 3),
+    (dict(T=64, N=1024, ldo=1024, K=8192, lda=8192, ldb=8192, ws=6 * A, ws_bytes=1024), 4), (dict(T=0, a=None, b=None, out=None), 0)])
+def test_mm_rejects(kw, st):
+    assert call("sffn_mm_e4m3", MM, kw) == st
+
+
+def test_mm_workspace():
+    ws = _lib.mm_workspace_size
+    assert ws(1, 4096, 4096) == 0 and ws(4096, 10240, 8192) == 0
+    a = ws(64, 1024, 8192)
+    assert a > 0 and a % 256 == 0 and a % (64 * 1024 * 4) == 0
+    assert ws(0, 64, 256) == 0 and ws(3, 60, 256) == 0 and ws(3, 64, 250) == 0 and ws(1 << 25, 64, 256) == 0
+
+
+@pytest.mark.parametrize("kw,st", [
+    (dict(type=0), 6), (dict(type=3), 6), (dict(cu=None), 1), (dict(len=None), 1), (dict(S=0), 2), (dict(S=65536), 2), (dict(T=-1), 2),
+    (dict(T=(1 << 24) + 1), 2), (dict(d=4), 2), (dict(d=60), 2), (dict(d=264), 2), (dict(rot=-8), 2), (dict(rot=72), 2), (dict(rot=12), 2),
+    (dict(Hq=0), 2), (dict(Hk=0), 2), (dict(Hq=65536), 2), (dict(Hk=65536), 2), (dict(eps=-1.0), 6), (dict(eps=math.nan), 6), (dict(eps=math.inf), 6),
+    (dict(freq=None), 1), (dict(q=None), 1), (dict(qo=None), 1), (dict(ko=None), 1), (dict(ldq=504), 2), (dict(ldq=516), 2), (dict(ldqo=504), 2),
+    (dict(ldk=120), 2), (dict(ldko=132), 2), (dict(q=A + 8), 3), (dict(qo=A + 2), 3), (dict(k=A + 8), 3), (dict(ko=A + 4), 3), (dict(cu=A + 2), 3),
+    (dict(len=A + 1), 3), (dict(wq=A + 2), 3), (dict(wk=A + 2), 3), (dict(freq=A + 2), 3), (dict(qo=2 * A, ldqo=520), 6), (dict(ko=3 * A, ldko=136), 6),
+    (dict(qo=3 * A), 6), (dict(ko=2 * A), 6), (dict(ko=4 * A), 6), (dict(T=0, q=None, qo=None), 0)])
+def test_rope_rejects(kw, st):
+    assert call("sffn_qk_norm_rope", ROPE, kw) == st
+
+
+def test_mass_rejects():
+    def mass(c=None, s=None, **kw):
+        return call("sffn_attn_mass", dict(MASS, cache=c or kv(), seqs=s or sq()), kw)
+    for kw, st in CACHE_BAD:
+        assert mass(c=kv(**kw)) == st, kw
+    for kw, st in SEQ_BAD:
+        assert mass(s=sq(**kw)) == st, kw
+    for kw, st in [(dict(type=0), 6), (dict(plen=None), 1), (dict(mass=None), 1), (dict(out=None), 1), (dict(pos=None), 1), (dict(lse=None), 1),
+                   (dict(q=None), 1), (dict(Hq=7), 2), (dict(Hq=0), 2), (dict(max_q=0), 2), (dict(W=0), 2), (dict(W=1 << 30), 2),
+                   (dict(scale=math.nan), 6), (dict(scale=-math.inf), 6), (dict(window=-1), 6), (dict(sinks=-1), 6), (dict(ldq=504), 2),
+                   (dict(ldq=516), 2), (dict(q=A + 8), 3), (dict(lse=A + 2), 3), (dict(mass=A + 1), 3), (dict(out=A + 2), 3), (dict(pos=A + 2), 3),
+                   (dict(plen=A + 2), 3), (dict(pos=2 * A), 6)]:
+        assert mass(**kw) == st, kw
+    big = dict(max_q=4096, max_kv=4096, W=4096)               # a long prompt's rows are shared out: a workspace is needed
+    assert mass(**big) == 1 and mass(ws=A + 16, ws_bytes=1 << 30, **big) == 3 and mass(ws=A, ws_bytes=64, **big) == 4
+    assert mass(c=kv(n_kv_heads=65), s=sq(S=65535), Hq=65, ldq=4160, W=8) == 2
+    assert mass(s=sq(T=0), q=None, lse=None) == 0
+    ws = _lib.attn_mass_workspace_size
+    assert ws(1, 64, 8, 128, 1, 131072, 131072) == 0 and ws(64, 64, 8, 128, 512, 8192, 8192) == 0
+    assert ws(1, 64, 8, 128, 2048, 6144, 6144) > 0 and ws(1, 63, 8, 128, 2048, 6144, 6144) == 0 and ws(0, 64, 8, 128, 1, 1, 1) == 0
+
+
+def test_evict_rejects():
+    def evict(c=None, **kw):
+        return call("sffn_kv_evict", dict(EVICT, cache=c or kv()), kw)
+    for kw, st in CACHE_BAD:
+        if kw not in (dict(type=0), dict(type=2), dict(type=9)):
+            assert evict(c=kv(**kw)) == st, kw
+    assert evict(c=kv(type=0)) == 6 and evict(c=kv(type=9)) == 6
+    for kw, st in [(dict(len=None), 1), (dict(plen=None), 1), (dict(table=None), 1), (dict(mass=None), 1), (dict(pos=None), 1), (dict(src=None), 1),
+                   (dict(mass_out=None), 1), (dict(pos_out=None), 1), (dict(len_out=None), 1), (dict(S=0), 2), (dict(S=65536), 2), (dict(cols=0), 2),
+                   (dict(cols=1 << 27, ldt=1 << 27), 2), (dict(ldt=2), 2), (dict(W=0), 2), (dict(W=1 << 30), 2), (dict(keep=0), 2), (dict(keep=49), 2),
+                   (dict(sinks=-1), 6), (dict(recent=-1), 6), (dict(sinks=25), 6), (dict(len=A + 2), 3), (dict(plen=A + 2), 3), (dict(table=A + 1), 3),
+                   (dict(mass=A + 2), 3), (dict(src=A + 2), 3), (dict(len_out=A + 2), 3), (dict(src=4 * A), 6), (dict(mass_out=5 * A), 6),
+                   (dict(pos_out=4 * A), 6), (dict(len_out=3 * A), 6), (dict(len_out=2 * A), 6), (dict(plen=A), 6), (dict(ws=None), 1),
+                   (dict(ws=A + 16), 3), (dict(ws_bytes=16), 4)]:
+        assert evict(**kw) == st, kw
+    assert evict(c=kv(n_kv_heads=65), S=65535, W=8, keep=1, sinks=0, recent=0) == 2
+    size = _lib.kv_evict_workspace_size
+    assert size(2, 2, 48, 32) >= 2 * 2 * 32 * 8 and size(2, 2, 48, 49) == 0 and size(0, 2, 48, 1) == 0
+    assert size(1, 8, 40000, 16384) > size(1, 8, 8192, 8192)
+
+
+# ------------------------------------------------------------------------------------------------ the binding
+H, I32, E4 = torch.float16, torch.int32, torch.float8_e4m3fn
+CU, KL, TAB = torch.tensor([0, 1, 3], dtype=I32), torch.tensor([4, 5], dtype=I32), torch.zeros((2, 3), dtype=I32)
+META = torch.device("meta")
+
+
+def refused(f, text, **kw):
+    with pytest.raises(ValueError) as e:
+        f(**kw)
+    assert text in str(e.value), str(e.value)
+
+
+def test_quant_binding():
+    X, Y, S = torch.zeros((3, 256)), torch.zeros((3, 256)).to(E4), torch.zeros((3, 2))
+
+    def f(x=X, y=Y, s=S, rows=1):
+        _lib.quant128(x, y, s, rows=rows)
+    for text, kw in [(LAST, {}), (LAST, dict(rows=128, s=S[:1])), ("x is not a tensor", dict(x=3)), ("x is [rows, D]", dict(x=X[0])),
+                     ("x: this type", dict(x=X.double())), ("y: this type", dict(y=X)), ("rows is 1 or 128", dict(rows=2)), ("y is not [3, 256]", dict(y=Y[:2])),
+                     ("x is not [256, 3] with dense rows", dict(x=X.t(), y=Y.t())), ("scale is contiguous fp32", dict(s=S[:2])),
+                     ("scale is contiguous fp32", dict(s=S.half())), ("scale is contiguous fp32", dict(rows=128)), ("different devices", dict(y=Y.to(META)))]:
+        refused(f, text, **kw)
+
+
+def test_mm_binding():
+    a, b, sa, sb, o = torch.zeros((3, 256)).to(E4), torch.zeros((200, 256)).to(E4), torch.zeros((3, 2)), torch.zeros((2, 2)), torch.zeros((3, 200))
+
+    def f(a=a, sa=sa, b=b, sb=sb, o=o, ws=None):
+        _lib.mm_e4m3(a, sa, b, sb, o, ws)
+    for text, kw in [(LAST, {}), (LAST, dict(ws=torch.zeros(4))), ("a is [tokens, K]", dict(a=a[0])), ("a: this type", dict(a=o)), ("b: this type", dict(b=b.to(H))),
+                     ("out: this type", dict(o=o.double())), ("b is not [200, 128]", dict(a=a[:, :128], sa=sa[:, :1].contiguous())), ("out is not [3, 200]", dict(o=o[:2])),
+                     ("a_scale is contiguous", dict(sa=sa[:, :1])), ("b_scale is contiguous", dict(sb=sb[:1])), ("a_scale is contiguous", dict(sa=sa.t().contiguous().t())),
+                     ("workspace must be contiguous", dict(ws=torch.zeros(8)[::2])), ("different devices", dict(b=b.to(META)))]:
+        refused(f, text, **kw)
+
+
+def test_rope_binding():
+    q, k = torch.zeros((3, 8, 64), dtype=H), torch.zeros((3, 2, 64), dtype=H)
+    w, fr = torch.zeros(64), torch.zeros(32)
+
+    def f(q=q, k=k, wq=w, wk=w, eps=1e-6, cu=CU, ln=KL, fr=fr, qo=q, ko=k):
+        _lib.qk_norm_rope(q, k, wq, wk, eps, cu, ln, fr, qo, ko)
+    for text, kw in [(LAST, {}), (LAST, dict(k=None, ko=None)), (LAST, dict(fr=None)), (LAST, dict(wq=None, wk=None, eps=None)), ("k and k_out go together", dict(ko=None)),
+                     ("q: this type", dict(q=q.float())), ("q and q_out", dict(qo=q[:2])), ("q and q_out", dict(qo=q.bfloat16())), ("k and k_out are", dict(k=k[:2], ko=k[:2])),
+                     ("k and k_out are", dict(k=k.bfloat16())), ("heads of a token must be dense", dict(q=q.transpose(1, 2).contiguous().transpose(1, 2))),
+                     ("cu [S + 1] and seq_len [S]", dict(cu=CU.long())), ("cu [S + 1] and seq_len [S]", dict(ln=KL[:1])), ("w_q and w_k are contiguous", dict(wq=w[:32])),
+                     ("w_q and w_k are contiguous", dict(wk=w.half())), ("freq is contiguous", dict(fr=fr.double())), ("w_q and w_k belong to a norm", dict(eps=None)),
+                     ("different devices", dict(cu=CU.to(META)))]:
+        refused(f, text, **kw)
+
+
+def test_mass_and_evict_binding():
+    K = torch.zeros((4, 2, 16, 64), dtype=H)
+    q, lse, m, pos = torch.zeros((3, 8, 64), dtype=H), torch.zeros((3, 8)), torch.zeros((2, 2, 48)), torch.zeros((2, 2, 48), dtype=I32)
+
+    def f(q=q, c=(K, K), cu=CU, kl=KL, tab=TAB, lse=lse, m=m, pos=pos, **kw):
+        _lib.attn_mass(q, c, cu, kl, tab, 2, 5, lse, m, pos, **kw)
+    for text, kw in [(LAST, {}), (LAST, dict(mass_out=m.clone(), seq_len=KL)), ("the cache is a tuple", dict(c=K)), ("q: this type", dict(q=q.float())),
+                     ("lse is contiguous", dict(lse=lse[:2])), ("lse is contiguous", dict(lse=lse.half())), ("mass is contiguous", dict(m=m[:1])),
+                     ("mass is contiguous", dict(m=m[:, :, ::2])), ("mass is contiguous", dict(mass_out=m.double())), ("pos is contiguous", dict(pos=pos.long())),
+                     ("pos is contiguous", dict(pos=pos[:, :, :4].contiguous())), ("lengths are contiguous int32", dict(seq_len=KL.long())), ("need cu [S + 1]", dict(kl=KL[:1])),
+                     ("workspace must be contiguous", dict(ws=torch.zeros(8)[::2])), ("different devices", dict(lse=lse.to(META)))]:
+        refused(f, text, **kw)
+    src = torch.zeros((2, 2, 32), dtype=I32)
+
+    def g(c=(K, K), kl=KL, tab=TAB, m=m, pos=pos, keep=32, src=src, ws=None, **kw):
+        _lib.kv_evict(c, kl, tab, m, pos, keep, src, ws, **kw)
+    for text, kw in [(LAST, {}), (LAST, dict(seq_len=KL, kv_len_out=KL.clone(), mass_out=m.clone(), pos_out=pos.clone())), ("the cache is a tuple", dict(c=(K,))),
+                     ("lengths are contiguous int32", dict(kl=KL.float())), ("table is int32", dict(tab=TAB[:1])), ("table is int32", dict(tab=TAB.long())),
+                     ("mass is contiguous", dict(m=m.half())), ("pos is contiguous", dict(pos_out=pos[:1])), ("src is contiguous", dict(keep=31)),
+                     ("src is contiguous", dict(src=src.float())), ("lengths are contiguous int32", dict(kv_len_out=KL[:1])), ("different devices", dict(src=src.to(META)))]:
+        refused(g, text, **kw)
