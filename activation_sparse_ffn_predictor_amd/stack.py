@@ -39,7 +39,10 @@ PAGES = tuple(1 << b for b in range(4, 11))
 
 @dataclasses.dataclass(frozen=True)
 class AttnConfig:
-    """Attention of a stack's layers: head layout, cache type ("f16", "i8" or "e4m3") and room, window and sinks."""
+    """Attention of a stack's layers: head layout, cache type ("f16", "i8" or "e4m3") and room, window and sinks; norms of heads,
+    rotary positions (rope_base > 0; of the first rope_dim elements of a head, 0: all), type of the projections' weights ("f16" or
+    "e4m3"). keep > 0: a sequence that would grow past max_len is cut down to `keep` cached tokens for each K/V head, the first
+    `sinks`, the last `recent` and those with the most attention (no window then: it would count slots)."""
     n_heads: int
     n_kv_heads: int
     head_dim: int
@@ -49,8 +52,20 @@ class AttnConfig:
     window: int = 0
     sinks: int = 0
     eps: float = 1e-5
+    qk_norm: bool = False
+    rope_base: float = 0.0
+    rope_dim: int = 0
+    rope_interleaved: bool = False
+    weights: str = "f16"
+    keep: int = 0
+    recent: int = 0
 
     def __post_init__(self):
+        rot = self.rope_dim or self.head_dim
+        if (not (self.rope_base >= 0 and math.isfinite(self.rope_base)) or not 8 <= rot <= self.head_dim or rot % 8
+                or self.weights not in ("f16", "e4m3") or not 0 <= self.keep < max(self.max_len, 1) or self.recent < 0
+                or (self.keep and (self.window or self.sinks + self.recent > self.keep)) or (self.recent and not self.keep)):
+            raise ValueError(f"attention: {self}")
         if (self.kv_type not in KV_TYPES or min(self.max_len, self.n_kv_heads, self.n_heads) < 1
                 or self.n_heads % self.n_kv_heads or not 16 <= self.head_dim <= 256
                 or self.head_dim % (8 if self.kv_type == "f16" else 16) or self.page not in PAGES
@@ -99,20 +114,32 @@ class SparseFFNStack:
         c, D, B, dev = self.attn, self.wl.D, self.max_batch, self.device
         width, cols = (c.n_heads + 2 * c.n_kv_heads) * c.head_dim, -(-c.max_len // c.page)
         kt, cache = KV_TYPES[c.kv_type], (B * cols, c.n_kv_heads, c.page, c.head_dim)
+        heads, slots, e8 = c.n_heads * c.head_dim, cols * c.page, c.weights == "e4m3"
+        if e8 and (D % 16 or heads % 16 or width % 8):
+            raise ValueError(f"e4m3 projections: d_model = {D}, heads of {heads} together: need multiples of 16")
         for l, t in zip(self.layer_ids, self.layers):
             g = torch.Generator(device=dev)
             g.manual_seed((seed * 1000003 + l) % (1 << 63))
             t["W_qkv"] = (torch.randn((width, D), generator=g, device=dev) / D ** 0.5).half()
-            t["W_o"] = (torch.randn((D, c.n_heads * c.head_dim), generator=g, device=dev) / (c.n_heads * c.head_dim) ** 0.5).half()
+            t["W_o"] = (torch.randn((D, heads), generator=g, device=dev) / heads ** 0.5).half()
+            if e8:
+                for name in ("W_qkv", "W_o"):
+                    t[name] = self._quantised(t[name], 128)
             t["w_attn"], t["w_ffn"] = (1 + 0.1 * torch.randn(D, generator=g, device=dev) for _ in range(2))
             kv = [torch.zeros(cache, device=dev).to(kt) for _ in range(2)]
             if c.kv_type != "f16":
                 kv += [torch.zeros(cache[:3], device=dev) for _ in range(2)]
             t["kv"] = tuple(kv)
+            if c.qk_norm:
+                t["w_q"], t["w_k"] = (1 + 0.1 * torch.randn(c.head_dim, generator=g, device=dev) for _ in range(2))
+            if c.keep:
+                t["mass"] = torch.zeros((B, c.n_kv_heads, slots), device=dev)
+                t["pos"] = torch.zeros((B, c.n_kv_heads, slots), dtype=torch.int32, device=dev)
         self.w_out = torch.ones(D, device=dev)
         self.table = torch.arange(B * cols, dtype=torch.int32, device=dev).view(B, cols)
         self.kv_len = torch.zeros(B, dtype=torch.int32, device=dev)
         self.lens = [0] * B                                    # the same on the host, to refuse what does not fit
+        self.seq_len = torch.zeros(B, dtype=torch.int32, device=dev)   # tokens entered, evicted ones with them
         self.cu_step = torch.arange(B + 1, dtype=torch.int32, device=dev)
         self.cu_prompt = {}
         self.h = torch.zeros((B, D), device=dev)               # residual stream
@@ -125,29 +152,86 @@ class SparseFFNStack:
         sizes = [_lib.attn_workspace_size(T, S, c.n_heads, c.n_kv_heads, c.head_dim, T // S, c.max_len, c.window, c.sinks)
                  for T in range(1, B + 1) for S in (1, T)]
         self.ws_attn = torch.zeros(max([256] + sizes), dtype=torch.uint8, device=dev)
+        rot = c.rope_dim or c.head_dim
+        self.freq = (c.rope_base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)).float().to(dev) if c.rope_base else None
+        if e8:
+            self.xq, self.xs = self._quantised(self.xn, 1)
+            self.oq, self.os = self._quantised(self.o.flatten(1), 1)
+            need = max(_lib.mm_workspace_size(T, *n_k) for T in range(1, B + 1) for n_k in ((width, D), (D, heads)))
+            self.ws_mm = torch.zeros(max(256, need), dtype=torch.uint8, device=dev)
+        if c.keep:
+            self.lse = torch.zeros((B, c.n_heads), device=dev)
+            need = max(_lib.attn_mass_workspace_size(S, c.n_heads, c.n_kv_heads, c.head_dim, T // S, c.max_len, slots)
+                       for T in range(1, B + 1) for S in (1, T))
+            self.ws_mass = torch.zeros(max(256, need), dtype=torch.uint8, device=dev)
+            self.ws_evict = torch.zeros(_lib.kv_evict_workspace_size(1, c.n_kv_heads, slots, c.keep), dtype=torch.uint8, device=dev)
+            self.src = torch.zeros((1, c.n_kv_heads, c.keep), dtype=torch.int32, device=dev)
+            self.cut_len = torch.zeros(1, dtype=torch.int32, device=dev)
 
-    def attn_layer(self, i: int, x, B: int, cu, kv_len, table, max_q: int):
+    @staticmethod
+    def _quantised(x, rows: int):
+        """(codes, scales) of x [T, K] in blocks of `rows` x 128."""
+        T, K = x.shape
+        q = torch.empty((T, K), dtype=torch.float8_e4m3fn, device=x.device)
+        s = torch.empty((-(-T // rows), -(-K // 128)), device=x.device)
+        _lib.quant128(x, q, s, rows=rows)
+        return q, s
+
+    def _project(self, x, xq, xs, w, out):
+        """out = x W^T: fp16, or x quantised into xq, xs and 8-bit weights."""
+        if self.attn.weights == "f16":
+            torch.mm(x, w.t(), out=out)
+            return
+        _lib.quant128(x, xq, xs)
+        _lib.mm_e4m3(xq, xs, *w, out, self.ws_mm)
+
+    def attn_layer(self, i: int, x, B: int, cu, kv_len, table, max_q: int, seq_len=None, rows: slice = slice(0, None)):
         """Attention half of stored layer i for B tokens: x (the FFN output before it, or the input with i = 0) joins the
-        residual stream self.h; leaves the FFN's input in self.xf."""
+        residual stream self.h; leaves the FFN's input in self.xf. The call's sequences are rows `rows` of the stack's, which
+        count seq_len tokens (None: kv_len)."""
         c, t = self.attn, self.layers[i]
+        e8 = c.weights == "e4m3"
         h, xn, qkv, o, ao = self.h[:B], self.xn[:B], self.qkv[:B], self.o[:B], self.ao[:B]
         _lib.add_rmsnorm(x, h if i else None, t["w_attn"], c.eps, xn, res_out=h)
-        torch.mm(xn, t["W_qkv"].t(), out=qkv)
+        self._project(xn, self.xq[:B] if e8 else None, self.xs[:B] if e8 else None, t["W_qkv"], qkv)
         parts = qkv.unflatten(1, (-1, c.head_dim))
         q, k, v = parts.split([c.n_heads, c.n_kv_heads, c.n_kv_heads], dim=1)
+        if c.qk_norm or self.freq is not None:
+            _lib.qk_norm_rope(q, k, t.get("w_q"), t.get("w_k"), c.eps if c.qk_norm else None, cu, kv_len if seq_len is None else seq_len,
+                              self.freq, q, k, interleaved=c.rope_interleaved)
         _lib.kv_write(k, v, t["kv"], cu, kv_len, table)
         # the keys are split for max_len however long the sequences are yet, so that eager and replayed steps give the same
         # bits (one sequence of 500 tokens, 64 heads on 8 of 128: 12.2 us with max_len 4096, 9.7 where the hint is 500)
-        _lib.attn(q, t["kv"], cu, kv_len, table, max_q, c.max_len, o, self.ws_attn, window=c.window, sinks=c.sinks)
-        torch.mm(o.flatten(1), t["W_o"].t(), out=ao)
+        lse = self.lse[:B] if c.keep else None
+        _lib.attn(q, t["kv"], cu, kv_len, table, max_q, c.max_len, o, self.ws_attn, window=c.window, sinks=c.sinks, lse=lse)
+        if c.keep:
+            mine = slice(rows.start, rows.start + table.shape[0])
+            _lib.attn_mass(q, t["kv"], cu, kv_len, table, max_q, c.max_len, lse, t["mass"][mine], t["pos"][mine], self.ws_mass,
+                           seq_len=seq_len)
+        self._project(o.flatten(1), self.oq[:B] if e8 else None, self.os[:B] if e8 else None, t["W_o"], ao)
         _lib.add_rmsnorm(ao, h, t["w_ffn"], c.eps, self.xf[:B], res_out=h)
 
-    def _layers(self, x, B: int, cu, kv_len, table, max_q: int):
+    def _layers(self, x, B: int, cu, rows: slice, max_q: int):
+        kv_len, seq_len, table = self.kv_len[rows], self.seq_len[rows], self.table[rows]
         for i in range(len(self.layers)):
-            self.attn_layer(i, x, B, cu, kv_len, table, max_q)
+            self.attn_layer(i, x, B, cu, kv_len, table, max_q, seq_len, rows)
             x = self.y[i, :B]
             self.layer_call(i, self.xf[:B], False, x)
         _lib.add_rmsnorm(x, self.h[:B], self.w_out, self.attn.eps, self.out[:B], res_out=self.h[:B])
+
+    def evict(self, s: int):
+        """Cut sequence s down to the configuration's `keep` cached tokens if it holds more, in every layer."""
+        c = self.attn
+        if c is None or not c.keep or not 0 <= s < self.max_batch:
+            raise ValueError(f"evict: sequence {s} (the stack needs attention with keep > 0)")
+        if self.lens[s] <= c.keep:
+            return
+        one = slice(s, s + 1)
+        for t in self.layers:
+            _lib.kv_evict(t["kv"], self.kv_len[one], self.table[one], t["mass"][one], t["pos"][one], c.keep, self.src, self.ws_evict,
+                          seq_len=self.seq_len[one], sinks=c.sinks, recent=c.recent, kv_len_out=self.cut_len)
+        self.kv_len[one] = self.cut_len
+        self.lens[s] = c.keep
 
     @contextlib.contextmanager
     def _grown(self, rows: slice, n: int):
@@ -155,11 +239,13 @@ class SparseFFNStack:
         before = self.lens[rows]
         self.lens[rows] = [m + n for m in before]
         self.kv_len[rows] += n
+        self.seq_len[rows] += n
         try:
             yield
         except Exception:
             self.lens[rows] = before
             self.kv_len[rows] -= n
+            self.seq_len[rows] -= n
             raise
 
     def _batch(self, B: int):
@@ -167,8 +253,18 @@ class SparseFFNStack:
             raise ValueError(f"{B} sequences: need 1 to max_batch = {self.max_batch}")
 
     def _room(self, s: int, n: int):
-        if self.lens[s] + n > self.attn.max_len:
+        """Refuse what does not fit (and with `keep` would not after an eviction either)."""
+        held = min(self.lens[s], self.attn.keep) if self.attn.keep else self.lens[s]
+        if held + n > self.attn.max_len:
             raise ValueError(f"sequence {s}: {self.lens[s]} + {n} tokens exceed max_len = {self.attn.max_len}")
+
+    def _make_room(self, rows, n: int):
+        """Refuse what does not fit; evict from the sequences that would grow past max_len."""
+        for s in rows:
+            self._room(s, n)
+        for s in rows:
+            if self.lens[s] + n > self.attn.max_len:
+                self.evict(s)
 
     def prompt(self, s: int, x: torch.Tensor):
         """Enter x [T, D] fp32 (T <= max_batch), the next tokens of sequence s; results in self.out[:T]."""
@@ -178,16 +274,17 @@ class SparseFFNStack:
         if x.dim() != 2 or x.shape[1] != self.wl.D or x.dtype != torch.float32 or x.device != self.out.device:
             raise ValueError(f"prompt: x is fp32 [T, {self.wl.D}] on {self.out.device}")
         x = x.contiguous()
-        self._room(s, T)
+        self._make_room([s], T)
         if T not in self.cu_prompt:
             self.cu_prompt[T] = torch.tensor([0, T], dtype=torch.int32, device=self.device)
         one = slice(s, s + 1)
         with self._grown(one, T):
-            self._layers(x, T, self.cu_prompt[T], self.kv_len[one], self.table[one], T)
+            self._layers(x, T, self.cu_prompt[T], one, T)
 
     def reset(self):
         """Forget every sequence's tokens."""
         self.kv_len.zero_()
+        self.seq_len.zero_()
         self.lens = [0] * self.max_batch
 
     # ------------------------------------------------------------------ one layer
@@ -229,10 +326,9 @@ class SparseFFNStack:
         x = self.x_in[:B]
         if self.attn is not None:
             self._batch(B)
-            for s in range(B):
-                self._room(s, 1)
+            self._make_room(range(B), 1)
             with self._grown(slice(0, B), 1):
-                self._layers(x, B, self.cu_step[:B + 1], self.kv_len[:B], self.table[:B], 1)
+                self._layers(x, B, self.cu_step[:B + 1], slice(0, B), 1)
             return
         for i in range(len(self.layers)):
             y = self.y[i, :B]
@@ -241,8 +337,13 @@ class SparseFFNStack:
 
     def capture(self, B: int = 1):
         """Capture step(B) into a HIP graph (after one eager warm-up). With attention the warm-up's tokens are taken
-        back: the sequences are as long afterwards as before."""
-        lens = None if self.attn is None else (list(self.lens), self.kv_len.clone())
+        back: the sequences are as long afterwards as before (unless one had to be cut down for it)."""
+        lens = None
+        if self.attn is not None:
+            self._batch(B)
+            self._make_room(range(B), 1)
+            seen = [(t["mass"][:B].clone(), t["pos"][:B].clone()) for t in self.layers] if self.attn.keep else []
+            lens = (list(self.lens), self.kv_len.clone(), self.seq_len.clone())
         self.step(B)
         torch.cuda.synchronize(self.device)
         try:
@@ -255,14 +356,17 @@ class SparseFFNStack:
             if lens is not None:
                 self.lens = lens[0]
                 self.kv_len.copy_(lens[1])
+                self.seq_len.copy_(lens[2])
+                for t, (mass, pos) in zip(self.layers, seen):
+                    t["mass"][:B] = mass
+                    t["pos"][:B] = pos
         self.graphs[B] = g
         return g
 
     def replay(self, B: int = 1):
         graph = self.graphs[B]                                 # (before any length grows)
         if self.attn is not None:
-            for s in range(B):
-                self._room(s, 1)
+            self._make_room(range(B), 1)
             self.lens[:B] = [n + 1 for n in self.lens[:B]]
         graph.replay()
 

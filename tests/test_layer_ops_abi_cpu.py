@@ -2,6 +2,9 @@
 turned away on the host before anything is enqueued (fake pointers that are never followed), and the binding checks what the
 C ABI cannot see. No GPU."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -10,6 +13,7 @@ from activation_sparse_ffn_predictor_amd import _lib
 from test_attention_abi_cpu import CACHE_BAD, SEQ_BAD, kv, sq
 
 A = 0x10000
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 LAST = "the tensors must be on the GPU"
 
 
@@ -189,3 +193,27 @@ def test_mass_and_evict_binding():
                      ("mass is contiguous", dict(m=m.half())), ("pos is contiguous", dict(pos_out=pos[:1])), ("src is contiguous", dict(keep=31)),
                      ("src is contiguous", dict(src=src.float())), ("lengths are contiguous int32", dict(kv_len_out=KL[:1])), ("different devices", dict(src=src.to(META)))]:
         refused(g, text, **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(rope_base=-1.0), dict(rope_base=math.inf), dict(rope_base=math.nan), dict(rope_dim=4), dict(rope_dim=72), dict(rope_dim=12),
+                                dict(weights="f8"), dict(keep=-1), dict(keep=100), dict(keep=101), dict(keep=20, window=5), dict(keep=20, sinks=15, recent=6),
+                                dict(recent=3), dict(keep=20, recent=-1)])
+def test_stack_configurations(kw):
+    from activation_sparse_ffn_predictor_amd.stack import AttnConfig
+    with pytest.raises(ValueError):
+        AttnConfig(8, 2, 64, **dict(dict(max_len=100), **kw))
+    AttnConfig(8, 2, 64, max_len=100, keep=20, sinks=14, recent=6, rope_base=10000.0, rope_dim=32, weights="e4m3", qk_norm=True)
+
+
+def test_refusals_under_host_sanitizers():
+    """The checks above once more against a library whose host code is instrumented, in a child process."""
+    if os.environ.get("SFFN_LIB_PATH"):
+        pytest.skip("this is the child")
+    if subprocess.run(["which", "hipcc"], capture_output=True).returncode != 0:
+        pytest.skip("hipcc is not installed")
+    from activation_sparse_ffn_predictor_amd import build_sanitized as bs
+    bs.build()
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-p", "no:cacheprovider", os.path.abspath(__file__)],
+                       env=bs.sanitizer_env(), cwd=ROOT, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout[-4000:] + r.stderr[-4000:]
+    assert "passed" in r.stdout and "AddressSanitizer" not in r.stderr and "runtime error" not in r.stderr
