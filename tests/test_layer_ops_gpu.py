@@ -473,3 +473,105 @@ def test_evict_odd(gpu_ready):
     check_evict(gpu_ready, b, 120, m[..., :120].contiguous(), pos[..., :120].contiguous(), plen, 90, 3, 20, True)
     plen[:] = -2147483648
     check_evict(gpu_ready, b, W, m, pos, plen, 90, 3, 20, False)
+
+
+# ------------------------------------------------------------------------------------------------ all of them, in graphs
+def test_graphs_and_streams(gpu_ready):
+    """A pass through all of them, eager, on a stream of its own, and in two captured graphs that share their workspaces, replayed
+    in turn with eager work between: the same bits every time."""
+    dev = gpu_ready
+    Hq, Hkv, d, page, D, S, W = 16, 4, 64, 16, 512, 3, 640
+    width = (Hq + 2 * Hkv) * d
+    g = torch.Generator().manual_seed(4)
+    wq = torch.randn((width, D), generator=g) / D ** 0.5
+    codes_w, sc_w = torch.empty((width, D), dtype=E4M3, device=dev), torch.empty((blocks(width), blocks(D)), device=dev)
+    _lib.quant128(wq.to(dev), codes_w, sc_w, rows=128)
+    fr = freqs(d).to(dev)
+
+    class Pass:
+        """One pass for ns new tokens of sequences that hold ks with them."""
+        def __init__(self, ns, ks, seed, shared):
+            gg = torch.Generator().manual_seed(seed)
+            b = Paged(ns, ks, Hkv, d, page, "f16", "i8", seed=seed, cols=W // page)
+            b.table = torch.arange(S * (W // page), dtype=torch.int32).view(S, -1) % b.n_pages
+            b.n_pages = S * (W // page)
+            b.table = torch.randperm(b.n_pages, generator=gg).to(torch.int32).view(S, -1)
+            x = torch.randn((2, b.n_pages, Hkv, page, d), generator=gg)
+            b.set_values(x.half())
+            self.kv, self.cu, self.kl, self.tab = b.gpu(dev)
+            self.kv0 = [t.clone() for t in self.kv]
+            self.ns, self.T = ns, sum(ns)
+            self.x = torch.randn((self.T, D), generator=gg).half().to(dev)
+            self.xq, self.xs = torch.empty((self.T, D), dtype=E4M3, device=dev), torch.empty((self.T, blocks(D)), device=dev)
+            self.qkv = torch.empty((self.T, width), dtype=torch.float16, device=dev)
+            self.o, self.lse = torch.empty((self.T, Hq, d), dtype=torch.float16, device=dev), torch.empty((self.T, Hq), device=dev)
+            self.mass0 = torch.rand((S, Hkv, W), generator=gg).to(dev)
+            self.pos0 = torch.arange(W, dtype=torch.int32, device=dev).expand(S, Hkv, W).contiguous()
+            self.mass, self.pos, self.len2 = self.mass0.clone(), self.pos0.clone(), torch.zeros_like(self.kl)
+            self.src = torch.zeros((S, Hkv, 100), dtype=torch.int32, device=dev)
+            self.ws = shared
+
+        def __call__(self):
+            for t, t0 in zip(self.kv, self.kv0):
+                t.copy_(t0)
+            self.mass.copy_(self.mass0)
+            self.pos.copy_(self.pos0)
+            _lib.quant128(self.x, self.xq, self.xs)
+            _lib.mm_e4m3(self.xq, self.xs, codes_w, sc_w, self.qkv, self.ws)
+            q, k, v = self.qkv.unflatten(1, (-1, d)).split([Hq, Hkv, Hkv], dim=1)
+            _lib.qk_norm_rope(q, k, None, None, 1e-6, self.cu, self.kl, fr, q, k)
+            _lib.kv_write(k, v, self.kv, self.cu, self.kl, self.tab)
+            _lib.attn(q, self.kv, self.cu, self.kl, self.tab, max(self.ns), W, self.o, self.ws, lse=self.lse)
+            _lib.attn_mass(q, self.kv, self.cu, self.kl, self.tab, max(self.ns), W, self.lse, self.mass, self.pos, self.ws)
+            _lib.kv_evict(self.kv, self.kl, self.tab, self.mass, self.pos, 100, self.src, self.ws, sinks=2, recent=20, kv_len_out=self.len2)
+            return [t.clone() for t in (self.qkv, self.o, self.lse, self.mass, self.pos, self.src, self.len2) + tuple(self.kv)]
+
+    def same(a, b, what):
+        for i, (x, y) in enumerate(zip(a, b)):
+            bits = {1: torch.uint8, 2: torch.int16, 4: torch.int32}[x.element_size()]
+            assert torch.equal(x.view(bits), y.view(bits)), (what, i)
+    need = max([_lib.mm_workspace_size(T, width, D) for T in (3, 150)] + [_lib.kv_evict_workspace_size(S, Hkv, W, 100)]
+               + [f for n in (1, 90) for f in (_lib.attn_workspace_size(150, S, Hq, Hkv, d, n, W), _lib.attn_workspace_size(3, S, Hq, Hkv, d, n, W),
+                                               _lib.attn_mass_workspace_size(S, Hq, Hkv, d, n, W, W))])
+    ws = torch.zeros(need, dtype=torch.uint8, device=dev)
+    a, b = Pass([1, 1, 1], [600, 99, 300], 1, ws), Pass([90, 1, 59], [500, 120, 59], 2, ws)
+    want = [a(), b()]
+    torch.cuda.synchronize()
+    assert want[0][6].tolist() == [100, 99, 100] and want[1][6].tolist() == [100, 100, 59]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        same(a(), want[0], "stream")
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for p in (a, b):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            out = p()
+        graphs.append(gr)
+        outs.append(out)
+    for rep in range(4):
+        for gr, out, w in zip(graphs, outs, want):
+            gr.replay()
+            torch.cuda.synchronize()
+            same(out, w, f"replay {rep}")
+            same(b() if w is want[0] else a(), want[1] if w is want[0] else want[0], "eager between")
+            torch.cuda.synchronize()
+
+
+def test_nothing_to_do(gpu_ready):
+    """No tokens, empty sequences, and rows behind the last one."""
+    dev = gpu_ready
+    e = torch.empty((0, 256), device=dev)
+    _lib.quant128(e, e.to(E4M3), torch.empty((0, 2), device=dev))
+    out = torch.empty((0, 64), device=dev)
+    _lib.mm_e4m3(e.to(E4M3), torch.empty((0, 2), device=dev), torch.zeros((64, 256), device=dev).to(E4M3), torch.zeros((1, 2), device=dev), out)
+    b = Paged([0, 0], [30, 0], 2, 64, 16, "f16", "f16", seed=1, pad=4)
+    kv, cu, kl, tab = b.gpu(dev)
+    q, k = torch.ones((4, 4, 64), dtype=torch.float16, device=dev), torch.ones((4, 2, 64), dtype=torch.float16, device=dev)
+    _lib.qk_norm_rope(q, k, None, None, 1e-6, cu, kl, freqs(64).to(dev), q, k)
+    m, pos = torch.full((2, 2, 40), 3.0, device=dev), torch.full((2, 2, 40), 5, dtype=torch.int32, device=dev)
+    _lib.attn_mass(q, kv, cu, kl, tab, 1, 30, torch.zeros((4, 4), device=dev), m, pos)
+    _lib.attn_mass(q[:0], kv, cu, kl, tab, 1, 30, torch.zeros((0, 4), device=dev), m, pos)
+    torch.cuda.synchronize()
+    assert bool((q == 1).all()) and bool((k == 1).all()) and bool((m == 3).all()) and bool((pos == 5).all())
