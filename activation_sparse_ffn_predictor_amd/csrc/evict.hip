@@ -22,13 +22,12 @@ struct Keys {
   const float* mass;
   const int* pos;
   const int* trow;
-  int psh, n_pages, cols, sinks, late;
+  int psh, n_pages, sinks, late;
   __device__ __forceinline__ uint32_t operator()(int j) const {
     const float m = mass[j];
-    const int p = pos[j], pid = trow[j >> psh];
-    if ((unsigned)pid >= (unsigned)n_pages) return 0;
-    if (p < sinks || p >= late) return 0xFFFFFFFFu;
-    return m > 0.f ? 1u + __float_as_uint(m) : 1u;
+    const int p = pos[j], pid = trow[j >> psh];    // (no branches, so that the loads of several slots are under way at once)
+    const uint32_t held = ((p < sinks) | (p >= late)) ? 0xFFFFFFFFu : 1u + (m > 0.f ? __float_as_uint(m) : 0u);
+    return (unsigned)pid < (unsigned)n_pages ? held : 0u;
   }
 };
 
@@ -82,19 +81,20 @@ __device__ __forceinline__ void find_digit(int n1, int n0, int need, int* tmp, i
   __syncthreads();
 }
 // A workgroup's slots j0, j0 + 64, ... of this lane, `steps` of them, below `end`; wave w owns (w * steps .. (w + 1) * steps - 1) * 64, so
-// that ranks in slot order need one prefix over the waves. Keys are in registers, or (WS) read REGS at a time.
+// that ranks in slot order need one prefix over the waves. Keys are in registers or, where a lane has more than REGS, read again (WS).
 template <bool WS>
 struct Slots {
   int j0, steps, end;
   const uint32_t* kept;
   uint32_t k[REGS];
+  __device__ __forceinline__ void read(int i0) {
+#pragma unroll
+    for (int i = 0; i < REGS; ++i) k[i] = kept[max(0, min(j0 + (i0 + i) * 64, end - 1))];
+  }
   template <class F>
   __device__ __forceinline__ void each(F f) {      // f(slot, key, does it exist) in every lane of the wave
     for (int i0 = 0; i0 < steps; i0 += REGS) {
-      if constexpr (WS) {
-#pragma unroll
-        for (int i = 0; i < REGS; ++i) k[i] = kept[min(j0 + (i0 + i) * 64, end - 1)];
-      }
+      if (WS && steps > REGS) read(i0);
 #pragma unroll
       for (int i = 0; i < REGS; ++i) {
         const int j = j0 + (i0 + i) * 64;
@@ -149,7 +149,7 @@ __device__ __forceinline__ void emit(Slots<WS>& sl, const EvictArgs& a, long sh,
 
 __device__ __forceinline__ int slots_of(const EvictArgs& a, int s) { return min(max(a.len[s], 0), min(a.cols << a.kv.psh, a.W)); }
 __device__ __forceinline__ Keys keys_of(const EvictArgs& a, int s, long sh) {
-  return {a.mass + sh * a.W, a.pos + sh * a.W, a.table + (long)s * a.ldt, a.kv.psh, a.kv.n_pages, a.cols, a.sinks,
+  return {a.mass + sh * a.W, a.pos + sh * a.W, a.table + (long)s * a.ldt, a.kv.psh, a.kv.n_pages, a.sinks,
           a.recent ? (int)max((long)a.plen[s] - a.recent, -2147483648l) : 2147483647};
 }
 __device__ __forceinline__ void keep_all(const EvictArgs& a, long sh, int first, int step) {
@@ -218,6 +218,18 @@ struct Chunk {
     end = max(end, begin);
   }
 };
+// f(chunk, the thread's two counts (digits b1 - 1 and b1)) for every chunk; eight chunks' are read at once
+template <class F>
+__device__ __forceinline__ void each_chunk(const int* counts, int chunks, int b1, F f) {
+  for (int c0 = 0; c0 < chunks; c0 += 8) {
+    int2 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const int2*>(counts + (long)min(c0 + i, chunks - 1) * BINS + b1 - 1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c0 + i < chunks) f(c0 + i, v[i]);
+  }
+}
 template <int D>
 __global__ __launch_bounds__(NT) void k_digit(EvictArgs a) {
   __shared__ int hist[BINS];
@@ -230,6 +242,12 @@ __global__ __launch_bounds__(NT) void k_digit(EvictArgs a) {
     return;
   }
   EvictFound* state = a.found + sh * 3;
+  Slots<true> sl;
+  sl.steps = (ch.end - ch.begin + NT - 1) / NT;
+  sl.j0 = ch.begin + w * sl.steps * 64 + l;
+  sl.end = ch.end;
+  sl.kept = a.keys + sh * a.W;
+  if (D > 0) sl.read(0);                           // (ahead of what the digit's count waits for)
   uint32_t cut = 0;
   int need = a.keep;
   hist[threadIdx.x] = hist[threadIdx.x + NT] = 0;
@@ -240,11 +258,7 @@ __global__ __launch_bounds__(NT) void k_digit(EvictArgs a) {
     // the digit before this one, from the counts of all chunks; and how many of this chunk's keys lie over it
     const int* before = a.hist + ((long)(D - 1) * a.kv.hkv * a.S + sh) * a.chunks * BINS;
     int n1 = 0, n0 = 0;
-    for (int c = 0; c < a.chunks; ++c) {
-      const int2 v = *reinterpret_cast<const int2*>(before + (long)c * BINS + b1 - 1);
-      n0 += v.x;
-      n1 += v.y;
-    }
+    each_chunk(before, a.chunks, b1, [&](int, int2 v) { n0 += v.x, n1 += v.y; });
     if (D == 1) {
       if (l < 64) {
         int p = 0;
@@ -275,11 +289,6 @@ __global__ __launch_bounds__(NT) void k_digit(EvictArgs a) {
     if (full) return;
   }
   const Digit g(D, cut);
-  Slots<true> sl;
-  sl.steps = (ch.end - ch.begin + NT - 1) / NT;
-  sl.j0 = ch.begin + w * sl.steps * 64 + l;
-  sl.end = ch.end;
-  sl.kept = a.keys + sh * a.W;
   int tops = 0, ones = 0;
   if constexpr (D == 0) {
     const Keys key = keys_of(a, s, sh);
@@ -295,7 +304,7 @@ __global__ __launch_bounds__(NT) void k_digit(EvictArgs a) {
         if (i0 + i < sl.steps) g.count(hist, sl.k[i], in, tops, ones);
       }
     }
-  } else if (ch.end > ch.begin) {
+  } else {
     sl.each([&](int, uint32_t x, bool in) { g.count(hist, x, in, tops, ones); });
   }
   if (l == 0 && ones) atomicAdd(&hist[g.of_ones()], ones);
@@ -311,6 +320,12 @@ __global__ __launch_bounds__(NT) void k_emit(EvictArgs a) {
   const Chunk ch(a, s);
   const long sh = ch.sh;
   if (ch.n <= a.keep) return;
+  Slots<true> sl;
+  sl.steps = (ch.end - ch.begin + NT - 1) / NT;
+  sl.j0 = ch.begin + w * sl.steps * 64 + l;
+  sl.end = ch.end;
+  sl.kept = a.keys + sh * a.W;
+  sl.read(0);
   uint32_t cut = a.found[sh * 3 + 1].cut;
   int ties = a.found[sh * 3 + 1].ties;
   const bool full = cut == 0xFFFFFFFFu;            // then the protected ones are the ties
@@ -323,21 +338,16 @@ __global__ __launch_bounds__(NT) void k_emit(EvictArgs a) {
   __syncthreads();
   if (!full) {
     int n1 = 0, n0 = 0;
-    for (int c = 0; c < a.chunks; ++c) {
-      const int2 v = *reinterpret_cast<const int2*>(before + (long)c * BINS + b1 - 1);
-      n0 += v.x;
-      n1 += v.y;
-    }
+    each_chunk(before, a.chunks, b1, [&](int, int2 v) { n0 += v.x, n1 += v.y; });
     find_digit(n1, n0, ties, tmp[0], found);
     cut |= (uint32_t)found[0];
     ties = found[1];
-    for (int c = 0; c < a.chunks; ++c) {
-      const int2 v = *reinterpret_cast<const int2*>(before + (long)c * BINS + b1 - 1);
+    each_chunk(before, a.chunks, b1, [&](int c, int2 v) {
       const int sum = wave_scan((b1 > found[0] ? v.y : 0) + (b1 - 1 > found[0] ? v.x : 0));
       if (l == 63 && sum) atomicAdd(&over[c], sum);
       if (b1 == found[0]) eq[c] = v.y;
       if (b1 - 1 == found[0]) eq[c] = v.x;
-    }
+    });
     __syncthreads();
   }
   // where this chunk's ties, movers and holes begin
@@ -353,11 +363,6 @@ __global__ __launch_bounds__(NT) void k_emit(EvictArgs a) {
     if (ch.c == 0) a.moves[sh] = m;
   }
   __syncthreads();
-  Slots<true> sl;
-  sl.steps = (ch.end - ch.begin + NT - 1) / NT;
-  sl.j0 = ch.begin + w * sl.steps * 64 + l;
-  sl.end = ch.end;
-  sl.kept = a.keys + sh * a.W;
   if (ch.end > ch.begin) emit<true>(sl, a, sh, cut, ties, start[0], start[1], start[2], tmp, nullptr);
 }
 
