@@ -421,7 +421,8 @@ hipError_t many(const MassArgs& a, bool bf, int kvm, dim3 grid, hipStream_t st) 
 
 hipError_t sffn_launch_mass(const MassArgs& a, int qt, int kvt, int tiles, hipStream_t st) {
   const bool bf = qt == T_BF16;
-  const int kvm = kvt == T_I8 ? 1 : kvt == T_E4M3 ? 2 : 0, d = a.kv.d, rows = a.max_q * a.G;
+  const int kvm = kvt == T_I8 ? 1 : kvt == T_E4M3 ? 2 : 0, d = a.kv.d;
+  const long rows = (long)a.max_q * a.G;             // (max_q may be far over what the sequences have)
   if (mass_few(rows, d)) {
     const dim3 grid(tiles, a.kv.hkv, a.sq.S);
     if (d <= 64) return rows > 32 ? few<64, 4>(a, bf, kvm, grid, st) : rows > 16 ? few<64, 2>(a, bf, kvm, grid, st) : few<64, 1>(a, bf, kvm, grid, st);

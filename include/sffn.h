@@ -390,7 +390,7 @@ int sffn_attn_mass(sffn_kv cache, sffn_seqs seqs, const int32_t* seq_len, int ty
  * new token's whatever its position, but a sliding window would count slots. The pages of the sequences must be their own (not
  * shared between rows of the table). A move into a page outside the cache loses the token. sinks, recent >= 0, sinks + recent <= keep;
  * 1 <= keep <= W; S, n_kv_heads and W as in sffn_attn_mass. cache: its 16-bit type or 8-bit as elsewhere. Limits of cache and table as in sffn_kv_write.
- * The workspace needs sffn_kv_evict_workspace_size bytes. Two kernels. */
+ * The workspace needs sffn_kv_evict_workspace_size bytes. Two kernels up to W = 8192, five above. */
 size_t sffn_kv_evict_workspace_size(int S, int n_kv_heads, int W, int keep);
 int sffn_kv_evict(sffn_kv cache, const int32_t* kv_len, const int32_t* seq_len, const int32_t* table, int S, int max_pages,
                   int table_stride, const float* mass, const int32_t* pos, int W, int keep, int sinks, int recent, int32_t* src,

@@ -371,6 +371,22 @@ def test_mass_after_attn(gpu_ready):
             assert bool(((per - ns[s] * G).abs() <= 1e-3 * ns[s] * G).all())
 
 
+def test_mass_far_max_q(gpu_ready):
+    """max_q is an upper bound, up to the largest int: also where its product with the shared heads passes 32 bits."""
+    dev, Hq, Hkv, d = gpu_ready, 8, 2, 64
+    for n in (9, 70):
+        b = Paged([n], [200], Hkv, d, 16, "f16", "f16", seed=n)
+        q = torch.randn((b.T, Hq, d), generator=b.g).to(DT["f16"])
+        _, lse, _, _ = attention(b, q, Hq, 0.1)
+        lse = lse.float()
+        old = torch.rand((1, Hkv, b.cols * 16), generator=b.g)
+        want, tol = mass(b, q, lse, Hq, 0.1, old)
+        for max_q in (1 << 29, 1 << 30, (1 << 30) + 1, (1 << 31) - 1):
+            say(f"[far {n} {max_q}]")
+            out, _ = mass_call(dev, b, q, lse, Hq, 0.1, old, 0, 0, max_q, 200)
+            assert_near(torch.where(torch.isnan(want), 0.0, out.cpu().double()), torch.nan_to_num(want), tol)
+
+
 # ------------------------------------------------------------------------------------------------ eviction
 EVICT = [([40, 16, 7], 16, 4, 2, 1, 16, 16, "f16"), ([1100, 1024, 1025, 30], 1024, 256, 4, 8, 128, 16, "f16"),
          ([300], 1, 0, 0, 2, 64, 32, "i8"), ([300, 299], 100, 1, 0, 3, 80, 16, "e4m3"), ([5000], 4999, 0, 0, 1, 32, 64, "bf16"),
