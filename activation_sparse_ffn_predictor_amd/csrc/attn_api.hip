@@ -164,9 +164,12 @@ MassPlan mass_plan(int S, int Hkv, int G, int d, int max_q, int max_kv, int W) {
   const int tile = sffn::mass_tile(d);
   p.tiles = (int)std::min<int64_t>((keys + tile - 1) / tile, std::max<int64_t>(1, (1 << 20) / seqs));
   const int64_t blocks = seqs * p.tiles;
-  // shares of the rows: about 2048 workgroups, eight times what runs at once, since early keys have more rows than late ones (2048 tokens
-  // over 6144, 64 heads on 8: 6 shares 350 us, 8 342, 11 317, 24 315, 32 327)
-  if (blocks < 2048) p.rs = (int)std::max<int64_t>(1, std::min({(2047 + blocks) / blocks, (rows + 511) / 512, (int64_t)16}));
+  // Shares of the rows: about 2048 workgroups, four times what runs at once, since early keys have more rows than late ones (2048
+  // tokens over 6144, 64 heads on 8: 6 shares 262 us, 8 255, 11 245, 22 262), of 512 rows or more; up to 1024 workgroups of 256 or
+  // more (700 tokens over 2000, 12 heads of 80 on 4: 5 shares 33 us, 9 24; 40 heads of 96 on 8: 7 shares 42.5, 14 37.8)
+  const int64_t fill = std::min({(2047 + blocks) / blocks, (rows + 511) / 512, (int64_t)16}),
+                few = std::min({(1023 + blocks) / blocks, (rows + 255) / 256, (int64_t)32});
+  if (blocks < 2048) p.rs = (int)std::max<int64_t>(1, std::max(fill, few));
   p.wp = p.tiles * tile;
   return p;
 }

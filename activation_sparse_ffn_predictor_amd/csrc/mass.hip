@@ -54,7 +54,8 @@ __device__ __forceinline__ uint4 codes8_bf16(uint2 c) {
 // ------------------------------------------------------------------------------------------------ few rows
 // Up to 16 * QB rows (single tokens, drafts): the queries stay in registers, every wave runs through its own units of 32 keys.
 // S = Q K^T (16x16x32): a lane's column is a key, its registers are rows, so a key's sum needs two exchanges for 16 keys.
-// Bound by K's bytes. KVM 0: cache of the queries' type, 1: int8, 2: e4m3 (products in fp16, bf16 queries brought into its
+// Bound by K's bytes (32 sequences to 6000 tokens on 40 heads, int8, 467 MB: 99 us, 4.7 TB/s; a large copy reaches 5.55, reading alone
+// 5.9; page ids ahead of the loads that need them: 130 -> 113). KVM 0: cache of the queries' type, 1: int8, 2: e4m3 (products in fp16, bf16 queries brought into its
 // range by one power of two). DP: head size padded.
 template <bool BF, int KVM, int DP, int QB>
 __global__ __launch_bounds__(256) void k_mass_few(MassArgs a) {
@@ -206,6 +207,10 @@ __global__ __launch_bounds__(256) void k_mass_few(MassArgs a) {
 // K stays in registers (KT tiles of 32 keys a wave), the queries stream through LDS, 64 rows at a time, shared by the waves.
 // S^T = K Q^T (32x32x16): a lane's column is a row, so it holds one log-sum-exp a tile, and keys' sums stay in its registers
 // until the rows are through; 32 lanes are joined once. 8-bit codes are widened once, exactly, to the queries' type.
+// Bound by exponentials and matrix products together: for 64 scores the vector unit needs 16 cycles (a multiply-add, an exponential, an
+// addition), and so does the matrix core for products of 128 elements; what each leaves idle the other cannot wholly use (a step of
+// one matrix instruction, two exponentials and four others takes 24 ns where the instruction alone takes 18.6). 2048 tokens over 6144,
+// 64 heads on 8, 172 GFLOP: 220 to 250 us on different cards; KT = 1 takes a sixth more.
 constexpr int MROWS = 64;
 template <bool BF, int KVM, int DP, int KT>
 __global__ __launch_bounds__(256, 2) void k_mass_many(MassArgs a) {
@@ -214,9 +219,16 @@ __global__ __launch_bounds__(256, 2) void k_mass_many(MassArgs a) {
   __shared__ __align__(16) char qs[2][MROWS * RB];
   __shared__ float Ls[2][MROWS];
   __shared__ int ps[2][MROWS];
+  __shared__ __align__(16) float fk[C8 ? 4 : 1][KT * 32];    // 8-bit: scales of the waves' keys times the softmax scale
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, hi = l >> 5, lc = l & 31;
-  const int hk = blockIdx.y, s = blockIdx.z, d = a.kv.d, G = a.G;
-  const int share = blockIdx.x % a.rs, first = blockIdx.x / a.rs, tiles = gridDim.x / a.rs;   // (keys' tiles: 0 .. tiles - 1 shared out)
+  const int d = a.kv.d, G = a.G, tiles = a.wp / WG;  // (keys' tiles: 0 .. tiles - 1 shared out)
+  // early keys have the most rows: theirs go first. K/V heads are neighbours: with 8 of them an XCD reads one head's rows
+  uint32_t id = blockIdx.x;
+  const int hk = id % a.kv.hkv;
+  id /= a.kv.hkv;
+  const int share = id % a.rs;
+  id /= a.rs;
+  const int s = id % a.sq.S, first = id / a.sq.S;
   const MassSeq m = mass_seq(a, s);
   if (m.q.n == 0 || m.rows == 0 || m.keys <= 0) return;
   const int* trow = a.sq.table + (long)s * a.sq.ldt;
@@ -229,7 +241,6 @@ __global__ __launch_bounds__(256, 2) void k_mass_many(MassArgs a) {
     const int wk = kt * WG + w * KT * 32;            // the wave's first key
     // K: lane holds key lc of each tile, 8 elements at 16 ks + 8 hi
     uint4 kf[KT][KS];
-    float f[KT][16];
     uint32_t held[KT];
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
@@ -254,10 +265,16 @@ __global__ __launch_bounds__(256, 2) void k_mass_many(MassArgs a) {
           }
         }
       }
-      const float sk = C8 ? (ok ? a.kv.ks[r] : 0.f) * a.c : a.c;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) f[t][i] = C8 ? __shfl(sk, 8 * (i >> 2) + 4 * hi + (i & 3), 32) : a.c;
+      if (C8 && hi == 0) fk[w][t * 32 + lc] = ok ? a.kv.ks[r] * a.c : 0.f;
     }
+    // factors of the scores 4 j .. 4 j + 3 of a lane and tile (written by this wave, and read behind the barrier below)
+    auto factors = [&](int t, int j) {
+      if constexpr (C8) return *reinterpret_cast<const f32x4*>(fk[w] + t * 32 + 8 * j + 4 * hi);
+      else return f32x4{a.c, a.c, a.c, a.c};
+    };
+    bool every = true;                               // are all of the wave's keys held?
+#pragma unroll
+    for (int t = 0; t < KT; ++t) every &= held[t] == 0xFFFFFFFFu;
     float sum[KT][16];
 #pragma unroll
     for (int t = 0; t < KT; ++t)
@@ -276,16 +293,20 @@ __global__ __launch_bounds__(256, 2) void k_mass_many(MassArgs a) {
       n_t = min(n_t, t_0 + per);
     }
 
-    // A thread's rows of a tile, and of its statistics: token and query head of each are kept and moved on a tile at a time
-    constexpr int RPL = 256 / CPR;                   // rows a load of the workgroup covers
+    // A thread's rows of a tile: a load of the workgroup covers RPL of them. Where the query heads divide that, a thread's place in a
+    // token is the same in all, and loads differ by a number of tokens only (the wave's own arithmetic); else token and head of
+    // its first row are moved on a tile at a time.
+    constexpr int RPL = 256 / CPR;
     const int ch = threadIdx.x % CPR, row = threadIdx.x / CPR, r_0 = r0 + t_0 * MROWS, step_i = MROWS / G, step_g = MROWS - step_i * G;
-    int ti[LOADS], tg[LOADS], si = (r_0 + (int)(threadIdx.x % MROWS)) / G, sg = r_0 + threadIdx.x % MROWS - si * G, left = r1 - r_0;
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      ti[i] = (r_0 + i * RPL + row) / G;
-      tg[i] = r_0 + i * RPL + row - ti[i] * G;
-    }
-    const char* qb = a.q + ((long)m.q.q0 * a.ldq + (long)hk * G * d) * 2 + ch * 16;
+    const bool even = RPL % G == 0 && a.ldq <= 1 << 24, chunk = ch * 8 < d;
+    int ti = (r_0 + row) / G, tg = r_0 + row - ti * G, si = (r_0 + (int)(threadIdx.x % MROWS)) / G, sg = r_0 + threadIdx.x % MROWS - si * G,
+        left = r1 - r_0;
+    // positions of a tile's first and last row
+    int pa_i = m.q.p0 + r_0 / G, pa_g = r_0 % G, pb_i = m.q.p0 + (r_0 + MROWS - 1) / G, pb_g = (r_0 + MROWS - 1) % G;
+    const char* qb = a.q + ((long)m.q.q0 * a.ldq + (long)hk * G * d) * 2;
+    const char* qt = qb + (long)(r_0 / G) * (a.ldq * 2);
+    const long step_t = (long)(RPL / G) * (a.ldq * 2);
+    const uint32_t mine = (uint32_t)(row / G) * (uint32_t)(a.ldq * 2) + (uint32_t)(row % G * d * 2 + ch * 16);
     const float* lb = a.lse + (long)m.q.q0 * a.hq + hk * G;
     auto on = [&](int& i, int& g) {
       g += step_g;
@@ -293,14 +314,31 @@ __global__ __launch_bounds__(256, 2) void k_mass_many(MassArgs a) {
       g -= g >= G ? G : 0;
     };
     uint4 st[LOADS];
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) st[i] = make_uint4(0, 0, 0, 0);
     float sl = 0.f;
     int sp = 0;
-    auto fetch = [&] {                               // the next tile's
+    // the next tile's (rows behind the last one keep what was there: they see nothing)
+    auto fetch = [&] {
+      if (chunk) {
+        if (even && left >= MROWS) {
 #pragma unroll
-      for (int i = 0; i < LOADS; ++i) {
-        st[i] = make_uint4(0, 0, 0, 0);
-        if (i * RPL + row < left && ch * 8 < d) st[i] = *reinterpret_cast<const uint4*>(qb + (long)ti[i] * (a.ldq * 2) + tg[i] * d * 2);
-        on(ti[i], tg[i]);
+          for (int i = 0; i < LOADS; ++i) st[i] = *reinterpret_cast<const uint4*>(qt + i * step_t + mine);
+        } else {
+#pragma unroll
+          for (int i = 0; i < LOADS; ++i) {
+            int g = tg + i * RPL % G, n = ti + i * RPL / G;
+            n += g >= G;
+            g -= g >= G ? G : 0;
+            if (i * RPL + row < left) st[i] = *reinterpret_cast<const uint4*>(qb + (long)n * (a.ldq * 2) + g * d * 2 + ch * 16);
+          }
+        }
+      }
+      if (even) {
+        qt += LOADS * step_t;
+        ti += step_i;
+      } else {
+        on(ti, tg);
       }
       if (threadIdx.x < MROWS) {
         sl = (int)threadIdx.x < left ? lb[(long)si * a.hq + sg] : -INFINITY;
@@ -325,10 +363,83 @@ __global__ __launch_bounds__(256, 2) void k_mass_many(MassArgs a) {
       __syncthreads();                               // (a former tile's readers are through)
       put(0);
     }
-    for (int t = t_0; t < n_t; ++t) {
-      const int b = (t - t_0) & 1;
+    int t = t_0, b = 0;
+    bool whole = false;
+    // tile t is in LDS, the next one is fetched; is it one that every row sees whole?
+    auto next = [&] {
       __syncthreads();
       if (t + 1 < n_t) fetch();
+      whole = DP <= 128 && every && all_seen(a, pa_i, pb_i, wk, wk + KT * 32 - 1) && __all(ps[b][l] >= 0);
+      on(pa_i, pa_g);
+      on(pb_i, pb_g);
+    };
+    if (t < n_t) next();
+    while (t < n_t) {
+      // Such a tile: a product of 32 x 32 scores runs on the matrix core under the former one's exponentials (a loop of its own, so that
+      // the sums stay in their registers). 2048 tokens over 6144, 64 heads on 8: 262 -> 235 us; head sizes over 128 have no registers
+      // left for it (32 on 4 of 256: 268 -> 293).
+      while (whole) {
+        constexpr int N = MROWS / 32 * KT * KS, EL = 16 / KS;  // steps of one matrix instruction; scores a step
+        uint4 qv[KS];
+        f32x16 sc[2];
+        f32x4 fc = factors(0, 0), fn = fc;           // this step's factors and the next ones
+        float L[MROWS / 32], z[EL], e[EL];
+        auto q16 = [&](int h, int ks) {
+          const int row = h * 32 + lc;
+          return *reinterpret_cast<const uint4*>(qs[b] + row * RB + (((ks * 2 + hi) ^ (row & (CPR - 1))) << 4));
+        };
+        auto product = [&](int n) {
+          const int ks = n % KS, x = n / KS % KT, h = n / (KS * KT);
+          f32x16& now = sc[n / KS & 1];
+          if (ks == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) now[i] = 0.f;
+          }
+          now = mfma32<BF>(kf[x][ks], qv[ks], now);
+          if (x == KT - 1 && h + 1 < MROWS / 32) qv[ks] = q16(h + 1, ks);
+        };
+#pragma unroll
+        for (int h = 0; h < MROWS / 32; ++h) L[h] = Ls[b][h * 32 + lc];
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) qv[ks] = q16(0, ks);
+#pragma unroll
+        for (int n = 0; n < KS; ++n) product(n);
+        // step n adds the scores of step n - 3, takes the exponentials of those of n - 2, finds the exponents of those of n - 1 (the
+        // empty statements keep a step's instructions together)
+#pragma unroll
+        for (int n = 0; n < N + 3; ++n) {
+#pragma unroll
+          for (int i = 0; i < EL; ++i) {
+            if (n > 2) {
+              float& to = sum[(n - 3) / KS % KT][(n - 3) % KS * EL + i];
+              to += e[i];
+              asm volatile("" : "+v"(to));
+            }
+            if (n > 1 && n < N + 2) {
+              e[i] = exp2_fast(z[i]);
+              asm volatile("" : "+v"(e[i]));
+            }
+            if (n > 0 && n < N + 1) {
+              const int x = (n - 1) / KS, c = (n - 1) % KS * EL + i;
+              if (c % 4 == 0) {
+                fc = fn;
+                fn = factors((x + c / 12) % KT, (c / 4 + 1) % 4);
+              }
+              z[i] = fmaf(sc[x & 1][c], fc[c % 4], -L[x / KT]);
+              asm volatile("" : "+v"(z[i]));
+            }
+          }
+          if (n + KS < N) product(n + KS);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (t + 1 < n_t) put(b ^ 1);
+        whole = false;
+        if (++t < n_t) {
+          b ^= 1;
+          next();
+        }
+      }
+      if (t >= n_t) break;
 #pragma unroll
       for (int h = 0; h < MROWS / 32; ++h) {
         const int row = h * 32 + lc;
@@ -351,7 +462,7 @@ __global__ __launch_bounds__(256, 2) void k_mass_many(MassArgs a) {
           const int ka = wk + x * 32;
           if (lines && held[x] == 0xFFFFFFFFu && all_seen(a, pa, pb, ka, ka + 31)) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sum[x][i] += exp2_fast(fmaf(sc[x][i], f[x][i], -L));
+            for (int i = 0; i < 16; ++i) sum[x][i] += exp2_fast(fmaf(sc[x][i], factors(x, i >> 2)[i & 3], -L));
           } else if (some_seen(a, pa, pb, ka, ka + 31)) {
             // this lane's row sees its keys up to `last`, from `from` on or before `sink`, where they are held (the numbers are hidden
             // from the compiler, which would keep 32 comparisons' results over the loop)
@@ -362,7 +473,7 @@ __global__ __launch_bounds__(256, 2) void k_mass_many(MassArgs a) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const int kk = 8 * (i >> 2) + (i & 3);
-              const float e = exp2_fast(fmaf(sc[x][i], f[x][i], -L));
+              const float e = exp2_fast(fmaf(sc[x][i], factors(x, i >> 2)[i & 3], -L));
               const bool see = (kk <= last) & ((kk > from) | (kk < sink)) & (((have >> kk) & 1) != 0);
               sum[x][i] += see ? e : 0.f;
             }
@@ -370,6 +481,10 @@ __global__ __launch_bounds__(256, 2) void k_mass_many(MassArgs a) {
         }
       }
       if (t + 1 < n_t) put(b ^ 1);
+      if (++t < n_t) {
+        b ^= 1;
+        next();
+      }
     }
     // over the 32 lanes of each half; lane i (of 16) of a half then takes key register i
 #pragma unroll
@@ -429,7 +544,7 @@ hipError_t sffn_launch_mass(const MassArgs& a, int qt, int kvt, int tiles, hipSt
     if (d <= 128) return rows > 32 ? few<128, 4>(a, bf, kvm, grid, st) : rows > 16 ? few<128, 2>(a, bf, kvm, grid, st) : few<128, 1>(a, bf, kvm, grid, st);
     return rows > 16 ? few<256, 2>(a, bf, kvm, grid, st) : few<256, 1>(a, bf, kvm, grid, st);
   }
-  const dim3 grid(tiles * a.rs, a.kv.hkv, a.sq.S);
+  const dim3 grid((unsigned)tiles * a.rs * a.kv.hkv * a.sq.S);
   const hipError_t e = d <= 64 ? many<64, 2>(a, bf, kvm, grid, st) : d <= 128 ? many<128, 2>(a, bf, kvm, grid, st) : many<256, 1>(a, bf, kvm, grid, st);
   if (e != hipSuccess || a.rs == 1) return e;
   hipLaunchKernelGGL(k_mass_join, dim3((a.wp + 255) / 256, a.kv.hkv, a.sq.S), dim3(256), 0, st, a);

@@ -3,6 +3,8 @@
 // A scale below 2^-60 becomes 0 (codes 0), a block with an infinity or NaN gets the scale NaN (codes 0), as in the cache.
 //
 // Bound by memory: x read and the codes written, once each (a block stays in registers between its maximum and its codes).
+// Measured: 10184 x 8192 fp32 in blocks of 128 rows, 417 MB, 73 us (5.7 TB/s; a large copy reaches 5.55); 4099 x 8192 bf16 rows, 101 MB,
+// 21 us (4.8); one row 3.9 us a call, its host side.
 #include "codes.h"
 
 using namespace sffn;
