@@ -262,7 +262,9 @@ MASS = [([1], [1], 1, 1, 16, 16, "f16", "f16", 0, 0, 0), ([1], [500], 64, 8, 128
         ([257, 1, 0, 90], [600, 5, 40, 300], 12, 4, 80, 32, "f16", "f16", 0, 0, 1), ([150], [1000], 8, 1, 128, 128, "f16", "i8", 200, 16, 0),
         ([150, 20], [700, 333], 4, 4, 256, 64, "bf16", "e4m3", 0, 0, 0), ([200], [900], 8, 2, 72, 16, "bf16", "bf16", 33, 5, 2),
         ([1000], [1000], 16, 2, 64, 32, "f16", "f16", 0, 0, 0), ([40, 40], [2000, 40], 16, 8, 16, 16, "bf16", "e4m3", 0, 0, 0),
-        ([300], [520], 8, 1, 160, 16, "f16", "i8", 0, 0, 0), ([64], [64], 1, 1, 256, 16, "f16", "f16", 7, 2, 0)]
+        ([300], [520], 8, 1, 160, 16, "f16", "i8", 0, 0, 0), ([64], [64], 1, 1, 256, 16, "f16", "f16", 7, 2, 0),
+        ([300], [900], 24, 2, 128, 16, "bf16", "i8", 0, 0, 0), ([130, 400], [500, 700], 9, 3, 64, 32, "f16", "e4m3", 0, 0, 2),
+        ([333], [1200], 20, 4, 96, 16, "bf16", "bf16", 300, 9, 0), ([600], [600], 8, 8, 112, 16, "f16", "e4m3", 0, 0, 0)]
 
 
 def mass_call(dev, b, q, lse, Hq, scale, old, window, sinks, max_q, max_kv, plen=None, in_place=False):
@@ -369,6 +371,30 @@ def test_mass_after_attn(gpu_ready):
             G = Hq // Hkv
             per = m[s].double().sum(-1).cpu()
             assert bool(((per - ns[s] * G).abs() <= 1e-3 * ns[s] * G).all())
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,kvt", [(16, 2, 128, "bf16"), (6, 2, 64, "i8"), (4, 1, 256, "e4m3")])
+def test_mass_strided_rows(gpu_ready, Hq, Hkv, d, kvt):
+    """Queries that are a part of wider rows, whose other parts hold NaN: the bits of the call on their copy."""
+    dev = gpu_ready
+    for ns, ks in (([1, 3], [70, 90]), ([200, 37], [500, 300])):
+        b = Paged(ns, ks, Hkv, d, 16, "bf16", kvt, seed=d)
+        wide = torch.full((b.T, Hq + 3, d), math.nan, dtype=DT["bf16"])
+        wide[:, 2:2 + Hq] = torch.randn((b.T, Hq, d), generator=b.g).to(DT["bf16"])
+        _, lse, _, _ = attention(b, wide[:, 2:2 + Hq], Hq, 0.1)
+        kv, cu, kl, tab = b.gpu(dev)
+        old = torch.rand((2, Hkv, b.cols * 16), generator=b.g).to(dev)
+        q, l = wide.to(dev)[:, 2:2 + Hq], lse.float().to(dev)
+        need = _lib.attn_mass_workspace_size(2, Hq, Hkv, d, max(ns), max(ks), old.shape[2])
+        ws = torch.full((need,), 255, dtype=torch.uint8, device=dev) if need else None
+        got = []
+        for x in (q, q.contiguous()):
+            out, pos = old.clone(), torch.zeros(old.shape, dtype=torch.int32, device=dev)
+            say(f"[strided {Hq} {Hkv} {d} {kvt} {ns} {x.stride(0)}]")
+            _lib.attn_mass(x, kv, cu, kl, tab, max(ns), max(ks), l, out, pos, ws, scale=0.1)
+            torch.cuda.synchronize()
+            got.append(out)
+        assert torch.equal(*got) and bool(torch.isfinite(got[0]).all())
 
 
 def test_mass_far_max_q(gpu_ready):
