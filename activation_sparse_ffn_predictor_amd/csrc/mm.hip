@@ -120,8 +120,8 @@ __global__ __launch_bounds__(NW * 64) void k_mm_few(MmArgs a) {
 // ------------------------------------------------------------------------------------------------ some tokens
 // BN rows of B x BT tokens a workgroup of WN x WT waves, for calls that B's bytes or a few tiles bound: four blocks of k in LDS,
 // three of them on their way (direct loads) while one is multiplied; k may be spread over workgroups, whose fp32 partial results
-// a second kernel adds up in order. Swizzle as below. 37 x 15360 x 5120, 80 MB: 24.5 us (3.3 TB/s; the operands' way through LDS and
-// their widening to fp16 do not wholly hide behind the loads); 10240 rows of K = 8192: 16 tokens 22.5 us, 64 29.
+// a second kernel adds up in order. Swizzle as below. 37 x 15360 x 5120, 80 MB: 23.3 us (3.4 TB/s; the operands' way through LDS and
+// their widening to fp16 do not wholly hide behind the loads); 10240 rows of K = 8192: 16 tokens 22.5 us, 64 30.
 template <int OT, bool EXACT, int BN, int BT, int WN, int WT>
 __global__ __launch_bounds__(WN * WT * 64) void k_mm_some(MmArgs a, int ks) {
   constexpr int W = WN * WT, MI = BN / WN / 16, NI = BT / WT / 16, FC = 32;   // FC: blocks whose factors LDS holds
@@ -390,10 +390,10 @@ __global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a, int ks) {
 }
 
 // Which kernel, and over how many workgroups k is spread: the sum of measured costs decides. Workgroups take a block of k in `one`
-// us when a compute unit has one of them and in `all` when it has as many as fit; a join starts in 4 us and moves each partial
-// result out and in at 5 TB/s. 10240 rows of K = 8192, us: 128 tokens SOME128 40, TILE128 in three shares 31; 256 tokens TILE128 59, in
-// three shares 45; 512 tokens TILE128 82, TILE256 in three shares 63; 1024 tokens TILE128 128, TILE256
-// 109; 2048 tokens 204 and 218; 4096 TILE256 340.
+// us when a compute unit has one of them and in `all` when it has as many as fit, at least a round of them; a join starts in 4 us and
+// moves each partial result out and in at 5 TB/s. 10240 rows of K = 8192, us: 64 tokens SOME64 41, in three shares 30; 128 tokens
+// SOME128 40, TILE128 in three shares 31; 256 tokens TILE128 59, in three shares 45; 512 tokens TILE128 82, TILE256 in three shares 63;
+// 1024 tokens TILE128 128, TILE256 109; 2048 tokens 204 and 218; 4096 TILE256 340.
 enum { FEW, SOME32, SOME64, SOME128, TILE128, TILE256 };
 struct Shape {
   int n, t, fit;                                   // rows and tokens of a workgroup, workgroups a compute unit
@@ -417,7 +417,7 @@ Plan plan(int T, int N, int K, bool f32) {
     const double tiles = (double)((N + c.n - 1) / c.n) * ((T + c.t - 1) / c.t);
     for (const int ks : {1, 2, 3, 4, 6, 8}) {
       if (ks > 1 && (KB < 4 * ks || tiles * ks > 512)) break;
-      const double wgs = tiles * ks, fit = 256.0 * c.fit, turns = c.fit == 1 ? ceil(wgs / fit) : std::max(wgs / fit, ceil(wgs / fit) - 0.4);
+      const double wgs = tiles * ks, fit = 256.0 * c.fit, turns = c.fit == 1 ? ceil(wgs / fit) : std::max({1.0, wgs / fit, ceil(wgs / fit) - 0.4});
       double us = turns * ((KB + ks - 1) / ks) * (wgs <= 256 ? c.one : c.all);
       if (ks > 1) us += 4.0 + (double)ks * T * N * 8 / 5e6;
       if (least == 0 || us < least) best = {how, ks}, least = us;
