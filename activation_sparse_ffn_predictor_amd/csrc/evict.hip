@@ -8,8 +8,8 @@
 // 10 bits) with counts in LDS. Up to 8192 slots one workgroup does all of it with the keys in registers; more slots are spread
 // over workgroups, a kernel a digit, since one workgroup's passes are bound by its instructions (6 x 8 heads of 40001 slots in
 // 48 workgroups: 69 us; by kernels of a digit 9.6 + 6.4 + 6.4, what moves 11.7). Each of them is a chain of dependent loads and
-// barriers rather than bytes. The moves are bound by memory: the moved rows in and out (86 MB of rows of 128 bytes: 23 us, 3.7
-// TB/s). 4 x 8 heads of 1100 slots: 9.3 + 3 us.
+// barriers rather than bytes. The moves are bound by memory: the moved rows in and out (115 MB with rows of 128 bytes: 20 to 24
+// us). 4 x 8 heads of 1100 slots: 9.3 + 3 us.
 #include "evict.h"
 
 using namespace sffn;
@@ -368,9 +368,11 @@ __global__ __launch_bounds__(NT) void k_emit(EvictArgs a) {
   if (ch.end > ch.begin) emit<true>(sl, a, sh, cut, ties, start[0], start[1], start[2], tmp, nullptr);
 }
 
-// The moves, `rest` workgroups a sequence and head: LPR lanes a row, 16 bytes each of K and V; its scales, weight and position.
+// The moves, `rest` workgroups a sequence and head: LPR lanes a row, 16 bytes each of K and V; its scales, weight and position. ROWS rows
+// at a time, since each waits for a chain of four loads (6 x 8 heads, 115 MB: one row 23 us, four 20), one where that leaves places
+// free (4 x 8 heads, up to 76 rows each: one 3.0 us, four 4.0).
 // Behind them workgroups for the weights and positions of tokens that stay where they are, a thread a slot, and the lengths.
-template <int LPR>
+template <int LPR, int ROWS>
 __global__ __launch_bounds__(256) void k_move(EvictArgs a, int eb, int rest) {
   const int hk = blockIdx.x % a.kv.hkv, s = blockIdx.x / a.kv.hkv % a.S, g = blockIdx.x / a.kv.hkv / a.S;
   const long sh = (long)s * a.kv.hkv + hk;
@@ -383,29 +385,63 @@ __global__ __launch_bounds__(256) void k_move(EvictArgs a, int eb, int rest) {
     if (a.pos_out != a.pos) a.pos_out[sh * a.W + j] = a.pos[sh * a.W + j];
     return;
   }
-  const int lane = threadIdx.x % LPR, i = g * (256 / LPR) + threadIdx.x / LPR;
-  if (i >= a.moves[sh]) return;
-  const int f = a.from[sh * a.keep + i], t = a.to[sh * a.keep + i];
-  if (lane == 0) {
-    a.src[sh * a.keep + t] = f;
-    a.mass_out[sh * a.W + t] = a.mass[sh * a.W + f];
-    a.pos_out[sh * a.W + t] = a.pos[sh * a.W + f];
-  }
+  const int lane = threadIdx.x % LPR, first = g * (ROWS * (256 / LPR)), n = a.moves[sh];
+  if (first >= n) return;
   const int* trow = a.table + (long)s * a.ldt;
-  const int mask = (1 << a.kv.psh) - 1, pf = trow[f >> a.kv.psh], pt = trow[t >> a.kv.psh];
-  if ((unsigned)pf >= (unsigned)a.kv.n_pages || (unsigned)pt >= (unsigned)a.kv.n_pages) return;
-  const long rf = (((long)pf * a.kv.hkv + hk) << a.kv.psh) + (f & mask), rt = (((long)pt * a.kv.hkv + hk) << a.kv.psh) + (t & mask);
-  const int row = a.kv.d * eb;
-  if (lane * 16 < row) {
-    const uint4 k = *reinterpret_cast<const uint4*>(a.kv.k + rf * row + lane * 16);
-    const uint4 v = *reinterpret_cast<const uint4*>(a.kv.v + rf * row + lane * 16);
-    *reinterpret_cast<uint4*>(a.kv.k + rt * row + lane * 16) = k;
-    *reinterpret_cast<uint4*>(a.kv.v + rt * row + lane * 16) = v;
+  const int mask = (1 << a.kv.psh) - 1, row = a.kv.d * eb;
+  int f[ROWS], t[ROWS], pf[ROWS], pt[ROWS];
+  bool in[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    const int i = first + r * (256 / LPR) + threadIdx.x / LPR;
+    in[r] = i < n;
+    f[r] = a.from[sh * a.keep + min(i, n - 1)];
+    t[r] = a.to[sh * a.keep + min(i, n - 1)];
   }
-  if (eb == 1 && lane == 0) {
-    a.kv.ks[rt] = a.kv.ks[rf];
-    a.kv.vs[rt] = a.kv.vs[rf];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    pf[r] = trow[f[r] >> a.kv.psh];
+    pt[r] = trow[t[r] >> a.kv.psh];
   }
+  long rf[ROWS], rt[ROWS];
+  bool held[ROWS];
+  uint4 k[ROWS], v[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    held[r] = in[r] && (unsigned)pf[r] < (unsigned)a.kv.n_pages && (unsigned)pt[r] < (unsigned)a.kv.n_pages;
+    rf[r] = (((long)(held[r] ? pf[r] : 0) * a.kv.hkv + hk) << a.kv.psh) + (f[r] & mask);
+    rt[r] = (((long)(held[r] ? pt[r] : 0) * a.kv.hkv + hk) << a.kv.psh) + (t[r] & mask);
+    k[r] = v[r] = make_uint4(0, 0, 0, 0);
+    if (held[r] && lane * 16 < row) {
+      k[r] = *reinterpret_cast<const uint4*>(a.kv.k + rf[r] * row + lane * 16);
+      v[r] = *reinterpret_cast<const uint4*>(a.kv.v + rf[r] * row + lane * 16);
+    }
+  }
+  // lane r takes what row r has besides
+  int mf = f[0], mt = t[0];
+  long mrf = rf[0], mrt = rt[0];
+  bool mine = in[0], mheld = held[0];
+#pragma unroll
+  for (int r = 1; r < ROWS; ++r)
+    if (lane == r) mf = f[r], mt = t[r], mrf = rf[r], mrt = rt[r], mine = in[r], mheld = held[r];
+  if (lane < ROWS && mine) {
+    const float mass = a.mass[sh * a.W + mf];
+    const int pos = a.pos[sh * a.W + mf];
+    a.src[sh * a.keep + mt] = mf;
+    if (eb == 1 && mheld) {
+      const float ks = a.kv.ks[mrf], vs = a.kv.vs[mrf];
+      a.kv.ks[mrt] = ks;
+      a.kv.vs[mrt] = vs;
+    }
+    a.mass_out[sh * a.W + mt] = mass;
+    a.pos_out[sh * a.W + mt] = pos;
+  }
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r)
+    if (held[r] && lane * 16 < row) {
+      *reinterpret_cast<uint4*>(a.kv.k + rt[r] * row + lane * 16) = k[r];
+      *reinterpret_cast<uint4*>(a.kv.v + rt[r] * row + lane * 16) = v[r];
+    }
 }
 
 }  // namespace
@@ -425,11 +461,18 @@ hipError_t sffn_launch_evict(const EvictArgs& a, int kvt, hipStream_t st) {
   const int eb = kvt == T_I8 || kvt == T_E4M3 ? 1 : 2, row = a.kv.d * eb;
   // at most as many rows move as there are slots on either side of `keep`
   const int lpr = row <= 64 ? 4 : row <= 128 ? 8 : row <= 256 ? 16 : 32, rows = most - a.keep < a.keep ? most - a.keep : a.keep;
-  const int rest = rows > 0 ? (rows + 256 / lpr - 1) / (256 / lpr) : 0, groups = rest + (a.keep + 255) / 256;
+  const int slots = 256 / lpr, each = (long)rows * a.kv.hkv * a.S > 4096l * slots ? 4 * slots : slots,
+            rest = rows > 0 ? (rows + each - 1) / each : 0, groups = rest + (a.keep + 255) / 256;
   const dim3 moves((unsigned)groups * a.kv.hkv * a.S);
-  if (lpr == 4) hipLaunchKernelGGL(k_move<4>, moves, dim3(256), 0, st, a, eb, rest);
-  else if (lpr == 8) hipLaunchKernelGGL(k_move<8>, moves, dim3(256), 0, st, a, eb, rest);
-  else if (lpr == 16) hipLaunchKernelGGL(k_move<16>, moves, dim3(256), 0, st, a, eb, rest);
-  else hipLaunchKernelGGL(k_move<32>, moves, dim3(256), 0, st, a, eb, rest);
+#define GO(LPR)                                                                                 \
+  do {                                                                                          \
+    if (each > slots) hipLaunchKernelGGL((k_move<LPR, 4>), moves, dim3(256), 0, st, a, eb, rest); \
+    else hipLaunchKernelGGL((k_move<LPR, 1>), moves, dim3(256), 0, st, a, eb, rest);            \
+  } while (0)
+  if (lpr == 4) GO(4);
+  else if (lpr == 8) GO(8);
+  else if (lpr == 16) GO(16);
+  else GO(32);
+#undef GO
   return hipGetLastError();
 }

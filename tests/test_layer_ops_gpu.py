@@ -417,7 +417,10 @@ def test_mass_far_max_q(gpu_ready):
 EVICT = [([40, 16, 7], 16, 4, 2, 1, 16, 16, "f16"), ([1100, 1024, 1025, 30], 1024, 256, 4, 8, 128, 16, "f16"),
          ([300], 1, 0, 0, 2, 64, 32, "i8"), ([300, 299], 100, 1, 0, 3, 80, 16, "e4m3"), ([5000], 4999, 0, 0, 1, 32, 64, "bf16"),
          ([9000, 8193], 3000, 500, 16, 2, 48, 128, "i8"), ([70000], 30000, 1000, 4, 1, 16, 1024, "f16"), ([64] * 20, 32, 8, 0, 2, 256, 16, "e4m3"),
-         ([600000], 250000, 70000, 5, 1, 16, 1024, "i8"), ([20000, 8200, 9000], 8500, 8000, 500, 2, 16, 64, "f16"), ([200], 200, 50, 4, 1, 24, 16, "f16"), ([130], 129, 64, 65, 2, 112, 16, "i8")]
+         ([600000], 250000, 70000, 5, 1, 16, 1024, "i8"), ([20000, 8200, 9000], 8500, 8000, 500, 2, 16, 64, "f16"), ([200], 200, 50, 4, 1, 24, 16, "f16"), ([130], 129, 64, 65, 2, 112, 16, "i8"),
+         # enough rows that several are moved at a time
+         ([20000], 9000, 100, 2, 4, 256, 16, "f16"), ([30000, 12001], 12000, 0, 0, 6, 128, 64, "bf16"),
+         ([40000, 30001], 12000, 100, 4, 6, 96, 32, "e4m3")]
 
 
 def evict_case(ks, keep, Hkv, d, page, kvt, seed=0, kind="mixed", extra=0):
