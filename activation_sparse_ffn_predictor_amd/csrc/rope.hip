@@ -2,10 +2,11 @@
 //   y = x / sqrt(mean(x^2) + eps) * w            (norm; else y = x)
 //   (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin), angle = position * freq[i], for the pairs of the first `rot` elements
 //
-// Bound by memory: q and k read and written once. Measured: 4500 tokens of 80 heads of 128, bf16, 182 MB in 42 us (4.4 TB/s; a large copy
-// reaches 5.55); one token of 72 heads 3.5 us on the device, a launch and a chain of three loads. Angles: position * freq and its reduction to turns in 64 bits, so that far
-// positions keep what fp32 would lose (at 10^6 an fp32 angle is off by 0.03), then sine and cosine of the fraction in 32; each
-// is worked out once for a token and shared by its heads through LDS.
+// Bound by memory: q and k read and written once. Measured: 4500 tokens of 80 heads of 128, bf16, 182 MB in 40.5 us (4.5 TB/s; a large
+// copy reaches 5.55; two to eight tokens a workgroup, or fewer registers, are slower); one token of 72 heads 3.5 us on the device, a
+// launch and a chain of three loads. Angles: position * freq and its reduction to turns in 64 bits, so that far positions keep what
+// fp32 would lose (at 10^6 an fp32 angle is off by 0.03), then sine and cosine of the fraction in 32; each is worked out once for a
+// token and shared by its heads through LDS.
 #include "attn.h"
 
 using namespace sffn;
@@ -74,6 +75,7 @@ __global__ __launch_bounds__(256) void k_rope(RopeArgs a, int tokens, int shares
   const int here = min(tokens, min(a.T, max(a.cu[a.S], 0)) - t0);      // rows behind the last sequence stay as they are
   if (here <= 0 || nh <= 0) return;
   const int m = a.rot >> 1, items = here * nh;
+  const float over_d = 1.f / (float)a.d, eps = (float)a.eps;
   const int slot = threadIdx.x / LPH, l = threadIdx.x % LPH;
   // rotated in halves, the pieces behind the rotated part are neighbours instead
   const bool halves = !a.inter && m > 0, half = halves && l * P < m, act = l * 2 * P < a.d;
@@ -128,9 +130,10 @@ __global__ __launch_bounds__(256) void k_rope(RopeArgs a, int tokens, int shares
 #pragma unroll
       for (int j = 0; j < P; ++j) sum = fmaf(x[0][j], x[0][j], fmaf(x[1][j], x[1][j], sum));
       sum = group_sum<LPH>(sum);
-      const float mean = sum / (float)a.d + (float)a.eps;
+      const float mean = fmaf(sum, over_d, eps);
       if (mean >= 1e-30f && mean < INFINITY) {
-        const float rs = 1.0f / sqrtf(mean);
+        // the unit's estimate and one step of Newton's method (a division and a root in full: 41.2 us for 40.5 of the tokens above)
+        const float near = __builtin_amdgcn_rsqf(mean), rs = fmaf(0.5f * near, fmaf(-mean * near, near, 1.f), near);
 #pragma unroll
         for (int j = 0; j < P; ++j) {
           x[0][j] = x[0][j] * rs * g[0][j];
