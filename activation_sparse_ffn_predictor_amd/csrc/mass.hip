@@ -66,6 +66,20 @@ __global__ __launch_bounds__(256) void k_mass_few(MassArgs a) {
   const MassSeq m = mass_seq(a, s);
   if (m.q.n == 0 || m.rows == 0 || m.keys <= 0) return;
   const bool copy = a.out != a.mass;                 // also what no row sees
+  const int* trow = a.sq.table + (long)s * a.sq.ldt;
+  const long base = ((long)s * a.kv.hkv + hk) * a.W;
+  const uint32_t dB = (uint32_t)d * EB, ko = (uint32_t)ql * dB + g4 * 16;
+  const int units = (m.keys + 31) >> 5, step = gridDim.x * 4;
+
+  // page ids are read a unit ahead of the loads that need them, which would wait for everything on its way otherwise
+  int page[2];
+  auto pages = [&](int u) {
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) page[kb] = trow[min((u * 32 + kb * 16) >> a.kv.psh, a.sq.cols - 1)];
+  };
+  int u = blockIdx.x * 4 + w;
+  if (u >= units) return;
+  pages(u);
 
   float c = a.c;
   uint4 qf[QB][KS];
@@ -84,40 +98,16 @@ __global__ __launch_bounds__(256) void k_mass_few(MassArgs a) {
     for (int e = 0; e < 4; ++e) {
       const int rr = qb * 16 + 4 * g4 + e, ii = rr / G;
       const float x = rr < m.rows ? a.lse[(long)(m.q.q0 + ii) * a.hq + hk * G + rr - ii * G] : -INFINITY;
-      pr[qb][e] = x == -INFINITY ? -1 : m.q.p0 + ii;    // rows without a sum see nothing
-      L[qb][e] = x * LOG2E;
+      pr[qb][e] = m.q.p0 + ii;
+      L[qb][e] = x;
     }
   }
-  if constexpr (C8 && BF) {
-    float big = 0.f;
-#pragma unroll
-    for (int qb = 0; qb < QB; ++qb)
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) big = fmaxf(big, absmax8<true>(finite_only<true>(qf[qb][ks])));
-    const float up = to_f16_range(wave_max(big), c);
-#pragma unroll
-    for (int qb = 0; qb < QB; ++qb)
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) qf[qb][ks] = bf16_to_f16(qf[qb][ks], up);
-  }
-
-  const int* trow = a.sq.table + (long)s * a.sq.ldt;
-  const long base = ((long)s * a.kv.hkv + hk) * a.W;
-  const uint32_t dB = (uint32_t)d * EB, ko = (uint32_t)ql * dB + g4 * 16;
-  const int units = (m.keys + 31) >> 5, step = gridDim.x * 4;
-
   struct Unit {
     uint4 kr[2][KL];
     float ksc[2], old;
     int have[2];
   };
   auto visible = [&](int u) { return some_seen(a, m.q.p0, m.p1, u * 32, u * 32 + 31); };
-  // page ids are read a unit ahead of the loads that need them, which would wait for everything on its way otherwise
-  int page[2];
-  auto pages = [&](int u) {
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) page[kb] = trow[min((u * 32 + kb * 16) >> a.kv.psh, a.sq.cols - 1)];
-  };
   auto load = [&](int u, const int (&pg)[2], Unit& x) {
     const int t0 = u * 32;
     x.old = 0.f;
@@ -184,8 +174,6 @@ __global__ __launch_bounds__(256) void k_mass_few(MassArgs a) {
     if (l < 32 && j < m.keys && (copy || j >= m.q.p0 || some)) give(a, m, base, j, now.old, l < 16 ? sum[0] : sum[1]);
   };
   // a unit's loads are on their way while the one before it is worked on; two turns in one, so that nothing is copied
-  int u = blockIdx.x * 4 + w;
-  if (u >= units) return;
   auto fetch = [&](int v, Unit& x) {
     if (v >= units) return;
     const int pg[2] = {page[0], page[1]};
@@ -193,8 +181,26 @@ __global__ __launch_bounds__(256) void k_mass_few(MassArgs a) {
     load(v, pg, x);
   };
   Unit x0, x1;
-  pages(u);
   fetch(u, x0);
+  if constexpr (C8 && BF) {
+    float big = 0.f;
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb)
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) big = fmaxf(big, absmax8<true>(finite_only<true>(qf[qb][ks])));
+    const float up = to_f16_range(wave_max(big), c);
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb)
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) qf[qb][ks] = bf16_to_f16(qf[qb][ks], up);
+  }
+#pragma unroll
+  for (int qb = 0; qb < QB; ++qb)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (L[qb][e] == -INFINITY) pr[qb][e] = -1;       // rows without a sum see nothing
+      L[qb][e] *= LOG2E;
+    }
   for (; u < units; u += 2 * step) {
     fetch(u + step, x1);
     work(u, x0);
