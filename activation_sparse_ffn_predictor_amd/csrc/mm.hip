@@ -61,11 +61,12 @@ __device__ __forceinline__ Buf rows_of(const char* p, long ld, long r0, long row
 
 // ------------------------------------------------------------------------------------------------ few tokens
 // Up to 16 tokens: 16 rows of B a workgroup, whose NW waves take blocks of k in turn and are added up in LDS. Bound by B's bytes;
-// a wave has U blocks on their way all the time. 1 x 10240 x 8192, 84 MB: 18.7 us a call (4.5 TB/s with its launch).
+// a wave has U blocks on their way beside the one it multiplies, the next waves of a compute unit theirs: 1 x 10240 x 8192, 84 MB, on
+// one card: U = 4 22.2 us, 2 21.4, 1 19.8 (4.2 TB/s with its launch), with registers for twice the waves.
 template <int OT, int NW>
 __global__ __launch_bounds__(NW * 64) void k_mm_few(MmArgs a) {
   __shared__ f32x4 part[NW][64];
-  constexpr int U = 4;
+  constexpr int U = 1;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, g4 = l >> 4, ql = l & 15;
   const int n0 = blockIdx.x * 16, KB = (a.K + 127) >> 7;
   const Buf bb = rows_of(a.b, a.ldb, n0, a.N, 16, a.K), ba = rows_of(a.a, a.lda, 0, a.T, 16, a.K), bs(a.sa, (uint32_t)a.T * KB * 4),
