@@ -123,12 +123,22 @@ __global__ __launch_bounds__(256) void k_mass_few(MassArgs a) {
       if constexpr (C8) x.ksc[kb] = Buf(a.kv.ks + r, x.have[kb] * 4).ldf(ql * 4);
     }
   };
-  auto work = [&](int u, const Unit& now) {
+  // A unit's registers are free once its products are made: the next one's loads are on their way under its exponentials and under
+  // other waves' work (two units in turn, with registers for fewer waves, take as long over long caches, 26 us for 24 over 16
+  // sequences of 5000 with 4 heads of 256)
+  auto fetch = [&](int v, Unit& x) {
+    if (v >= units) return;
+    const int pg[2] = {page[0], page[1]};
+    pages(v + step);
+    load(v, pg, x);
+  };
+  auto work = [&](int u, Unit& now) {
     const int t0 = u * 32, h0 = now.have[0], h1 = now.have[1];
+    const float old = now.old, sk[2] = {C8 ? now.ksc[0] : 0.f, C8 ? now.ksc[1] : 0.f};
     float sum[2] = {0.f, 0.f};
     const bool some = visible(u);
+    f32x4 sc[QB][2];
     if (some) {
-      f32x4 sc[QB][2];
 #pragma unroll
       for (int qb = 0; qb < QB; ++qb)
 #pragma unroll
@@ -151,11 +161,14 @@ __global__ __launch_bounds__(256) void k_mass_few(MassArgs a) {
             for (int qb = 0; qb < QB; ++qb) sc[qb][kb] = mfma16<CB>(qf[qb][i], now.kr[kb][i], sc[qb][kb]);
           }
         }
+    }
+    fetch(u + step, now);
+    if (some) {
       // most units are seen whole by every row: then rows alone decide
       const bool full = h0 + h1 == 32 && all_seen(a, m.q.p0, m.p1, t0, t0 + 31);
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
-        const float f = C8 ? now.ksc[kb] * c : c;
+        const float f = C8 ? sk[kb] * c : c;
         const int j = t0 + kb * 16 + ql;
         const bool held = ql < (kb ? h1 : h0);
 #pragma unroll
@@ -171,16 +184,9 @@ __global__ __launch_bounds__(256) void k_mass_few(MassArgs a) {
       }
     }
     const int j = t0 + l;
-    if (l < 32 && j < m.keys && (copy || j >= m.q.p0 || some)) give(a, m, base, j, now.old, l < 16 ? sum[0] : sum[1]);
+    if (l < 32 && j < m.keys && (copy || j >= m.q.p0 || some)) give(a, m, base, j, old, l < 16 ? sum[0] : sum[1]);
   };
-  // a unit's loads are on their way while the one before it is worked on; two turns in one, so that nothing is copied
-  auto fetch = [&](int v, Unit& x) {
-    if (v >= units) return;
-    const int pg[2] = {page[0], page[1]};
-    pages(v + step);
-    load(v, pg, x);
-  };
-  Unit x0, x1;
+  Unit x0;
   fetch(u, x0);
   if constexpr (C8 && BF) {
     float big = 0.f;
@@ -201,12 +207,7 @@ __global__ __launch_bounds__(256) void k_mass_few(MassArgs a) {
       if (L[qb][e] == -INFINITY) pr[qb][e] = -1;       // rows without a sum see nothing
       L[qb][e] *= LOG2E;
     }
-  for (; u < units; u += 2 * step) {
-    fetch(u + step, x1);
-    work(u, x0);
-    fetch(u + 2 * step, x0);
-    if (u + step < units) work(u + step, x1);
-  }
+  for (; u < units; u += step) work(u, x0);
 }
 
 // ------------------------------------------------------------------------------------------------ many rows
