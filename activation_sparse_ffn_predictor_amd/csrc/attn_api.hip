@@ -156,8 +156,10 @@ MassPlan mass_plan(int S, int Hkv, int G, int d, int max_q, int max_kv, int W) {
   MassPlan p{1, 1, 0};
   if (sffn::mass_few(rows, d)) {
     // Workgroups of 1024 keys, eight units a wave; of fewer where that leaves places free (32 sequences to 6000 tokens on 40 heads,
-    // int8: of 512 keys 105 us, 1024 101, 2048 105)
-    p.tiles = (int)std::min((keys + 127) / 128, std::max((keys + 1023) / 1024, (2048 + seqs - 1) / seqs));
+    // int8: of 512 keys 102 us, 1024 100, 2048 109): up to 4096 workgroups, or 2048 where each has more than 16 rows to load first (16
+    // sequences of 5000, 4 heads of 256: 2048 workgroups 24 us, 4096 19.6; 48 of 4000, 8 heads of 64 and 32 rows: 27 and 31.5)
+    const int64_t places = rows <= 16 ? 4096 : 2048;
+    p.tiles = (int)std::min((keys + 127) / 128, std::max((keys + 1023) / 1024, (places + seqs - 1) / seqs));
     p.tiles = std::max(1, std::min(p.tiles, (1 << 22) / (int)seqs));
     return p;
   }
