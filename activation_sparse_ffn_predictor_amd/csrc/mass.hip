@@ -54,7 +54,7 @@ __device__ __forceinline__ uint4 codes8_bf16(uint2 c) {
 // ------------------------------------------------------------------------------------------------ few rows
 // Up to 16 * QB rows (single tokens, drafts): the queries stay in registers, every wave runs through its own units of 32 keys.
 // S = Q K^T (16x16x32): a lane's column is a key, its registers are rows, so a key's sum needs two exchanges for 16 keys.
-// Bound by K's bytes (32 sequences to 6000 tokens on 40 heads, int8, 467 MB: 99 us, 4.7 TB/s; a large copy reaches 5.55, reading alone
+// Bound by K's bytes (32 sequences to 6000 tokens on 40 heads, int8, 467 MB: 98 us, 4.8 TB/s; a large copy reaches 5.55, reading alone
 // 5.9; page ids ahead of the loads that need them: 130 -> 113). KVM 0: cache of the queries' type, 1: int8, 2: e4m3 (products in fp16, bf16 queries brought into its
 // range by one power of two). DP: head size padded.
 template <bool BF, int KVM, int DP, int QB>

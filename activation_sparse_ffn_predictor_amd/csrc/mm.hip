@@ -121,7 +121,7 @@ __global__ __launch_bounds__(NW * 64) void k_mm_few(MmArgs a) {
 // ------------------------------------------------------------------------------------------------ some tokens
 // BN rows of B x BT tokens a workgroup of WN x WT waves, for calls that B's bytes or a few tiles bound: four blocks of k in LDS,
 // three of them on their way (direct loads) while one is multiplied; k may be spread over workgroups, whose fp32 partial results
-// a second kernel adds up in order. Swizzle as below. 37 x 15360 x 5120, 80 MB: 23.3 us (3.4 TB/s; the operands' way through LDS and
+// a second kernel adds up in order. Swizzle as below. 37 x 15360 x 5120, 80 MB: 22 to 23 us (20.6 of them before the join, 4.1 TB/s; the operands' way through LDS and
 // their widening to fp16 do not wholly hide behind the loads); 10240 rows of K = 8192: 16 tokens 22.5 us, 64 30.
 template <int OT, bool EXACT, int BN, int BT, int WN, int WT>
 __global__ __launch_bounds__(WN * WT * 64) void k_mm_some(MmArgs a, int ks) {
