@@ -140,7 +140,9 @@ __device__ __forceinline__ f32x16 mfma32(const uint4& a, const uint4& b, f32x16 
   if constexpr (BF) return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
   else return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
 }
-// buffer load at voff + soff (a wave-uniform part): voff = OOB still reads zeros
+// buffer load at voff + soff (a wave-uniform part): voff = OOB still reads zeros, and so does what lies past the descriptor's bytes
+// through soff (gfx950 counts it, also where it exceeds them alone: NaN in slots behind a sequence's end change nothing in the
+// attention's tests). Used where the memory behind is the tensor's own either way.
 __device__ __forceinline__ uint4 ld16(const Buf& b, uint32_t voff, uint32_t soff) {
   const v4u32 v = __builtin_amdgcn_raw_buffer_load_b128(b.r, (int)voff, (int)soff, 0);
   return make_uint4(v.x, v.y, v.z, v.w);

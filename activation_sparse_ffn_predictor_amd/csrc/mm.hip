@@ -53,10 +53,10 @@ __device__ __forceinline__ void store4(void* p, long i, f32x4 v) {
   if constexpr (OT == T_F32) *reinterpret_cast<f32x4*>((float*)p + i) = v;
   else *reinterpret_cast<uint2*>((char*)p + 2 * i) = make_uint2(pack2<OT == T_BF16>(v[0], v[1]), pack2<OT == T_BF16>(v[2], v[3]));
 }
-// rows r0 .. r0 + n - 1 of a matrix of codes; what lies past the last row's end reads as zeros
-__device__ __forceinline__ Buf rows_of(const char* p, long ld, long r0, long rows, int n, int K) {
-  const long have = rows - r0 < n ? rows - r0 : n;
-  return Buf(p + r0 * ld, have > 0 ? (uint32_t)((have - 1) * ld + K) : 0u);
+// what lies past a span's end reads as zeros
+__device__ __forceinline__ Buf buf(const Span& s) { return Buf(s.p, s.bytes); }
+__device__ __forceinline__ void load_lds(const Span& s, uint32_t off, uint32_t at, char* to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(buf(s).r, (__attribute__((address_space(3))) void*)to, 16, (int)off, (int)at, 0, 0);
 }
 
 // ------------------------------------------------------------------------------------------------ few tokens
@@ -69,7 +69,7 @@ __global__ __launch_bounds__(NW * 64) void k_mm_few(MmArgs a) {
   constexpr int U = 1;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63, g4 = l >> 4, ql = l & 15;
   const int n0 = blockIdx.x * 16, KB = (a.K + 127) >> 7;
-  const Buf bb = rows_of(a.b, a.ldb, n0, a.N, 16, a.K), ba = rows_of(a.a, a.lda, 0, a.T, 16, a.K), bs(a.sa, (uint32_t)a.T * KB * 4),
+  const Buf bb = buf(rows_of(a.b, a.ldb, n0, a.N, 16, a.K)), ba = buf(rows_of(a.a, a.lda, 0, a.T, 16, a.K)), bs(a.sa, (uint32_t)a.T * KB * 4),
       bw(a.sb + (long)(n0 >> 7) * KB, (uint32_t)KB * 4);
   const uint32_t vb = ql * (uint32_t)a.ldb + g4 * 16, va = ql * (uint32_t)a.lda + g4 * 16, vs = boff(ql < a.T, ql * (uint32_t)KB * 4);
   uint4 x[U][2], y[U][2];
@@ -127,7 +127,7 @@ template <int OT, bool EXACT, int BN, int BT, int WN, int WT>
 __global__ __launch_bounds__(WN * WT * 64) void k_mm_some(MmArgs a, int ks) {
   constexpr int W = WN * WT, MI = BN / WN / 16, NI = BT / WT / 16, FC = 32;   // FC: blocks whose factors LDS holds
   constexpr int LB = BN / 8 / W, LA = BT / 8 / W, L = LB + LA;
-  static_assert(LB * 8 * W == BN && LA * 8 * W == BT && BN <= 128, "whole direct loads, one block of 128 rows");
+  static_assert(LB * 8 * W == BN && LA * 8 * W == BT && BN <= 128 && W % 2 == 0, "whole direct loads, one block of 128 rows");
   constexpr int SW = BN + BT;
   __shared__ __align__(16) char s0[SW * 128], s1[SW * 128], s2[SW * 128], s3[SW * 128];
   __shared__ float fs[BT * (FC + 1)], ws[FC];
@@ -135,21 +135,20 @@ __global__ __launch_bounds__(WN * WT * 64) void k_mm_some(MmArgs a, int ks) {
   const int wn = (w % WN) * (BN / WN), wt = (w / WN) * (BT / WT);
   const int tn = (a.N + BN - 1) / BN, share = blockIdx.x % ks, id = blockIdx.x / ks, n0 = id % tn * BN, t0 = id / tn * BT;
   const int KB = (a.K + 127) >> 7, per = (KB + ks - 1) / ks, k0 = min(KB, share * per), n = min(KB, k0 + per) - k0;   // (its n blocks)
-  const Buf bb = rows_of(a.b, a.ldb, n0, a.N, BN, a.K), ba = rows_of(a.a, a.lda, t0, a.T, BT, a.K);
-  const int rr = w * 8 + (l >> 3), ch = ((l & 7) ^ ((rr >> 1) & 7)) << 4;
+  const Span bb = rows_of(a.b, a.ldb, n0, a.N, BN, a.K), ba = rows_of(a.a, a.lda, t0, a.T, BT, a.K);
+  const int rr = lane_row(w, l), ch = lane_col(rr, l);
   const uint32_t vb = rr * (uint32_t)a.ldb + ch, va = rr * (uint32_t)a.lda + ch;
-  const bool tail = (KB - 1) * 128 + ch < a.K;
+  Span tb[LB], ta[LA];
+#pragma unroll
+  for (int i = 0; i < LB; ++i) tb[i] = turn_of(bb, i, W, a.ldb);
+#pragma unroll
+  for (int i = 0; i < LA; ++i) ta[i] = turn_of(ba, i, W, a.lda);
   auto load = [&](int i0, char* st) {              // (past the end: nothing is read)
-    const int kb = k0 + i0;
-    const bool in = (i0 < n) & ((kb < KB - 1) | tail);
+    const Cols c = cols_of(k0 + i0, KB, a.K, ch, i0 < n);
 #pragma unroll
-    for (int i = 0; i < LB; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(bb.r, (__attribute__((address_space(3))) void*)(st + (i * W + w) * 1024), 16,
-                                               (int)boff(in, vb), (int)(i * W * 8 * (uint32_t)a.ldb + kb * 128), 0, 0);
+    for (int i = 0; i < LB; ++i) load_lds(tb[i], boff(c.in, vb), c.at, st + (i * W + w) * 1024);
 #pragma unroll
-    for (int i = 0; i < LA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ba.r, (__attribute__((address_space(3))) void*)(st + BN * 128 + (i * W + w) * 1024), 16,
-                                               (int)boff(in, va), (int)(i * W * 8 * (uint32_t)a.lda + kb * 128), 0, 0);
+    for (int i = 0; i < LA; ++i) load_lds(ta[i], boff(c.in, va), c.at, st + BN * 128 + (i * W + w) * 1024);
   };
   auto frag = [&](const char* tile, int row) {     // chunks g4 and 4 + g4 of a row
     Codes<EXACT> c;
@@ -267,21 +266,20 @@ __global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a, int ks) {
   const int first = id / (4 * tn) * 4, wide = min(4, tt - first), in = id % (4 * tn);
   const int n0 = in / wide * BN, t0 = (first + in % wide) * BT;
   const int KB = (a.K + 127) >> 7, per = (KB + ks - 1) / ks, k0 = min(KB, share * per), nk = min(KB, k0 + per) - k0;   // (its nk blocks)
-  const Buf bb = rows_of(a.b, a.ldb, n0, a.N, BN, a.K), ba = rows_of(a.a, a.lda, t0, a.T, BT, a.K);
-  // direct loads: a wave's 8 rows at a time, W waves beside each other; a lane's row keeps its swizzle from turn to turn, so one
-  // offset serves all, with the rows and blocks passed as the wave's own. Past the last row, and past K, zeros are read.
-  const int rr = w * 8 + (l >> 3), ch = ((l & 7) ^ ((rr >> 1) & 7)) << 4;
+  const Span bb = rows_of(a.b, a.ldb, n0, a.N, BN, a.K), ba = rows_of(a.a, a.lda, t0, a.T, BT, a.K);
+  // direct loads: one offset of a lane serves all turns and blocks. Past the last row, and past K, zeros are read.
+  const int rr = lane_row(w, l), ch = lane_col(rr, l);
   const uint32_t vb = rr * (uint32_t)a.ldb + ch, va = rr * (uint32_t)a.lda + ch;
-  const bool tail = (KB - 1) * 128 + ch < a.K;     // does the lane's chunk of the last block exist?
   constexpr int LB = BN / 8 / W, LA = BT / 8 / W;  // direct loads of a wave and block
+  Span tb[LB], ta[LA];
+#pragma unroll
+  for (int i = 0; i < LB; ++i) tb[i] = turn_of(bb, i, W, a.ldb);
+#pragma unroll
+  for (int i = 0; i < LA; ++i) ta[i] = turn_of(ba, i, W, a.lda);
   auto load = [&](int i, int kb, char* lb, char* la) {
-    const bool in = (kb < nk) & ((k0 + kb < KB - 1) | tail);
-    if (i < LB)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(bb.r, (__attribute__((address_space(3))) void*)(lb + (i * W + w) * 1024), 16,
-                                               (int)boff(in, vb), (int)(i * W * 8 * (uint32_t)a.ldb + (k0 + kb) * 128), 0, 0);
-    else
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ba.r, (__attribute__((address_space(3))) void*)(la + ((i - LB) * W + w) * 1024), 16,
-                                               (int)boff(in, va), (int)((i - LB) * W * 8 * (uint32_t)a.lda + (k0 + kb) * 128), 0, 0);
+    const Cols c = cols_of(k0 + kb, KB, a.K, ch, kb < nk);
+    if (i < LB) load_lds(tb[i], boff(c.in, vb), c.at, lb + (i * W + w) * 1024);
+    else load_lds(ta[i - LB], boff(c.in, va), c.at, la + ((i - LB) * W + w) * 1024);
   };
   auto arrive = [&] {                              // every wave's direct loads are there
     asm volatile("" ::: "memory");
@@ -292,15 +290,15 @@ __global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a, int ks) {
   // came from L2 as often as the codes': 4096 x 8192 x 8192 in 311 us, so in 282). Of the tile's BT tokens x 8 blocks, BT values are
   // loaded with every block and put in their place with the next; they are complete when the 8 blocks begin, and the ring's third
   // place is the one that nobody reads.
-  const Buf bs(a.sa + (long)t0 * KB, (uint32_t)min(a.T - t0, BT) * KB * 4),
-      bw(a.sb + (long)((n0 + wn) >> 7) * KB, n0 + wn < a.N ? (uint32_t)KB * 4 : 0u);
+  const Span bs{(const char*)(a.sa + (long)t0 * KB), (uint32_t)min(a.T - t0, BT) * KB * 4},
+      bw{(const char*)(a.sb + (long)((n0 + wn) >> 7) * KB), n0 + wn < a.N ? (uint32_t)KB * 4 : 0u};
   constexpr int SL = BT / 8;                       // tokens of a slice
   const int ft = (threadIdx.x % BT) >> 3, fk = threadIdx.x & 7;
   auto fetch = [&](int p) {                        // slice p & 7 of the 8 blocks behind those of block p
-    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bs.r, (int)((ft * KB + fk) * 4), (int)(((p & 7) * SL * KB + (p & ~7) + 8 + k0) * 4), 0));
+    return buf(factors_of(bs, p, SL, KB, k0)).ldf((ft * KB + fk) * 4);
   };
   auto place = [&](int p, float v) { fs[((((p >> 3) + 1) % 3) * BT + (p & 7) * SL + ft) * 8 + fk] = v; };
-  auto weight = [&](int kb) { return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(bw.r, 0, (k0 + kb) * 4, 0)); };
+  auto weight = [&](int kb) { return buf(bw.from((k0 + kb) * 4)).ldf(0); };
   f32x4 acc[MI][NI];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
