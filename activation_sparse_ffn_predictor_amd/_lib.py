@@ -378,7 +378,8 @@ def kv_evict(kv, kv_len, table, mass, pos, keep: int, src, ws, seq_len=None, sin
              mass_out=None, pos_out=None, stream=None):
     """sffn_kv_evict: cuts every sequence with more than `keep` cached tokens down to them: those at positions below `sinks` or
     among the last `recent` (of seq_len tokens; None: kv_len), then those with the largest mass. src [S, K/V heads, keep] int32
-    tells which slot each came from. kv_len_out, mass_out, pos_out None: in place."""
+    tells which slot each came from. kv_len_out, mass_out, pos_out None: in place. seq_len or kv_len_out has to be given: with both
+    left out the cached length would overwrite the sequence's own, which is refused."""
     rc = (_bound or _fast()).kv_evict(kv, kv_len, table, mass, pos, keep, src, ws, seq_len, sinks, recent, kv_len_out, mass_out,
                                       pos_out, _handle_of(stream))
     if rc:

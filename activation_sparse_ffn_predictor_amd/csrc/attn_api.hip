@@ -454,6 +454,8 @@ int sffn_kv_evict(sffn_kv c, const int32_t* kv_len, const int32_t* seq_len, cons
     return fail(SFFN_ERR_ARG, "sinks=%d, recent=%d: need both >= 0, their sum at most keep=%d", sinks, recent, keep);
   if (!al(seq_len, 4) || !al(mass, 4) || !al(pos, 4) || !al(src, 4) || !al(mass_out, 4) || !al(pos_out, 4) || !al(kv_len_out, 4))
     return fail(SFFN_ERR_ALIGN, "kv_evict: misaligned pointer");
+  if (kv_len_out == seq_len)
+    return fail(SFFN_ERR_ARG, "kv_evict: kv_len_out is seq_len, so the sequences would forget how many tokens they count: one of them has to be a tensor of its own");
   const void* all[] = {mass, pos, src, mass_out, pos_out, kv_len, seq_len, kv_len_out, table};
   for (int i = 0; i < 9; ++i)
     for (int j = 0; j < i; ++j)
