@@ -133,8 +133,11 @@ class SparseFFNStack:
             if c.qk_norm:
                 t["w_q"], t["w_k"] = (1 + 0.1 * torch.randn(c.head_dim, generator=g, device=dev) for _ in range(2))
             if c.keep:
-                t["mass"] = torch.zeros((B, c.n_kv_heads, slots), device=dev)
                 t["pos"] = torch.zeros((B, c.n_kv_heads, slots), dtype=torch.int32, device=dev)
+        if c.keep:
+            self.mass = torch.zeros((len(self.layers), B, c.n_kv_heads, slots), device=dev)
+            for t, m in zip(self.layers, self.mass):
+                t["mass"] = m
         self.w_out = torch.ones(D, device=dev)
         self.table = torch.arange(B * cols, dtype=torch.int32, device=dev).view(B, cols)
         self.kv_len = torch.zeros(B, dtype=torch.int32, device=dev)
@@ -235,8 +238,13 @@ class SparseFFNStack:
 
     @contextlib.contextmanager
     def _grown(self, rows: slice, n: int):
-        """The sequences `rows` longer by n tokens for the calls inside; as they were if one of these is refused."""
-        before = self.lens[rows]
+        """The sequences `rows` longer by n tokens for the calls inside; as they were if one of these is refused, with the attention
+        weight of their tokens (not while a graph is captured: see capture; sequences that were cut down to make room stay so)."""
+        # (the copy costs an eager step about 10 us whatever its layers; replays have none)
+        before, mass = self.lens[rows], None
+        if self.attn.keep and not torch.cuda.is_current_stream_capturing():
+            mass = self.mass[:, rows, :, :max(before)]
+            seen = mass.clone()
         self.lens[rows] = [m + n for m in before]
         self.kv_len[rows] += n
         self.seq_len[rows] += n
@@ -246,6 +254,8 @@ class SparseFFNStack:
             self.lens[rows] = before
             self.kv_len[rows] -= n
             self.seq_len[rows] -= n
+            if mass is not None:
+                mass.copy_(seen)
             raise
 
     def _batch(self, B: int):
@@ -344,9 +354,9 @@ class SparseFFNStack:
             self._make_room(range(B), 1)
             seen = [(t["mass"][:B].clone(), t["pos"][:B].clone()) for t in self.layers] if self.attn.keep else []
             lens = (list(self.lens), self.kv_len.clone(), self.seq_len.clone())
-        self.step(B)
-        torch.cuda.synchronize(self.device)
         try:
+            self.step(B)
+            torch.cuda.synchronize(self.device)
             if lens is not None:
                 self.lens = list(lens[0])
             g = torch.cuda.CUDAGraph()
