@@ -169,7 +169,7 @@ class SparseFFNStack:
             self.ws_mass = torch.zeros(max(256, need), dtype=torch.uint8, device=dev)
             self.ws_evict = torch.zeros(_lib.kv_evict_workspace_size(1, c.n_kv_heads, slots, c.keep), dtype=torch.uint8, device=dev)
             self.src = torch.zeros((1, c.n_kv_heads, c.keep), dtype=torch.int32, device=dev)
-            self.cut_len = torch.zeros(1, dtype=torch.int32, device=dev)
+            self.no_len, self.cut_len = (torch.zeros(1, dtype=torch.int32, device=dev) for _ in range(2))
 
     @staticmethod
     def _quantised(x, rows: int):
@@ -223,16 +223,19 @@ class SparseFFNStack:
         _lib.add_rmsnorm(x, self.h[:B], self.w_out, self.attn.eps, self.out[:B], res_out=self.h[:B])
 
     def evict(self, s: int):
-        """Cut sequence s down to the configuration's `keep` cached tokens if it holds more, in every layer."""
+        """Cut sequence s down to the configuration's `keep` cached tokens if it holds more, in every layer, or in none if a layer's
+        call is refused."""
         c = self.attn
         if c is None or not c.keep or not 0 <= s < self.max_batch:
             raise ValueError(f"evict: sequence {s} (the stack needs attention with keep > 0)")
         if self.lens[s] <= c.keep:
             return
         one = slice(s, s + 1)
-        for t in self.layers:
-            _lib.kv_evict(t["kv"], self.kv_len[one], self.table[one], t["mass"][one], t["pos"][one], c.keep, self.src, self.ws_evict,
-                          seq_len=self.seq_len[one], sinks=c.sinks, recent=c.recent, kv_len_out=self.cut_len)
+        # what is moved cannot be put back, so every layer's call goes through the library once with no tokens held, which moves none
+        for held in (self.no_len, self.kv_len[one]):
+            for t in self.layers:
+                _lib.kv_evict(t["kv"], held, self.table[one], t["mass"][one], t["pos"][one], c.keep, self.src, self.ws_evict,
+                              seq_len=self.seq_len[one], sinks=c.sinks, recent=c.recent, kv_len_out=self.cut_len)
         self.kv_len[one] = self.cut_len
         self.lens[s] = c.keep
 

@@ -1,4 +1,4 @@
-"""A stack that keeps the attended tokens: a step, prompt or capture that is refused in a later layer leaves every layer's
+"""A stack that keeps the attended tokens: a step, prompt, capture or eviction that is refused in a later layer leaves every layer's
 weights, positions and cache as they were, so what follows has the bits of a stack that never saw it."""
 import dataclasses
 
@@ -75,3 +75,21 @@ def test_refused_calls(gpu_ready, c, what):
             st.x_in[:2] = y
             st.step(2)
         assert held(a) == held(b) and torch.equal(a.out[:2], b.out[:2])
+
+
+def test_refused_evictions(gpu_ready):
+    dev = gpu_ready
+    st = toy(dev, BASE)
+    g = torch.Generator().manual_seed(4)
+    for _ in range(6):
+        st.prompt(1, torch.randn((8, 512), generator=g).to(dev))
+    before = held(st)
+    assert st.lens[1] == 48
+    for call in (lambda: st.evict(1), lambda: st.prompt(1, torch.randn((4, 512), generator=g).to(dev))):
+        undo = spoil(st, 2, "kv")
+        with pytest.raises(SffnError):
+            call()
+        undo()
+        assert held(st) == before
+    st.evict(1)
+    assert st.lens[1] == 30 and st.kv_len.tolist()[1] == 30 and st.seq_len.tolist()[1] == 48
