@@ -1,5 +1,9 @@
-// Arguments of the block-scaled product's kernels (mm.hip), and where their lanes read.
+// Arguments of the block-scaled product's kernels (mm.hip), where their lanes read, and which of them a call takes.
 #pragma once
+#include <math.h>
+
+#include <algorithm>
+
 #include "attn.h"
 
 namespace sffn {
@@ -52,6 +56,43 @@ __host__ __device__ __forceinline__ Cols cols_of(int kb, int KB, int K, int col,
 // Factors of a tile's tokens (rows of KB): in slice p & 7 (SL tokens) of the 8 blocks behind those of block p, counted from k0 on
 __host__ __device__ __forceinline__ Span factors_of(const Span& s, int p, int SL, int KB, int k0) {
   return s.from((uint32_t)(((p & 7) * SL * KB + (p & ~7) + 8 + k0) * 4));
+}
+
+// Which kernel, and over how many workgroups k is spread: the sum of measured costs decides. Workgroups take a block of k in `one`
+// us when a compute unit has one of them and in `all` when it has as many as fit, at least a round of them; a join starts in 4 us and
+// moves each partial result out and in at 5 TB/s. 10240 rows of K = 8192, us: 64 tokens SOME64 41, in three shares 30; 128 tokens
+// SOME128 40, TILE128 in three shares 31; 256 tokens TILE128 59, in three shares 45; 512 tokens TILE128 82, TILE256 in three shares 63;
+// 1024 tokens TILE128 128, TILE256 109; 2048 tokens 204 and 218; 4096 TILE256 340.
+enum MmKernel { FEW, SOME32, SOME64, SOME128, TILE128, TILE256 };
+struct MmShape {
+  int n, t, fit;                                   // rows and tokens of a workgroup, workgroups a compute unit
+  double one, all;
+};
+constexpr MmShape MM_SHAPES[] = {{16, 16, 4, 0, 0},        {64, 32, 3, 0.42, 0.75},   {64, 64, 2, 0.62, 0.9},
+                            {64, 128, 1, 0.6, 0.6},   {128, 128, 2, 0.92, 1.28}, {256, 256, 1, 1.75, 1.75}};
+struct MmPlan {
+  int how, ks;
+};
+inline MmPlan mm_plan(int T, int N, int K, bool f32) {
+  // few tokens' rows go to registers; past 4 tokens and 16 MB their loads outweigh what LDS costs (10240 x 8192: 16 tokens 31 us, by
+  // LDS 22; 512 x 1024, 8 tokens: 4.9 and 5.6)
+  if (T <= 4 || (T <= 16 && (long)N * K <= 1 << 24)) return {FEW, 1};
+  const int KB = (K + 127) / 128, from = T <= 32 ? SOME32 : T <= 64 ? SOME64 : SOME128,
+            to = T <= 32 ? SOME32 : T <= 64 ? SOME64 : f32 ? TILE128 : TILE256;
+  MmPlan best{from, 1};
+  double least = 0;
+  for (int how = from; how <= to; ++how) {
+    const MmShape& c = MM_SHAPES[how];
+    const double tiles = (double)((N + c.n - 1) / c.n) * ((T + c.t - 1) / c.t);
+    for (const int ks : {1, 2, 3, 4, 6, 8}) {
+      if (ks > 1 && (KB < 4 * ks || tiles * ks > 512)) break;
+      const double wgs = tiles * ks, fit = 256.0 * c.fit, turns = c.fit == 1 ? ceil(wgs / fit) : std::max({1.0, wgs / fit, ceil(wgs / fit) - 0.4});
+      double us = turns * ((KB + ks - 1) / ks) * (wgs <= 256 ? c.one : c.all);
+      if (ks > 1) us += 4.0 + (double)ks * T * N * 8 / 5e6;
+      if (least == 0 || us < least) best = {how, ks}, least = us;
+    }
+  }
+  return best;
 }
 
 }  // namespace sffn

@@ -9,10 +9,6 @@
 // 1.4e-4 of a sum of independent terms, fp16's own rounding 2.1e-4, bf16's 1.7e-3.
 #include "mm.h"
 
-#include <math.h>
-
-#include <algorithm>
-
 using namespace sffn;
 
 namespace {
@@ -388,46 +384,9 @@ __global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a, int ks) {
   }
 }
 
-// Which kernel, and over how many workgroups k is spread: the sum of measured costs decides. Workgroups take a block of k in `one`
-// us when a compute unit has one of them and in `all` when it has as many as fit, at least a round of them; a join starts in 4 us and
-// moves each partial result out and in at 5 TB/s. 10240 rows of K = 8192, us: 64 tokens SOME64 41, in three shares 30; 128 tokens
-// SOME128 40, TILE128 in three shares 31; 256 tokens TILE128 59, in three shares 45; 512 tokens TILE128 82, TILE256 in three shares 63;
-// 1024 tokens TILE128 128, TILE256 109; 2048 tokens 204 and 218; 4096 TILE256 340.
-enum { FEW, SOME32, SOME64, SOME128, TILE128, TILE256 };
-struct Shape {
-  int n, t, fit;                                   // rows and tokens of a workgroup, workgroups a compute unit
-  double one, all;
-};
-constexpr Shape SHAPES[] = {{16, 16, 4, 0, 0},        {64, 32, 3, 0.42, 0.75},   {64, 64, 2, 0.62, 0.9},
-                            {64, 128, 1, 0.6, 0.6},   {128, 128, 2, 0.92, 1.28}, {256, 256, 1, 1.75, 1.75}};
-struct Plan {
-  int how, ks;
-};
-Plan plan(int T, int N, int K, bool f32) {
-  // few tokens' rows go to registers; past 4 tokens and 16 MB their loads outweigh what LDS costs (10240 x 8192: 16 tokens 31 us, by
-  // LDS 22; 512 x 1024, 8 tokens: 4.9 and 5.6)
-  if (T <= 4 || (T <= 16 && (long)N * K <= 1 << 24)) return {FEW, 1};
-  const int KB = (K + 127) / 128, from = T <= 32 ? SOME32 : T <= 64 ? SOME64 : SOME128,
-            to = T <= 32 ? SOME32 : T <= 64 ? SOME64 : f32 ? TILE128 : TILE256;
-  Plan best{from, 1};
-  double least = 0;
-  for (int how = from; how <= to; ++how) {
-    const Shape& c = SHAPES[how];
-    const double tiles = (double)((N + c.n - 1) / c.n) * ((T + c.t - 1) / c.t);
-    for (const int ks : {1, 2, 3, 4, 6, 8}) {
-      if (ks > 1 && (KB < 4 * ks || tiles * ks > 512)) break;
-      const double wgs = tiles * ks, fit = 256.0 * c.fit, turns = c.fit == 1 ? ceil(wgs / fit) : std::max({1.0, wgs / fit, ceil(wgs / fit) - 0.4});
-      double us = turns * ((KB + ks - 1) / ks) * (wgs <= 256 ? c.one : c.all);
-      if (ks > 1) us += 4.0 + (double)ks * T * N * 8 / 5e6;
-      if (least == 0 || us < least) best = {how, ks}, least = us;
-    }
-  }
-  return best;
-}
-
 template <int OT>
 hipError_t go(const MmArgs& a, hipStream_t st) {
-  const Plan p = plan(a.T, a.N, a.K, OT == T_F32);
+  const MmPlan p = mm_plan(a.T, a.N, a.K, OT == T_F32);
   auto tiles = [&](int n, int t) { return (unsigned)((long)((a.N + n - 1) / n) * ((a.T + t - 1) / t)); };
   auto whole = [&](unsigned v) { return dim3((v + 7) / 8 * 8); };
   if (p.how == FEW) {
@@ -451,7 +410,7 @@ hipError_t go(const MmArgs& a, hipStream_t st) {
 
 size_t sffn_mm_workspace(int T, int N, int K) {
   // (whichever type the results are of)
-  const Plan p = plan(T, N, K, false), q = plan(T, N, K, true);
+  const MmPlan p = mm_plan(T, N, K, false), q = mm_plan(T, N, K, true);
   const int ks = p.ks > q.ks ? p.ks : q.ks;
   return ks > 1 ? (size_t)ks * T * N * sizeof(float) : 0;
 }
