@@ -45,17 +45,19 @@ __host__ __device__ __forceinline__ Span turn_of(const Span& s, int i, int W, lo
   const uint32_t off = (uint32_t)(i * W * 8) * (uint32_t)ld;
   return off < s.bytes ? s.from(off) : s;
 }
-// Block kb of them: the wave's offset, and whether the lane's column exists (`some`: is there such a block?)
+// Block kb of them: the wave's offset (the last block's behind it), and whether the lane's column exists (`some`: is there such a block?)
 struct Cols {
   uint32_t at;
   bool in;
 };
 __host__ __device__ __forceinline__ Cols cols_of(int kb, int KB, int K, int col, bool some) {
-  return {some ? (uint32_t)kb * 128u : 0u, (bool)(some & ((kb < KB - 1) | ((KB - 1) * 128 + col < K)))};
+  return {(uint32_t)(kb < KB ? kb : KB - 1) * 128u, (bool)(some & ((kb < KB - 1) | ((KB - 1) * 128 + col < K)))};
 }
-// Factors of a tile's tokens (rows of KB): in slice p & 7 (SL tokens) of the 8 blocks behind those of block p, counted from k0 on
-__host__ __device__ __forceinline__ Span factors_of(const Span& s, int p, int SL, int KB, int k0) {
-  return s.from((uint32_t)(((p & 7) * SL * KB + (p & ~7) + 8 + k0) * 4));
+// Factors of a tile's tokens (rows of KB): in slice p & 7 (SL tokens) of the 8 blocks behind those of block p, counted from k0 on, that
+// of the slice's token ft and block fk. All of it in the lane's offset: descriptors of what a wave's part leaves would put a chain of
+// scalar instructions before a block's first products (4096 x 10240 x 8192: 342 us for 339, 1024 tokens 114 for 111).
+__host__ __device__ __forceinline__ uint32_t factor_at(int p, int SL, int KB, int k0, int ft, int fk) {
+  return (uint32_t)(ft * KB + fk) * 4u + (uint32_t)(((p & 7) * SL * KB + (p & ~7) + 8 + k0) * 4);
 }
 
 // Which kernel, and over how many workgroups k is spread: the sum of measured costs decides. Workgroups take a block of k in `one`

@@ -286,15 +286,15 @@ __global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a, int ks) {
   // came from L2 as often as the codes': 4096 x 8192 x 8192 in 311 us, so in 282). Of the tile's BT tokens x 8 blocks, BT values are
   // loaded with every block and put in their place with the next; they are complete when the 8 blocks begin, and the ring's third
   // place is the one that nobody reads.
-  const Span bs{(const char*)(a.sa + (long)t0 * KB), (uint32_t)min(a.T - t0, BT) * KB * 4},
-      bw{(const char*)(a.sb + (long)((n0 + wn) >> 7) * KB), n0 + wn < a.N ? (uint32_t)KB * 4 : 0u};
+  const Buf bs(a.sa + (long)t0 * KB, (uint32_t)min(a.T - t0, BT) * KB * 4),
+      bw(a.sb + (long)((n0 + wn) >> 7) * KB, n0 + wn < a.N ? (uint32_t)KB * 4 : 0u);
   constexpr int SL = BT / 8;                       // tokens of a slice
   const int ft = (threadIdx.x % BT) >> 3, fk = threadIdx.x & 7;
   auto fetch = [&](int p) {                        // slice p & 7 of the 8 blocks behind those of block p
-    return buf(factors_of(bs, p, SL, KB, k0)).ldf((ft * KB + fk) * 4);
+    return bs.ldf(factor_at(p, SL, KB, k0, ft, fk));
   };
   auto place = [&](int p, float v) { fs[((((p >> 3) + 1) % 3) * BT + (p & 7) * SL + ft) * 8 + fk] = v; };
-  auto weight = [&](int kb) { return buf(bw.from((k0 + kb) * 4)).ldf(0); };
+  auto weight = [&](int kb) { return bw.ldf((k0 + kb) * 4); };
   f32x4 acc[MI][NI];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
