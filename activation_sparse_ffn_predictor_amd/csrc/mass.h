@@ -23,6 +23,16 @@ struct MassArgs {
 
 // the few-row kernel keeps the queries in registers
 __host__ __device__ constexpr bool mass_few(long rows, int d) { return rows <= (d <= 128 ? 64 : 32); }
+// New tokens first .. end - 1 of a sequence's n (at positions p0, p0 + 1, ...): outside them no token sees any of the keys k0 .. k1.
+// Always tokens that there are, however far p0 lies from them, so that their rows' numbers keep to 32 bits.
+struct Tokens {
+  int first, end;
+};
+__host__ __device__ __forceinline__ Tokens tokens_of_keys(int p0, int n, int k0, int k1, int window, int sinks) {
+  const int a = k0 - p0;                           // (k0 < 2^30, p0 >= -2^25)
+  const long b = (long)k1 + window - p0;
+  return {a < 0 ? 0 : a < n ? a : n, window > 0 && k0 >= sinks ? (int)(b < 0 ? 0 : b < n ? b : n) : n};
+}
 // keys of a workgroup of the tile kernel
 __host__ __device__ constexpr int mass_tile(int d) { return d <= 128 ? 256 : 128; }
 

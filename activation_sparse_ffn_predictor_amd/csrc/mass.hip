@@ -290,9 +290,8 @@ __global__ __launch_bounds__(256, 2) void k_mass_many(MassArgs a) {
 
     // rows that see some key of the workgroup's, and this share of them
     const int k0 = kt * WG, k1 = min(k0 + WG, m.keys) - 1;
-    const int i0 = max(0, k0 - m.q.p0);
-    const int i1 = a.window > 0 && k0 >= a.sinks ? (int)min((long)m.n, max(0l, (long)k1 + a.window - m.q.p0)) : m.n;
-    const int r0 = i0 * G, r1 = i1 * G;
+    const Tokens tk = tokens_of_keys(m.q.p0, m.n, k0, k1, a.window, a.sinks);
+    const int r0 = tk.first * G, r1 = tk.end * G;
     int n_t = r1 > r0 ? (r1 - r0 + MROWS - 1) / MROWS : 0, t_0 = 0;
     if (split) {
       const int per = (n_t + a.rs - 1) / a.rs;
