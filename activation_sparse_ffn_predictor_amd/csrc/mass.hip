@@ -11,19 +11,19 @@ namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
 
-// The sequence of a workgroup: its clamped numbers, the first new token's position in the sequence, the keys that have a place.
+// The sequence of a workgroup: its clamped numbers, how far its tokens' positions are ahead of their slots, the keys that have a place.
 struct MassSeq {
   Seq q;
-  int n, rows, p1, at, keys;
+  int n, rows, p1, ahead, keys;
 };
 __device__ __forceinline__ MassSeq mass_seq(const MassArgs& a, int s) {
   MassSeq m;
   m.q = load_seq(a.sq, s, a.kv.psh);
+  m.ahead = token_pos(a.plen[s], max(a.sq.cu[s + 1], m.q.q0), m.q.q0) - m.q.p0;
   m.q.p0 = max(m.q.p0, -(1 << 25));                  // (below it no token of a call can see anything)
   m.n = min(m.q.n, a.max_q);
   m.rows = m.n * a.G;
   m.p1 = m.q.p0 + m.n - 1;
-  m.at = token_pos(a.plen[s], max(a.sq.cu[s + 1], m.q.q0), m.q.q0);
   m.keys = min(m.q.len, a.W);
   return m;
 }
@@ -31,7 +31,7 @@ __device__ __forceinline__ MassSeq mass_seq(const MassArgs& a, int s) {
 __device__ __forceinline__ void give(const MassArgs& a, const MassSeq& m, long base, int j, float old, float sum) {
   const bool fresh = j >= m.q.p0;
   a.out[base + j] = (fresh ? 0.f : old) + sum;
-  if (fresh) a.pos[base + j] = m.at + (j - m.q.p0);
+  if (fresh) a.pos[base + j] = j + m.ahead;
 }
 // does any (every) row at positions pa .. pb see any (every one) of the keys k0 .. k1?
 __device__ __forceinline__ bool some_seen(const MassArgs& a, int pa, int pb, int k0, int k1) {

@@ -29,3 +29,4 @@ def test_rows_past_the_call(gpu_ready, Hq, Hkv, d, kvt, end):
         _lib.attn_mass(q, kv, cu, kl, tab, max_q, n, lse, m, pos, ws, seq_len=kl + 1000)
         torch.cuda.synchronize()
         assert bool((m[..., :n] == 0).all()) and torch.equal(m[..., n:], old[..., n:])
+        assert torch.equal(pos[0, 0, :n].cpu(), torch.arange(1000, 1000 + n, dtype=torch.int32)) and bool((pos[..., n:] == -5).all())
