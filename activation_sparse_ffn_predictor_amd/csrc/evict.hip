@@ -7,9 +7,9 @@
 // Selection: a token's place in the order is a 32-bit key; the key of the last one that stays is found digit by digit (11, 11 and
 // 10 bits) with counts in LDS. Up to 8192 slots one workgroup does all of it with the keys in registers; more slots are spread
 // over workgroups, a kernel a digit, since one workgroup's passes are bound by its instructions (6 x 8 heads of 40001 slots in
-// 48 workgroups: 69 us; by kernels of a digit 9.6 + 6.4 + 6.4, what moves 11.7). Each of them is a chain of dependent loads and
-// barriers rather than bytes. The moves are bound by memory: the moved rows in and out (115 MB with rows of 128 bytes: 20 to 24
-// us). 4 x 8 heads of 1100 slots: 9.3 + 3 us.
+// 48 workgroups: 69 us; by kernels of a digit 10.3 + 6.2 + 6.2, what moves 11.4). Each of them is a chain of dependent loads and
+// barriers rather than bytes. The moves are bound by memory: the moved rows in and out (115 MB with rows of 128 bytes: 20 to 27
+// us). 4 x 8 heads of 1100 slots: 9.1 to 10.7 and 2.1 to 4.1 us.
 #include "evict.h"
 
 using namespace sffn;

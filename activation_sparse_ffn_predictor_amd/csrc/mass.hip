@@ -217,7 +217,9 @@ __global__ __launch_bounds__(256) void k_mass_few(MassArgs a) {
 // Bound by exponentials and matrix products together: for 64 scores the vector unit needs 16 cycles (a multiply-add, an exponential, an
 // addition), and so does the matrix core for products of 128 elements; what each leaves idle the other cannot wholly use (a step of
 // one matrix instruction, two exponentials and four others takes 24 ns where the instruction alone takes 18.6). 2048 tokens over 6144,
-// 64 heads on 8, 172 GFLOP: 205 to 250 us on different cards; with KT = 1, before they overlapped, 313 for 298.
+// 64 heads on 8, 172 GFLOP: 205 to 252 us on different cards; with KT = 1, before they overlapped, 313 for 298. No vector registers spill;
+// 71 to 115 scalar ones do: written to lanes of vector registers at the start, read back where K is loaded and the sums are given, not
+// in the loops of products (k_mass_few: 28 to 32 with four blocks of rows, none with fewer).
 constexpr int MROWS = 64;
 template <bool BF, int KVM, int DP, int KT>
 __global__ __launch_bounds__(256, 2) void k_mass_many(MassArgs a) {

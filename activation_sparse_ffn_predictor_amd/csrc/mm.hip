@@ -3,10 +3,11 @@
 // Rows of B are the matrix instructions' rows, tokens their columns: a lane's results belong to one token, so its factor is one
 // register, and sb is the same for the whole tile. Blocks are scaled and added in fp32.
 //
-// A block's own sum: the 8-bit instruction (16x16x128, a block at once) brings each 8 products to the largest one's exponent and
-// drops what lies 2^-13 under it; the fp16 instruction on widened codes (exact) adds in fp32, at half the rate. Few tokens wait
-// for memory, so they take the fp16 one, as do fp32 results; 16-bit results of many tokens take the 8-bit one: dropped bits are
-// 1.4e-4 of a sum of independent terms, fp16's own rounding 2.1e-4, bf16's 1.7e-3.
+// A block's own sum: the 8-bit instruction (16x16x128, a block at once) brings each 8 products to the largest one's exponent (the
+// sum of its factors') and drops, towards zero, what lies 2^-13 under it; the fp16 instruction on widened codes (exact) adds in fp32,
+// at half the rate (599 us for 340 at 4096 x 10240 x 8192). Few tokens wait for memory, so they take the fp16 one, as do fp32 results;
+// 16-bit results of many tokens take the 8-bit one, fewer than 32 bits by choice: measured at K = 1024 and 8192, the dropped bits are
+// 1.8e-5 of the results (root mean squares, their mean 1e-6 or less), fp16's own rounding 2.1e-4, bf16's 1.7e-3.
 #include "mm.h"
 
 using namespace sffn;
@@ -71,7 +72,7 @@ __global__ __launch_bounds__(NW * 64) void k_mm_few(MmArgs a) {
   uint4 x[U][2], y[U][2];
   float f[U], s[U];
   // workgroups begin at different blocks: rows are often a power of two apart, and those that read the same columns of theirs wait
-  // for the same memory channels (1 x 10240 x 8192: 25 us, so 22)
+  // for the same memory channels (1 x 10240 x 8192 with four blocks ahead: 25 us, so 22; with one ahead 19.5 either way)
   const int turn = blockIdx.x * 5 % KB;
   auto load = [&](int u, int i) {                  // (past the end nothing is loaded)
     int kb = i + turn;
@@ -243,9 +244,10 @@ __global__ __launch_bounds__(256) void k_mm_join(MmArgs a, int ks) {
 // while this one is multiplied. A row's 16-byte chunk c lies in slot c ^ ((row >> 1) & 7): the 16 rows that a fragment's
 // read touches at one chunk spread over all banks. Workgroups of one XCD take neighbouring tiles, 4 along the tokens, so that
 // what they load at one time is shared in its L2.
-// 4096 x 10240 x 8192, 687 GFLOP, fp16 results: 337 to 346 us (2.0 PFLOP/s; a library product of that shape with one scale for each
-// matrix takes 376). The matrix cores bound it together with the scaling (a multiply-add a result and block) and with the power they
-// draw: 4096 x 8192 x 8192 takes 282 us, without its loads 211, with operands of zeros 218.
+// 4096 x 10240 x 8192, 687 GFLOP, fp16 results: 338 to 352 us on different cards, 362 to 375 under the profiler (1.8 to 2.0 PFLOP/s; a library product of that shape
+// with one scale for each matrix takes 372 to 376). The matrix cores bound it together with the scaling (a multiply-add a result and
+// block) and with the power they draw: 4096 x 8192 x 8192 took 282 us on a card where it took 211 without its loads and 218 with
+// operands of zeros; 243 on another.
 template <int OT, int BN, int BT, int WN, int WT>
 __global__ __launch_bounds__(WN * WT * 64, 2) void k_mm_tile(MmArgs a, int ks) {
   constexpr int W = WN * WT, MI = BN / WN / 16, NI = BT / WT / 16;        // waves; 16-blocks of a wave

@@ -337,7 +337,8 @@ int sffn_quant128(int x_type, const void* x, int64_t x_stride, int T, int D, int
  * a [T, K] codes with a_scale [T, ceil(K / 128)], b [N, K] codes with b_scale [ceil(N / 128), ceil(K / 128)] (scales contiguous),
  * out [T, N] of F32, F16 or BF16, rounded once. The sums over a block are fp32 (codes widened exactly to fp16 products) up to 64
  * tokens and for fp32 results; 16-bit results of more tokens take the 8-bit matrix instruction, which drops of each 8 products what
- * lies 2^-13 under the largest one's leading bit. Blocks are scaled and added in fp32, so a block's sum times its scales has to
+ * lies 2^-13 under the largest one's leading bit (of independent terms about a tenth of fp16's rounding of the result; more where
+ * large products cancel: fp32 results keep it whatever the number of tokens). Blocks are scaled and added in fp32, so the product of a block's two scales, and its sum times that, have to
  * stay in fp32's range. e4m3's NaN codes and NaN scales make NaN of the results
  * that they enter. K % 16 == 0, 16 <= K <= 65536; N % 8 == 0, 8 <= N <= 2^22; 0 <= T <= 2^24; strides of a and b multiples of
  * 16, at least K, at most 2^22; of out a multiple of 8, at least N. out overlaps no input. The workspace needs
@@ -385,7 +386,7 @@ int sffn_attn_mass(sffn_kv cache, sffn_seqs seqs, const int32_t* seq_len, int ty
  * src [S, n_kv_heads, keep] int32: the slot that each of the first `keep` slots' tokens stood in (its own where nothing moved).
  * Moved are K, V, their scales, mass and pos: mass_out and pos_out [S, n_kv_heads, W] get the first min(kv_len, keep) slots (they
  * may be mass and pos themselves), kv_len_out[s] = keep where tokens were evicted, else kv_len[s] (it may be kv_len, but not
- * where seq_len is kv_len too: the sequence would forget how long it is). Pages wholly
+ * seq_len, nor kv_len where seq_len is kv_len too: the sequence would forget how long it is). Pages wholly
  * behind the new length are free. Slots are no longer in the order of positions afterwards: attention sees every slot below a
  * new token's whatever its position, but a sliding window would count slots. The pages of the sequences must be their own (not
  * shared between rows of the table). A move into a page outside the cache loses the token. sinks, recent >= 0, sinks + recent <= keep;
